@@ -183,6 +183,29 @@ fa_status fa_bwd_kv(const void* Q, const void* K, const void* V, const void* O, 
                     int causal, int dtype, void* stream);
 
 /*
+ * Sliding-window attention with sinks, forward and backward.  The masks of
+ * fa_fwd_kv's causal rule (past_len = Lk - Lq, Lk >= Lq) narrowed to a window:
+ * the query at position a = i + past_len sees key j iff
+ *   j <= a  and  (j > a - window  or  j < sinks),
+ * that is itself, the window - 1 keys before it, and the first `sinks` keys of
+ * the sequence.  window >= 1 and sinks >= 0 (FA_ERR_INVALID_ARG otherwise); a
+ * window of Lk or more is plain causal attention.  Every query sees at least
+ * itself, so no row is empty.  Work and reads grow with
+ * Lq * (window + sinks), not with Lq * Lk.  K and V must be finite in every
+ * position, as for fa_fwd: a hidden key's V is multiplied by a zero weight.
+ * Everything else (layouts, dtypes, limits, the fp32 dQ accumulator, Delta
+ * from fa_bwd_preprocess) is as for fa_fwd_kv and fa_bwd_kv; dK and dV of keys
+ * that no query sees are zero.
+ */
+fa_status fa_window_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE, int B,
+                        int Lq, int Lk, int H, int Hkv, int D, int window, int sinks, int dtype,
+                        void* stream);
+fa_status fa_window_bwd(const void* Q, const void* K, const void* V, const void* dO,
+                        const float* LSE, const float* Delta, void* dQ, void* dK, void* dV,
+                        float* dq_accum, int zero_accum, int B, int Lq, int Lk, int H, int Hkv,
+                        int D, int window, int sinks, int dtype, void* stream);
+
+/*
  * The two stages fa_bwd runs, for callers that schedule or time them apart:
  *   fa_bwd_main        dK, dV (written in full) and the dQ accumulator (added
  *                      into; it must hold zeros on entry unless zero_accum);

@@ -25,9 +25,13 @@ from .api import (  # noqa: F401
     decode_workspace_size,
     fwd,
     fwd_fp8,
+    window_attention_backward,
+    window_bwd,
+    window_fwd,
     workspace_size,
 )
 
 __all__ = ["fwd", "bwd_preprocess", "bwd", "attention_backward", "bwd_main", "bwd_postprocess", "workspace_size",
            "alloc_workspace", "check_device_error", "HostRunner", "HostPipeline", "decode", "decode_workspace_size",
-           "decode_slices", "decode_merge", "alloc_decode_workspace", "DecodeHostRunner", "fwd_fp8", "Fp8HostRunner"]
+           "decode_slices", "decode_merge", "alloc_decode_workspace", "DecodeHostRunner", "fwd_fp8", "Fp8HostRunner",
+           "window_fwd", "window_bwd", "window_attention_backward"]

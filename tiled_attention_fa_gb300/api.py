@@ -71,6 +71,30 @@ def fwd(q, k, v, causal: bool = False, out=None, lse=None, stream=None):
     return out, lse
 
 
+def window_fwd(q, k, v, window: int, sinks: int = 0, out=None, lse=None, stream=None):
+    """O, LSE = causal attention in which each query sees the last ``window``
+    keys up to its own position and the first ``sinks`` keys.
+    q [B, Lq, H, D]; k, v [B, Lk, Hkv, D] with Lq <= Lk (the queries are the
+    last Lq positions): query i, at position a = i + Lk - Lq, sees key j iff
+    j <= a and (j > a - window or j < sinks)."""
+    B, L, H, D = q.shape
+    Lk, Hkv = k.shape[1], k.shape[2]
+    _need(q, "q")
+    _need(k, "k", (B, Lk, Hkv, D), q.dtype)
+    _need(v, "v", (B, Lk, Hkv, D), q.dtype)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty(B, H, L, device=q.device, dtype=torch.float32)
+    _need(out, "out", q.shape, q.dtype)
+    _need(lse, "lse", (B, H, L), torch.float32)
+    st = _lib.load().fa_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                   lse.data_ptr(), B, L, Lk, H, Hkv, D, window, sinks,
+                                   _dtype_code(q), _stream(stream))
+    _lib.check("fa_window_fwd", st)
+    return out, lse
+
+
 def decode_workspace_size(B: int, Lq: int, Lk: int, H: int, Hkv: int, D: int) -> int:
     """Bytes of the partial-result workspace ``decode`` needs on the current device."""
     return int(_lib.load().fa_decode_workspace_size(B, Lq, Lk, H, Hkv, D))
@@ -245,6 +269,49 @@ def bwd(q, k, v, o, do, lse, delta, causal: bool = False, dq=None, dk=None, dv=N
                            _stream(stream))
         _lib.check("fa_bwd_kv", st)
     return dq, dk, dv
+
+
+def window_bwd(q, k, v, do, lse, delta, window: int, sinks: int = 0, dq=None, dk=None, dv=None,
+               dq_accum=None, accum_zeroed: bool = False, stream=None):
+    """dQ, dK, dV of ``window_fwd``; ``delta`` and ``dq_accum`` as for ``bwd``."""
+    B, L, H, D = q.shape
+    Lk, Hkv = k.shape[1], k.shape[2]
+    _need(q, "q")
+    for name, t, shp in (("k", k, (B, Lk, Hkv, D)), ("v", v, (B, Lk, Hkv, D)), ("do", do, q.shape)):
+        _need(t, name, shp, q.dtype)
+    _need(lse, "lse", (B, H, L), torch.float32)
+    _need(delta, "delta", (B, H, L), torch.float32)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    _need(dq, "dq", q.shape, q.dtype)
+    _need(dk, "dk", k.shape, q.dtype)
+    _need(dv, "dv", v.shape, q.dtype)
+    if dq_accum is None:
+        dq_accum = alloc_workspace(B, L, H, D, q.device)
+        accum_zeroed = False
+    _need(dq_accum, "dq_accum", dtype=torch.float32)
+    if dq_accum.numel() * 4 < workspace_size(B, L, H, D):
+        raise ValueError("dq_accum is smaller than workspace_size()")
+    st = _lib.load().fa_window_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), do.data_ptr(),
+                                   lse.data_ptr(), delta.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                                   dv.data_ptr(), dq_accum.data_ptr(), 0 if accum_zeroed else 1, B,
+                                   L, Lk, H, Hkv, D, window, sinks, _dtype_code(q),
+                                   _stream(stream))
+    _lib.check("fa_window_bwd", st)
+    return dq, dk, dv
+
+
+def window_attention_backward(q, k, v, o, lse, do, window: int, sinks: int = 0, dq_accum=None,
+                              stream=None):
+    """``attention_backward`` for ``window_fwd``: preprocess + backward in one call."""
+    B, L, H, D = q.shape
+    if dq_accum is None:
+        dq_accum = alloc_workspace(B, L, H, D, q.device)
+    delta = bwd_preprocess(o, do, dq_accum=dq_accum, stream=stream)
+    dq, dk, dv = window_bwd(q, k, v, do, lse, delta, window, sinks, dq_accum=dq_accum,
+                            accum_zeroed=True, stream=stream)
+    return dq, dk, dv, delta
 
 
 def bwd_main(q, k, v, do, lse, delta, dq_accum, causal: bool = False, dk=None, dv=None,

@@ -117,6 +117,32 @@ fa_status fa_bwd_kv(const void* Q, const void* K, const void* V, const void* O, 
                      D, causal, dtype, static_cast<cudaStream_t>(stream));
 }
 
+fa_status fa_window_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE, int B,
+                        int Lq, int Lk, int H, int Hkv, int D, int window, int sinks, int dtype,
+                        void* stream) {
+  fa_status st = check_shape(B, Lq, Lk, H, Hkv, D, dtype);
+  if (st != FA_OK) return st;
+  if (Lk < Lq || window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
+  if (!ptr_ok(Q) || !ptr_ok(K) || !ptr_ok(V) || !ptr_ok(O) || !ptr_ok(LSE))
+    return FA_ERR_INVALID_ARG;
+  return fa::run_window_fwd(Q, K, V, O, LSE, B, Lq, Lk, H, Hkv, D, window, sinks, dtype,
+                            static_cast<cudaStream_t>(stream));
+}
+
+fa_status fa_window_bwd(const void* Q, const void* K, const void* V, const void* dO,
+                        const float* LSE, const float* Delta, void* dQ, void* dK, void* dV,
+                        float* dq_accum, int zero_accum, int B, int Lq, int Lk, int H, int Hkv,
+                        int D, int window, int sinks, int dtype, void* stream) {
+  fa_status st = check_shape(B, Lq, Lk, H, Hkv, D, dtype);
+  if (st != FA_OK) return st;
+  if (Lk < Lq || window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
+  if (!ptr_ok(Q) || !ptr_ok(K) || !ptr_ok(V) || !ptr_ok(dO) || !ptr_ok(LSE) || !ptr_ok(Delta) ||
+      !ptr_ok(dQ) || !ptr_ok(dK) || !ptr_ok(dV) || !ptr_ok(dq_accum))
+    return FA_ERR_INVALID_ARG;
+  return fa::run_window_bwd(Q, K, V, dO, LSE, Delta, dQ, dK, dV, dq_accum, zero_accum, B, Lq, Lk, H,
+                            Hkv, D, window, sinks, dtype, static_cast<cudaStream_t>(stream));
+}
+
 fa_status fa_bwd_main(const void* Q, const void* K, const void* V, const void* dO,
                       const float* LSE, const float* Delta, void* dK, void* dV, float* dq_accum,
                       int zero_accum, int B, int L, int H, int Hkv, int D, int causal, int dtype,

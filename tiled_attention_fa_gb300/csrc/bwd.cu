@@ -51,11 +51,12 @@ static double l2_bytes() {
   return n;
 }
 
-template <int D, bool BF16>
+// window > 0 (WIN, causal calls only): the backward of run_window_fwd.
+template <int D, bool BF16, bool WIN = false>
 static fa_status launch_bwd(const void* Q, const void* K, const void* V, const void* dO,
                             const float* LSE, const float* Delta, void* dK, void* dV,
                             float* dq_accum, int zero_accum, int B, int Lq, int Lk, int H,
-                            int Hkv, int causal, cudaStream_t s) {
+                            int Hkv, int causal, cudaStream_t s, int window = 0, int sinks = 0) {
   using Ly = BwdLayout<D>;
   const int Lpad = padded_len(Lq);
   if (zero_accum &&
@@ -97,11 +98,29 @@ static fa_status launch_bwd(const void* Q, const void* K, const void* V, const v
     // with it, hence the limits.
     const int sm = sm_count();
     const double qdo_bytes = 4.0 * B * H * static_cast<double>(Lq) * D;  // Q and dO, 16-bit
-    if (p.causal && p.n_items >= sm && p.n_units <= 4 * sm && qdo_bytes <= 0.6 * l2_bytes()) {
+    if (!WIN && p.causal && p.n_items >= sm && p.n_units <= 4 * sm && qdo_bytes <= 0.6 * l2_bytes()) {
       p.snake = 1;
       p.ipu = 1;
       p.n_units = (p.n_items + sm - 1) / sm * sm;
     }
+  }
+  p.window = window < Lk ? window : Lk;  // as good as every key when larger
+  p.sinks = sinks < Lk ? sinks : Lk;
+  p.n_long = p.cost_long = p.cost_win = 0;
+  if (WIN) {
+    p.ipu = 1;
+    p.n_long = B * Hkv * ((p.sinks + 127) / 128);
+    const int grid = p.n_items < sm_count() ? p.n_items : sm_count();
+    // Q tiles per K/V tile and query head; one tile per CTA when they are few.
+    const bool few = p.n_items <= grid;
+    p.cost_long = few ? 1 : p.n_q;
+    p.cost_win = few ? 1 : (p.n_q < (p.window + 254) / 128 ? p.n_q : (p.window + 254) / 128);
+    int most = 0;
+    for (int c = 0; c < grid; ++c) {
+      const int n = bwd_win_start(p, grid, c + 1) - bwd_win_start(p, grid, c);
+      most = n > most ? n : most;
+    }
+    p.n_units = most * grid;
   }
   p.scale = 1.f / sqrtf(static_cast<float>(D));
   p.sl2 = 1.4426950408889634f * p.scale;
@@ -109,7 +128,7 @@ static fa_status launch_bwd(const void* Q, const void* K, const void* V, const v
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   if (optin < static_cast<int>(Ly::SMEM_ALLOC)) return FA_ERR_UNSUPPORTED;
-  auto kern = fa_bwd_kernel<D, BF16>;
+  auto kern = fa_bwd_kernel<D, BF16, WIN>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::SMEM_ALLOC) !=
       cudaSuccess)
     return FA_ERR_CUDA;
@@ -160,6 +179,26 @@ fa_status run_bwd_main(const void* Q, const void* K, const void* V, const void* 
                                       Lq, Lk, H, Hkv, causal, s)
               : launch_bwd<128, false>(Q, K, V, dO, LSE, Delta, dK, dV, dq_accum, zero_accum, B,
                                        Lq, Lk, H, Hkv, causal, s);
+}
+
+fa_status run_window_bwd(const void* Q, const void* K, const void* V, const void* dO,
+                         const float* LSE, const float* Delta, void* dQ, void* dK, void* dV,
+                         float* dq_accum, int zero_accum, int B, int Lq, int Lk, int H, int Hkv,
+                         int D, int window, int sinks, int dtype, cudaStream_t s) {
+  const bool bf16 = dtype == FA_BF16;
+  fa_status st;
+  if (D == 64)
+    st = bf16 ? launch_bwd<64, true, true>(Q, K, V, dO, LSE, Delta, dK, dV, dq_accum, zero_accum, B,
+                                           Lq, Lk, H, Hkv, 1, s, window, sinks)
+              : launch_bwd<64, false, true>(Q, K, V, dO, LSE, Delta, dK, dV, dq_accum, zero_accum,
+                                            B, Lq, Lk, H, Hkv, 1, s, window, sinks);
+  else
+    st = bf16 ? launch_bwd<128, true, true>(Q, K, V, dO, LSE, Delta, dK, dV, dq_accum, zero_accum,
+                                            B, Lq, Lk, H, Hkv, 1, s, window, sinks)
+              : launch_bwd<128, false, true>(Q, K, V, dO, LSE, Delta, dK, dV, dq_accum, zero_accum,
+                                             B, Lq, Lk, H, Hkv, 1, s, window, sinks);
+  if (st != FA_OK) return st;
+  return run_bwd_post(dq_accum, dQ, B, Lq, H, D, dtype, s);
 }
 
 fa_status run_bwd_post(const float* dq_accum, void* dQ, int B, int L, int H, int D, int dtype,

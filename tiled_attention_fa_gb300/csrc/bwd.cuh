@@ -88,6 +88,11 @@ struct BwdParams {
   int snake;    // 1: units are single tiles in decreasing-work order, dealt out in snake order
   float sl2;    // log2(e) / sqrt(D)
   float scale;  // 1 / sqrt(D)
+  // WIN only: query position a sees key j iff j <= a and (j > a - window or
+  // j < sinks); n_long K/V tiles of all heads hold sink keys and cost cost_long
+  // Q tiles each, the others cost_win (see bwd_unit_item).
+  int window, sinks;
+  int n_long, cost_long, cost_win;
 };
 
 template <int D>
@@ -157,9 +162,11 @@ struct BwdLayout {
 struct BwdItem {
   int b, hkv, j;
   int i0;      // first Q tile visited
+  int per;     // Q tiles visited per query head
   int ntiles;  // (query heads of the group) x (Q tiles visited)
 };
 
+template <bool WIN>
 __device__ __forceinline__ BwdItem bwd_decode(int item, const BwdParams& p) {
   BwdItem it;
   it.j = item % p.n_kv;
@@ -168,8 +175,28 @@ __device__ __forceinline__ BwdItem bwd_decode(int item, const BwdParams& p) {
   it.hkv = bh - it.b * p.Hkv;
   // causal: the first Q tile holding a query that sees key j*128
   it.i0 = p.causal ? max(0, it.j * 128 - p.past) / 128 : 0;
-  it.ntiles = (p.H / p.Hkv) * (p.n_q - it.i0);
+  it.per = p.n_q - it.i0;
+  if constexpr (WIN) {
+    // A tile without sink keys is seen up to position j*128 + 127 + window - 1
+    // (by no query at all when that lies before the first one).
+    if (it.j * 128 >= p.sinks) {
+      const int last = it.j * 128 + 126 + p.window - p.past;  // last query that sees the tile
+      it.per = last < 0 ? 0 : max(0, min(p.n_q, last / 128 + 1) - it.i0);
+    }
+  }
+  it.ntiles = (p.H / p.Hkv) * it.per;
   return it;
+}
+
+// WIN: start of CTA c's contiguous share of the K/V tiles (all heads' sink
+// tiles first, then the others head by head) when G CTAs split their total
+// cost evenly.
+__host__ __device__ inline int bwd_win_start(const BwdParams& p, int G, int c) {
+  const long long head = static_cast<long long>(p.n_long) * p.cost_long;
+  const long long all = head + static_cast<long long>(p.n_items - p.n_long) * p.cost_win;
+  const long long t = all * c / G;
+  return static_cast<int>(t < head ? (t + p.cost_long - 1) / p.cost_long
+                                   : p.n_long + (t - head + p.cost_win - 1) / p.cost_win);
 }
 
 // K/V tile s of work unit u of the persistent CTAs.  Under causal masking a
@@ -186,7 +213,26 @@ __device__ __forceinline__ BwdItem bwd_decode(int item, const BwdParams& p) {
 // heads), round r of the CTAs takes the next gridDim.x of them, CTA c the c-th
 // in even rounds and the (gridDim.x-1-c)-th in odd ones.  The CTAs' loops
 // then run over rounds x gridDim.x units; positions past the tiles are empty.
+// With a window (WIN) every tile costs about the same except the tiles of the
+// sink keys, which every later query sees.  Those come first, then the others
+// head by head, and CTA c takes a contiguous share of the list that costs
+// 1/G of the whole (bwd_win_start): unit u is the (u / G)-th of CTA u % G.
+template <bool WIN>
 __device__ __forceinline__ bool bwd_unit_item(int u, int s, const BwdParams& p, int& item) {
+  if constexpr (WIN) {
+    const int G = static_cast<int>(gridDim.x);
+    const int r = u / G, c = u - r * G;
+    int k = bwd_win_start(p, G, c) + r;
+    if (k >= bwd_win_start(p, G, c + 1)) return false;
+    const int per_head = p.n_long / (p.n_items / p.n_kv);  // sink tiles of one head
+    if (k < p.n_long) {
+      item = k / per_head * p.n_kv + k % per_head;
+    } else {
+      k -= p.n_long;
+      item = k / (p.n_kv - per_head) * p.n_kv + per_head + k % (p.n_kv - per_head);
+    }
+    return true;
+  }
   if (p.snake) {
     const int G = static_cast<int>(gridDim.x);
     const int r = u / G, c = u - r * G;
@@ -212,7 +258,7 @@ __device__ __forceinline__ bool bwd_unit_item(int u, int s, const BwdParams& p, 
 // n-th (head, Q tile) pair of an item: heads of the group outer, tiles inner.
 __device__ __forceinline__ void bwd_tile(const BwdItem& it, const BwdParams& p, int n, int& h,
                                          int& i) {
-  const int per = p.n_q - it.i0;
+  const int per = it.per;
   const int g = n / per;
   // The CTA of K/V tile j starts at the j-th of its Q tiles and wraps around,
   // so the CTAs working on one head at the same time read different Q / dO
@@ -221,7 +267,7 @@ __device__ __forceinline__ void bwd_tile(const BwdItem& it, const BwdParams& p, 
   h = it.hkv * (p.H / p.Hkv) + g;
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool WIN = false>
 __global__ void __launch_bounds__(512, 1)
     fa_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -308,8 +354,8 @@ __global__ void __launch_bounds__(512, 1)
     for (int u = p.ipu * static_cast<int>(blockIdx.x); ok && u < p.ipu * p.n_units;
          u += (u % p.ipu == p.ipu - 1) ? p.ipu * (G - 1) + 1 : 1) {
     int item;
-    if (!bwd_unit_item(u / p.ipu, u % p.ipu, p, item)) continue;
-    const BwdItem it = bwd_decode(item, p);
+    if (!bwd_unit_item<WIN>(u / p.ipu, u % p.ipu, p, item)) continue;
+    const BwdItem it = bwd_decode<WIN>(item, p);
     const int kvs = static_cast<int>(kv_cnt % Ly::KVS);
     const uint32_t kv_round = kv_cnt / Ly::KVS;
     if (kv_round > 0 &&
@@ -416,8 +462,8 @@ __global__ void __launch_bounds__(512, 1)
     for (int u = p.ipu * static_cast<int>(blockIdx.x); ok && u < p.ipu * p.n_units;
          u += (u % p.ipu == p.ipu - 1) ? p.ipu * (G - 1) + 1 : 1) {
     int item;
-    if (!bwd_unit_item(u / p.ipu, u % p.ipu, p, item)) continue;
-    const BwdItem it = bwd_decode(item, p);
+    if (!bwd_unit_item<WIN>(u / p.ipu, u % p.ipu, p, item)) continue;
+    const BwdItem it = bwd_decode<WIN>(item, p);
     const int kvs = static_cast<int>(kv_cnt % Ly::KVS);
     if (!mbar_wait_warp(bar(Ly::B_KVFULL + kvs), (kv_cnt / Ly::KVS) & 1, ab, err, 501)) {
       ok = false;
@@ -552,8 +598,8 @@ __global__ void __launch_bounds__(512, 1)
     for (int u = p.ipu * static_cast<int>(blockIdx.x); ok && u < p.ipu * p.n_units;
          u += (u % p.ipu == p.ipu - 1) ? p.ipu * (G - 1) + 1 : 1) {
     int item;
-    if (!bwd_unit_item(u / p.ipu, u % p.ipu, p, item)) continue;
-    const BwdItem it = bwd_decode(item, p);
+    if (!bwd_unit_item<WIN>(u / p.ipu, u % p.ipu, p, item)) continue;
+    const BwdItem it = bwd_decode<WIN>(item, p);
     const int kr = it.j * 128 + r;
     for (int n = 0; ok && n < it.ntiles; ++n, ++g) {
       int h, i;
@@ -574,6 +620,7 @@ __global__ void __launch_bounds__(512, 1)
         int lo = 0, hi = min(32, p.Lq - q0);
         if (kr >= p.Lk) hi = 0;
         if (p.causal) lo = max(0, kr - p.past - q0);
+        if (WIN && kr >= p.sinks) hi = min(hi, kr + p.window - p.past - q0);
         const bool full = (lo == 0 && hi == 32);
         // P^T = exp2(S^T*c - LSE*log2e), from S^T alone.
         uint32_t* sv = pf[hc];
@@ -678,6 +725,10 @@ __global__ void __launch_bounds__(512, 1)
         uint32_t o[32];
         tmem_ld32(tsrc + 32 * cc, o);
         tmem_ld_wait32(o);
+        if (WIN && it.ntiles == 0) {  // keys no query sees: nothing was accumulated
+#pragma unroll
+          for (int u = 0; u < 32; ++u) o[u] = 0u;
+        }
         uint32_t pk[16];
 #pragma unroll
         for (int u = 0; u < 16; ++u)
@@ -702,8 +753,8 @@ __global__ void __launch_bounds__(512, 1)
     for (int u = p.ipu * static_cast<int>(blockIdx.x); ok && u < p.ipu * p.n_units;
          u += (u % p.ipu == p.ipu - 1) ? p.ipu * (G - 1) + 1 : 1) {
     int item;
-    if (!bwd_unit_item(u / p.ipu, u % p.ipu, p, item)) continue;
-    const BwdItem it = bwd_decode(item, p);
+    if (!bwd_unit_item<WIN>(u / p.ipu, u % p.ipu, p, item)) continue;
+    const BwdItem it = bwd_decode<WIN>(item, p);
     for (int n = 0; n < it.ntiles; ++n, ++g) {
       int h, i;
       bwd_tile(it, p, n, h, i);

@@ -10,10 +10,12 @@ namespace fa {
 
 // FP8: Q, K, V are E4M3 codes with per-tensor scales qs, ks, vs; BF16 then
 // selects the output type.
-template <int D, bool BF16, bool FP8 = false>
+// window > 0 (WIN, causal calls only) limits each query to the last `window`
+// keys before it and the first `sinks`.
+template <int D, bool BF16, bool FP8 = false, bool WIN = false>
 static fa_status launch(const void* Q, const void* K, const void* V, void* O, float* LSE, int B,
                         int Lq, int Lk, int H, int Hkv, int causal, cudaStream_t s, float qs = 1.f,
-                        float ks = 1.f, float vs = 1.f) {
+                        float ks = 1.f, float vs = 1.f, int window = 0, int sinks = 0) {
   using Ly = FwdLayout<D, FP8>;
   CUtensorMap tq, tk, tv;
   if constexpr (FP8) {
@@ -54,7 +56,9 @@ static fa_status launch(const void* Q, const void* K, const void* V, void* O, fl
   // (512 MiB, 54 rounds) it lost 12%, and at D = 64 (B8 H32 L1024, B4 H32/8
   // L1024) it was neutral to 5% slower, so D = 128 only.
   p.sorted = 0;
-  {
+  p.window = window < Lk ? window : Lk;  // as good as every key when larger
+  p.sinks = sinks < Lk ? sinks : Lk;
+  if (!WIN) {
     const int sm = sm_count();
     int dev = 0, l2 = 0;
     cudaGetDevice(&dev);
@@ -63,7 +67,7 @@ static fa_status launch(const void* Q, const void* K, const void* V, void* O, fl
     if (D == 128 && causal && p.n_items >= sm && p.n_items <= 8 * sm && kv_bytes <= 1.2 * l2)
       p.sorted = 1;
   }
-  auto kern = fa_fwd_kernel<D, BF16, FP8>;
+  auto kern = fa_fwd_kernel<D, BF16, FP8, WIN>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::SMEM_ALLOC) !=
       cudaSuccess)
     return FA_ERR_CUDA;
@@ -81,6 +85,22 @@ fa_status run_fwd(const void* Q, const void* K, const void* V, void* O, float* L
   }
   return bf16 ? launch<128, true>(Q, K, V, O, LSE, B, Lq, Lk, H, Hkv, causal, s)
               : launch<128, false>(Q, K, V, O, LSE, B, Lq, Lk, H, Hkv, causal, s);
+}
+
+fa_status run_window_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE, int B,
+                         int Lq, int Lk, int H, int Hkv, int D, int window, int sinks, int dtype,
+                         cudaStream_t s) {
+  const bool bf16 = dtype == FA_BF16;
+  if (D == 64) {
+    return bf16 ? launch<64, true, false, true>(Q, K, V, O, LSE, B, Lq, Lk, H, Hkv, 1, s, 1.f, 1.f,
+                                                1.f, window, sinks)
+                : launch<64, false, false, true>(Q, K, V, O, LSE, B, Lq, Lk, H, Hkv, 1, s, 1.f,
+                                                 1.f, 1.f, window, sinks);
+  }
+  return bf16 ? launch<128, true, false, true>(Q, K, V, O, LSE, B, Lq, Lk, H, Hkv, 1, s, 1.f, 1.f,
+                                               1.f, window, sinks)
+              : launch<128, false, false, true>(Q, K, V, O, LSE, B, Lq, Lk, H, Hkv, 1, s, 1.f, 1.f,
+                                                1.f, window, sinks);
 }
 
 fa_status run_fwd_fp8(const void* Q8, const void* K8, const void* V8, float q_scale, float k_scale,

@@ -26,6 +26,16 @@
 // exponentials overlap the MMAs.  O is rescaled only when a row max grows by
 // more than 2^8 (in exp2 units); the stale max is used consistently for l and
 // O, so the final O / l is exact up to rounding.
+//
+// Sliding window with sinks (WIN): query position a = q + past sees key j iff
+// j <= a and (j > a - window or j < sinks).  A Q tile then visits the tiles
+// that hold its sink keys and the tiles its rows' windows touch, and nothing
+// between, so the work per query is window + sinks keys however long the
+// sequence is.  The two Q tiles of a pair share one list of K/V tiles (sink
+// tiles, then window tiles from the first row's window on); the second tile
+// skips the one window tile that only the first needs.  A row may see nothing
+// of its first tiles (its window starts further right), so the running max can
+// be -inf there: exponents are then taken against 0, giving P = 0.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -47,6 +57,7 @@ struct FwdParams {
   float sl2;     // log2(e) / sqrt(D) (times q_scale * k_scale for E4M3 inputs)
   float o_scale; // factor on O / l at the store: 1, or v_scale for E4M3 inputs
   int sorted;    // 1: items ordered by decreasing work across all heads (else head-major)
+  int window, sinks;  // WIN only: 1 <= window <= Lk, 0 <= sinks <= Lk
 };
 
 // FP8: Q, K, V are E4M3 codes (one byte per element; D = 128 only).
@@ -89,8 +100,12 @@ struct FwdLayout {
 struct FwdItem {
   int b, h, hkv, q0;
   int n[2];  // KV tiles visited by Q tile 0 / 1 (0 = tile lies past L)
+  // WIN: step j of the item visits tile j of the ns sink tiles, then tiles lo,
+  // lo + 1, ...; step `hole` (or none, -1) is not visited by Q tile 1.
+  int ns, lo, hole;
 };
 
+template <bool WIN>
 __device__ __forceinline__ FwdItem fwd_decode(int item, const FwdParams& p) {
   FwdItem it;
   int bh, qp;
@@ -111,11 +126,24 @@ __device__ __forceinline__ FwdItem fwd_decode(int item, const FwdParams& p) {
   it.h = bh - it.b * p.H;
   it.hkv = it.h / (p.H / p.Hkv);
   it.q0 = qp * 256;
+  if constexpr (WIN) {
+    const int n_sink = (p.sinks + 127) / 128;
+    const int a0 = it.q0 + p.past;  // position of the pair's first row
+    const int lo1 = max(a0 + 128 - p.window + 1, 0) / 128;
+    it.lo = max(a0 - p.window + 1, 0) / 128;
+    it.ns = min(n_sink, it.lo);
+    // Rows past Lq lie past Lk too; a tile with any row inside has a last
+    // visible tile of at least its own window's first.
+    it.n[0] = it.ns + min((a0 + 127) / 128 + 1, p.n_kv) - it.lo;
+    it.n[1] = it.q0 + 128 < p.Lq ? it.ns + min((a0 + 255) / 128 + 1, p.n_kv) - it.lo : 0;
+    it.hole = (it.n[1] > 0 && lo1 > it.lo && n_sink <= it.lo) ? it.ns : -1;
+  } else {
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int lo = it.q0 + 128 * t;
-    if (lo >= p.Lq) it.n[t] = 0;
-    else it.n[t] = p.causal ? min((lo + 127 + p.past) / 128 + 1, p.n_kv) : p.n_kv;
+    for (int t = 0; t < 2; ++t) {
+      const int lo = it.q0 + 128 * t;
+      if (lo >= p.Lq) it.n[t] = 0;
+      else it.n[t] = p.causal ? min((lo + 127 + p.past) / 128 + 1, p.n_kv) : p.n_kv;
+    }
   }
   return it;
 }
@@ -143,7 +171,22 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-template <int D, bool BF16, bool FP8 = false>
+// Does Q tile t visit step j of the item / is it its first step, and which
+// K/V tile is it.
+template <bool WIN>
+__device__ __forceinline__ bool fwd_visits(const FwdItem& it, int t, int j) {
+  return j < it.n[t] && (!WIN || t == 0 || j != it.hole);
+}
+template <bool WIN>
+__device__ __forceinline__ bool fwd_first(const FwdItem& it, int t, int j) {
+  return j == ((WIN && t == 1 && it.hole == 0) ? 1 : 0);
+}
+template <bool WIN>
+__device__ __forceinline__ int fwd_kv_tile(const FwdItem& it, int j) {
+  return !WIN || j < it.ns ? j : it.lo + j - it.ns;
+}
+
+template <int D, bool BF16, bool FP8 = false, bool WIN = false>
 __global__ void __launch_bounds__(320, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
@@ -210,7 +253,7 @@ __global__ void __launch_bounds__(320, 1)
       for (int round = 0; ok && round * static_cast<int>(gridDim.x) < p.n_items; ++round) {
         const int item = fwd_item_of(round);
         if (item >= p.n_items) continue;
-        const FwdItem it = fwd_decode(item, p);
+        const FwdItem it = fwd_decode<WIN>(item, p);
         if (q_uses > 0 && !mbar_wait(bar(Ly::B_QEMPTY), (q_uses - 1) & 1, ab, err, 101)) {
           ok = false;
           break;
@@ -234,10 +277,10 @@ __global__ void __launch_bounds__(320, 1)
           for (int c = 0; c < Ly::KCH; ++c) {
             if (j > 0)
               tma_load_4d_hint(slot + c * Ly::CHUNK, &tmV, bar(Ly::B_KVFULL + stage),
-                               c * (128 / Ly::EB), it.hkv, (j - 1) * 128, it.b, keep);
+                               c * (128 / Ly::EB), it.hkv, fwd_kv_tile<WIN>(it, j - 1) * 128, it.b, keep);
             if (j < nmax)
               tma_load_4d_hint(slot + Ly::TILE + c * Ly::CHUNK, &tmK, bar(Ly::B_KVFULL + stage),
-                               c * (128 / Ly::EB), it.hkv, j * 128, it.b, keep);
+                               c * (128 / Ly::EB), it.hkv, fwd_kv_tile<WIN>(it, j) * 128, it.b, keep);
           }
           ++issued[stage];
           if (++stage == Ly::STAGES) {
@@ -322,7 +365,7 @@ __global__ void __launch_bounds__(320, 1)
       for (int round = 0; ok && round * static_cast<int>(gridDim.x) < p.n_items; ++round) {
         const int item = fwd_item_of(round);
         if (item >= p.n_items) continue;
-        const FwdItem it = fwd_decode(item, p);
+        const FwdItem it = fwd_decode<WIN>(item, p);
         const int nmax = max(it.n[0], it.n[1]);
         if (!mbar_wait_warp(bar(Ly::B_QFULL), q_cnt & 1, ab, err, 201)) { ok = false; break; }
         ++q_cnt;
@@ -350,7 +393,7 @@ __global__ void __launch_bounds__(320, 1)
         if (!take(ps, 202)) { ok = false; break; }
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          if (it.n[t] > 0) {
+          if (fwd_visits<WIN>(it, t, 0)) {
             issue_s(t, ps);
             commit(Ly::B_SFULL + t);
           }
@@ -362,8 +405,9 @@ __global__ void __launch_bounds__(320, 1)
           for (int t = 0; t < 2; ++t) {
             uint32_t& p_cnt = t ? p_cnt1 : p_cnt0;
             uint32_t& o_uses = t ? o_uses1 : o_uses0;
-            if (j < it.n[t]) {
-              if (j == 0 && o_uses > 0 &&
+            if (fwd_visits<WIN>(it, t, j)) {
+              const bool first = fwd_first<WIN>(it, t, j);
+              if (first && o_uses > 0 &&
                   !mbar_wait_warp(bar(Ly::B_OEMPTY + t), (o_uses - 1) & 1, ab, err, 204)) {
                 ok = false;
                 break;
@@ -374,7 +418,7 @@ __global__ void __launch_bounds__(320, 1)
                 break;
               }
               tc_fence_after();
-              issue_pv(t, ps, j > 0, 0, Ly::KS_PV / 2);
+              issue_pv(t, ps, !first, 0, Ly::KS_PV / 2);
               if (!mbar_wait_warp(bar(Ly::B_PFULL + 2 * t + 1), p_cnt & 1, ab, err, 207)) {
                 ok = false;
                 break;
@@ -387,7 +431,7 @@ __global__ void __launch_bounds__(320, 1)
                 ++o_uses;
               }
             }
-            if (j + 1 < it.n[t]) {
+            if (fwd_visits<WIN>(it, t, j + 1)) {
               issue_s(t, ps);
               commit(Ly::B_SFULL + t);
             }
@@ -416,13 +460,14 @@ __global__ void __launch_bounds__(320, 1)
     for (int round = 0; ok && round * static_cast<int>(gridDim.x) < p.n_items; ++round) {
         const int item = fwd_item_of(round);
         if (item >= p.n_items) continue;
-      const FwdItem it = fwd_decode(item, p);
+      const FwdItem it = fwd_decode<WIN>(item, p);
       const int n = it.n[t];
       if (n == 0) continue;
       const int tile_lo = it.q0 + 128 * t;
       const int q = tile_lo + r;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
+        if (!fwd_visits<WIN>(it, t, j)) continue;
         if (!mbar_wait_warp(bar(Ly::B_SFULL + t), s_cnt & 1, ab, err, 301)) { ok = false; break; }
         ++s_cnt;
         tc_fence_after();
@@ -435,9 +480,19 @@ __global__ void __launch_bounds__(320, 1)
         tmem_ld_wait32(sr + 32);
         tmem_ld_wait32(sr + 64);
         tmem_ld_wait32(sr + 96);
-        const int k0 = j * 128;
+        const int k0 = fwd_kv_tile<WIN>(it, j) * 128;
         const bool need_mask = (k0 + 128 > p.Lk) || (p.causal && k0 + 127 > tile_lo + p.past);
-        if (need_mask) {
+        if constexpr (WIN) {
+          // Tiles that straddle the diagonal, the window's start or the last
+          // sink key; hidden: key >= lim, or sinks <= key < wlo.
+          const int a = q + p.past;
+          if (need_mask || (k0 + p.window <= tile_lo + 127 + p.past && k0 + 128 > p.sinks)) {
+            const int lim = min(a + 1, p.Lk) - k0, wlo = a - p.window + 1 - k0, snk = p.sinks - k0;
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (c >= lim || (c < wlo && c >= snk)) sr[c] = __float_as_uint(-INFINITY);
+          }
+        } else if (need_mask) {
           const int lim = p.causal ? min(q + p.past + 1, p.Lk) : p.Lk;  // keys [0, lim) visible
 #pragma unroll
           for (int c = 0; c < 128; ++c)
@@ -460,12 +515,13 @@ __global__ void __launch_bounds__(320, 1)
         const float m_new = fmaxf(m, mx);
         float alpha = 1.f;
         bool rescale = false;
-        if (j == 0) {
+        if (fwd_first<WIN>(it, t, j)) {
           m = m_new;
         } else if (__any_sync(0xffffffffu, (m_new - m) * sl2 > 8.0f)) {
           // The running max grew by more than 2^8 somewhere in this warp:
           // rescale this warp's rows (others get alpha = 1).
-          alpha = ex2((m - m_new) * sl2);
+          // (WIN: a row that has seen no key yet keeps its -inf and has O = l = 0.)
+          if (!WIN || m_new != -INFINITY) alpha = ex2((m - m_new) * sl2);
           m = m_new;
           rescale = true;
         }
@@ -492,7 +548,7 @@ __global__ void __launch_bounds__(320, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(Ly::B_PFULL + 2 * t + h));
         };
-        const float mb = m * sl2;
+        const float mb = (WIN && m == -INFINITY) ? 0.f : m * sl2;
         float rs = 0.f;
         if constexpr (FP8) {
           // Exponent arguments and the row sum on paired fp32 instructions

@@ -12,6 +12,9 @@ fa_status run_fwd(const void* Q, const void* K, const void* V, void* O, float* L
 fa_status run_fwd_fp8(const void* Q8, const void* K8, const void* V8, float q_scale, float k_scale,
                       float v_scale, void* O, float* LSE, int B, int Lq, int Lk, int H, int Hkv,
                       int causal, int out_dtype, cudaStream_t s);
+fa_status run_window_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE, int B,
+                         int Lq, int Lk, int H, int Hkv, int D, int window, int sinks, int dtype,
+                         cudaStream_t s);
 unsigned int fwd_read_error(cudaStream_t s);
 fa_status run_selftest_wait(unsigned long long limit_ns, cudaStream_t s);
 
@@ -27,6 +30,10 @@ fa_status run_bwd_main(const void* Q, const void* K, const void* V, const void* 
                        int dtype, cudaStream_t s);
 fa_status run_bwd_post(const float* dq_accum, void* dQ, int B, int L, int H, int D, int dtype,
                        cudaStream_t s);
+fa_status run_window_bwd(const void* Q, const void* K, const void* V, const void* dO,
+                         const float* LSE, const float* Delta, void* dQ, void* dK, void* dV,
+                         float* dq_accum, int zero_accum, int B, int Lq, int Lk, int H, int Hkv,
+                         int D, int window, int sinks, int dtype, cudaStream_t s);
 unsigned int bwd_read_error(cudaStream_t s);
 fa_status run_bwd_noalloc(const void* Q, const void* K, const void* V, const void* dO,
                           const float* LSE, const float* Delta, void* dQ, void* dK, void* dV,
