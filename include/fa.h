@@ -135,6 +135,62 @@ fa_status fa_decode_merge(const void* workspace, size_t workspace_bytes, void* O
                           int Lq, int Lk, int H, int Hkv, int D, int dtype, void* stream);
 
 /*
+ * Paged key/value cache.  K and V live in two pools of pages,
+ * [num_pages, page, Hkv, D] (page in {16, 32, 64, 128, 256},
+ * FA_ERR_UNSUPPORTED otherwise), whose pages are page_stride elements apart
+ * (a multiple of 8, at least page * Hkv * D: both pools may be halves of one
+ * tensor).  Row b of block_table [B, max_pages] int32 lists the pages of
+ * sequence b in order: its key t lies in page block_table[b, t / page], row
+ * t % page.  Tables and lengths are read on the device when the kernels run.
+ * A page id outside [0, num_pages) reads as zero keys and values and is never
+ * written; lengths are clamped to [0, max_pages * page].
+ * Tables, lengths and the like need the alignment of an int only.
+ * Key weights, where given, are fp32 [B, Hkv, *]: the weight of key t of
+ * sequence b and K/V head h is weights[(b * Hkv + h) * weights_stride + t],
+ * with weights_stride >= max_pages * page.
+ *
+ * fa_paged_write: put the new keys and values K, V [B, L, Hkv, D] into the
+ * pages.  Token j of sequence b goes to position start[b] + j; only the first
+ * counts[b] tokens when counts [B] is given (a padded batch).  Positions
+ * outside the table are skipped.  With `weights`, the weights of the slots
+ * written become new_weights [B, Hkv, L] (fa_key_weights of the prompt), or 0
+ * when that is NULL.  Two tokens of one call must not share a slot.
+ */
+fa_status fa_paged_write(const void* K, const void* V, void* K_pool, void* V_pool,
+                         long long k_page_stride, long long v_page_stride, const int* block_table,
+                         const int* start, const int* counts, float* weights,
+                         long long weights_stride, const float* new_weights, int B, int L, int Hkv,
+                         int D, int page, int max_pages, int num_pages, int dtype, void* stream);
+
+/*
+ * fa_paged_decode: attention of the last Lq tokens of every sequence over its
+ * paged keys and values (already written).  lens [B] counts all keys, the new
+ * ones included: query i of sequence b has position a = lens[b] - Lq + i and
+ * sees key j iff j <= a and (window == 0, or j > a - window, or j < sinks).
+ * A query that sees nothing (a negative position, an empty sequence) gives
+ * O = 0, LSE = -inf.  Keys that no query of the call sees are never used,
+ * whatever their slots hold; pages wholly behind the length or before the
+ * window are not read and may be absent from the table.
+ * Q, O [B, Lq, H, D]; LSE [B, H, Lq]; (H / Hkv) * Lq <= 128
+ * (FA_ERR_UNSUPPORTED otherwise).  With `weights` the call adds to each
+ * visible key's weight sum over the group's heads and the queries of
+ * exp(q . k / sqrt(D) - LSE).  Every key is added to once, by one thread:
+ * results do not depend on any order, and sequences may share pages.
+ * `workspace`: fa_paged_decode_workspace_size bytes, asked with the device
+ * that runs the call current (FA_ERR_SCRATCH_TOO_SMALL when smaller); its
+ * contents need no initialisation; calls (and replayed graphs) that overlap
+ * on the GPU must not share one.
+ */
+size_t fa_paged_decode_workspace_size(int B, int Lq, int H, int Hkv, int D, int page, int max_pages,
+                                      int weights);
+fa_status fa_paged_decode(const void* Q, const void* K_pool, const void* V_pool,
+                          long long k_page_stride, long long v_page_stride, const int* block_table,
+                          const int* lens, void* O, float* LSE, float* weights,
+                          long long weights_stride, void* workspace, size_t workspace_bytes, int B,
+                          int Lq, int H, int Hkv, int D, int page, int max_pages, int num_pages,
+                          int window, int sinks, int dtype, void* stream);
+
+/*
  * Backward preprocess: Delta[b, h, i] = sum_d O[b, i, h, d] * dO[b, i, h, d]
  * (fp32 accumulation), the per-row term of the softmax gradient.  Page
  * "TileLang与机器学习训练：反向传播算子优化案例", section 算子拆分与流水线设计

@@ -1,0 +1,74 @@
+"""Host-side checks of the window and paged-cache entry points (no GPU): every bad argument is
+refused before anything reaches the device."""
+
+import os
+
+import pytest
+
+from tiled_attention_fa_gb300 import _lib
+
+FAKE = 0x10000  # never dereferenced: every call below fails validation first
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(_lib.LIB_PATH):
+        from tiled_attention_fa_gb300 import build
+        build.build(quiet=True)
+    return _lib.load()
+
+
+def caller(fn, names, good):
+    def call(**kw):
+        a = list(good)
+        for key, val in kw.items():
+            a[names.index(key)] = val
+        return fn(*a, None)
+    return call
+
+
+INVALID, UNSUPPORTED, SMALL = _lib.FA_ERR_INVALID_ARG, _lib.FA_ERR_UNSUPPORTED, _lib.FA_ERR_SCRATCH_TOO_SMALL
+
+
+def test_window(lib):
+    fwd = caller(lib.fa_window_fwd, "Q K V O LSE B Lq Lk H Hkv D window sinks dtype".split(),
+                 [FAKE] * 5 + [1, 100, 200, 4, 2, 64, 50, 4, 0])
+    bwd = caller(lib.fa_window_bwd, "Q K V dO LSE Delta dQ dK dV acc zero B Lq Lk H Hkv D window sinks dtype".split(),
+                 [FAKE] * 10 + [1, 1, 100, 200, 4, 2, 64, 50, 4, 0])
+    for call in (fwd, bwd):
+        for kw in (dict(Q=None), dict(K=FAKE + 8), dict(LSE=None), dict(window=0), dict(sinks=-1), dict(Lk=99),
+                   dict(H=3), dict(B=0)):
+            assert call(**kw) == INVALID, kw
+        assert call(D=96) == UNSUPPORTED and call(dtype=5) == UNSUPPORTED
+    assert bwd(acc=None) == INVALID and bwd(dK=None) == INVALID
+
+
+def test_paged_decode(lib):
+    names = ("Q K V kst vst table lens O LSE w wst ws ws_bytes B Lq H Hkv D page max_pages num_pages window sinks "
+             "dtype").split()
+    call = caller(lib.fa_paged_decode, names,
+                  [FAKE, FAKE, FAKE, 16 * 2 * 64, 16 * 2 * 64, FAKE, FAKE, FAKE, FAKE, None, 0, FAKE, 1 << 40, 2, 1, 4,
+                   2, 64, 16, 10, 30, 0, 0, 0])
+    for kw in (dict(Q=None), dict(V=FAKE + 8), dict(table=None), dict(lens=FAKE + 2), dict(O=None), dict(ws=None),
+               dict(kst=16 * 2 * 64 - 8), dict(vst=16 * 2 * 64 + 4), dict(window=-1), dict(sinks=-1), dict(max_pages=0),
+               dict(num_pages=0), dict(H=5), dict(B=0), dict(w=FAKE, wst=100), dict(w=FAKE + 4, wst=160),
+               dict(max_pages=1 << 30)):
+        assert call(**kw) == INVALID, kw
+    for kw in (dict(D=80), dict(dtype=2), dict(page=24), dict(page=8), dict(Lq=65)):
+        kw = dict(kw, kst=1 << 20, vst=1 << 20)
+        assert call(**kw) == UNSUPPORTED, kw
+    assert call(ws_bytes=0) == SMALL
+    size = lib.fa_paged_decode_workspace_size
+    assert size(2, 1, 4, 2, 64, 16, 10, 1) - size(2, 1, 4, 2, 64, 16, 10, 0) == 2 * 2 * 2 * 2 * 128 * 4
+    assert size(0, 1, 4, 2, 64, 16, 10, 0) == 0 and size(2, 1, 4, 2, 80, 16, 10, 0) == 0
+    assert size(2, 65, 4, 2, 64, 16, 10, 0) == 0
+
+
+def test_paged_write(lib):
+    names = "K V kc vc kst vst table start counts w wst nw B L Hkv D page max_pages num_pages dtype".split()
+    call = caller(lib.fa_paged_write, names,
+                  [FAKE] * 4 + [2048, 2048, FAKE, FAKE, None, None, 0, None, 2, 7, 2, 64, 16, 10, 30, 0])
+    for kw in (dict(K=None), dict(vc=FAKE + 8), dict(start=None), dict(counts=FAKE + 1), dict(nw=FAKE), dict(w=FAKE, wst=5),
+               dict(kst=2040), dict(L=0), dict(max_pages=0)):
+        assert call(**kw) == INVALID, kw
+    assert call(D=96, kst=1 << 20, vst=1 << 20) == UNSUPPORTED and call(page=17) == UNSUPPORTED

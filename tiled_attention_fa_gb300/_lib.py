@@ -23,6 +23,7 @@ _lib = None
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
+_ll = ctypes.c_longlong
 _SIGS = {
     "fa_fwd": ([_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp], _i),
     "fa_fwd_kv": ([_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp], _i),
@@ -40,6 +41,10 @@ _SIGS = {
     "fa_decode": ([_vp] * 6 + [ctypes.c_size_t] + [_i] * 8 + [_vp], _i),
     "fa_decode_slices": ([_vp] * 4 + [ctypes.c_size_t] + [_i] * 8 + [_vp], _i),
     "fa_decode_merge": ([_vp, ctypes.c_size_t, _vp, _vp] + [_i] * 7 + [_vp], _i),
+    "fa_paged_write": ([_vp] * 4 + [_ll, _ll] + [_vp] * 4 + [_ll, _vp] + [_i] * 8 + [_vp], _i),
+    "fa_paged_decode_workspace_size": ([_i] * 8, ctypes.c_size_t),
+    "fa_paged_decode": ([_vp] * 3 + [_ll, _ll] + [_vp] * 5 + [_ll, _vp, ctypes.c_size_t] + [_i] * 11
+                        + [_vp], _i),
     "fa_check_device_error": ([_vp], _i),
     "fa_last_error_site": ([], ctypes.c_uint),
     "fa_selftest_bounded_wait": ([ctypes.c_ulonglong, _vp], _i),

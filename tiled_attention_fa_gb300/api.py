@@ -36,6 +36,20 @@ def _need(t: torch.Tensor, name: str, shape=None, dtype=None):
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
 
 
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on_current_device(*tensors) -> None:
+    """Refuse tensors that lie elsewhere than on the current device, whose
+    stream the kernels go to."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"a tensor lies on cuda:{t.get_device()}, the current device is "
+                             f"cuda:{here}")
+
+
 def _stream(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -88,6 +102,7 @@ def window_fwd(q, k, v, window: int, sinks: int = 0, out=None, lse=None, stream=
         lse = torch.empty(B, H, L, device=q.device, dtype=torch.float32)
     _need(out, "out", q.shape, q.dtype)
     _need(lse, "lse", (B, H, L), torch.float32)
+    _on_current_device(q, k, v, out, lse)
     st = _lib.load().fa_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                    lse.data_ptr(), B, L, Lk, H, Hkv, D, window, sinks,
                                    _dtype_code(q), _stream(stream))
@@ -204,6 +219,107 @@ def decode_merge(workspace, out, lse, Lk: int, Hkv: int, stream=None):
     _lib.check("fa_decode_merge", st)
 
 
+def _pools(k_cache, v_cache, dtype):
+    """(num_pages, page, Hkv, D) of two pools whose pages may lie apart but are
+    contiguous in themselves (halves of one tensor, for instance)."""
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        if t.dim() != 4 or t.shape != k_cache.shape:
+            raise ValueError(f"{name} must be [pages, page, Hkv, D], both pools alike")
+        _, page, hkv, d = t.shape
+        if t.stride()[1:] != (hkv * d, d, 1):
+            raise ValueError(f"the pages of {name} must be contiguous")
+    return k_cache.shape
+
+
+def _page_stride(t) -> int:
+    """Elements between two pages (of a pool of one page: the page itself)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2] * t.shape[3]
+
+
+def _row_stride(weights, name, B, Hkv, cap) -> int:
+    """Elements between the rows of key weights [B, Hkv, >= cap] fp32."""
+    _need(weights, name, dtype=torch.float32)
+    if weights.dim() != 3 or weights.shape[:2] != (B, Hkv) or weights.shape[2] < cap:
+        raise ValueError(f"{name} has shape {tuple(weights.shape)}, expected ({B}, {Hkv}, >= {cap})")
+    return weights.shape[2]
+
+
+def paged_write(k, v, k_cache, v_cache, block_table, start, counts=None, weights=None,
+                new_weights=None, stream=None) -> None:
+    """Write new keys and values k, v [B, L, Hkv, D] into the pages of
+    k_cache, v_cache [pages, page, Hkv, D]: token j of sequence b goes to
+    position start[b] + j, in page block_table[b, position // page].
+    block_table [B, P], start [B] and counts [B] (tokens of each sequence that
+    count, all L when None) are int32.  ``weights`` [B, Hkv, >= P * page] fp32
+    gets ``new_weights`` [B, Hkv, L] (or 0) at the positions written."""
+    num_pages, page, Hkv, D = _pools(k_cache, v_cache, k.dtype)
+    B, L = k.shape[:2]
+    _need(k, "k", (B, L, Hkv, D))
+    _need(v, "v", (B, L, Hkv, D), k.dtype)
+    P = block_table.shape[-1]
+    _need(block_table, "block_table", (B, P), torch.int32)
+    _need(start, "start", (B,), torch.int32)
+    if counts is not None:
+        _need(counts, "counts", (B,), torch.int32)
+    wstride = 0
+    if weights is not None:
+        wstride = _row_stride(weights, "weights", B, Hkv, P * page)
+    if new_weights is not None:
+        _need(new_weights, "new_weights", (B, Hkv, L), torch.float32)
+    _on_current_device(k, v, k_cache, v_cache, block_table, start, counts, weights, new_weights)
+    st = _lib.load().fa_paged_write(
+        k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _page_stride(k_cache),
+        _page_stride(v_cache), block_table.data_ptr(), start.data_ptr(), _ptr(counts), _ptr(weights),
+        wstride, _ptr(new_weights), B, L, Hkv, D, page, P, num_pages, _dtype_code(k), _stream(stream))
+    _lib.check("fa_paged_write", st)
+
+
+def paged_decode_workspace_size(B: int, Lq: int, H: int, Hkv: int, D: int, page: int, max_pages: int,
+                                weights: bool = False) -> int:
+    """Bytes of the workspace ``paged_decode`` needs on the current device."""
+    return int(_lib.load().fa_paged_decode_workspace_size(B, Lq, H, Hkv, D, page, max_pages,
+                                                          int(weights)))
+
+
+def paged_decode(q, k_cache, v_cache, block_table, lens, window: int = 0, sinks: int = 0,
+                 weights=None, out=None, lse=None, workspace=None, stream=None):
+    """O, LSE of the last Lq tokens of every sequence, q [B, Lq, H, D], over
+    its keys and values in the pages of k_cache, v_cache [pages, page, Hkv, D].
+    block_table [B, P] and lens [B] are int32; lens counts all keys, the new
+    tokens' own included: query i sits at position a = lens[b] - Lq + i and
+    sees key j iff j <= a and (window == 0 or j > a - window or j < sinks).  A
+    query that sees nothing gives O = 0, LSE = -inf.  (H / Hkv) * Lq <= 128.
+    ``weights`` [B, Hkv, >= P * page] fp32 is added to in place: each key's
+    attention weight over the queries and the group's heads.  ``workspace`` (a
+    CUDA byte tensor of at least ``paged_decode_workspace_size`` bytes) is
+    allocated when not given."""
+    num_pages, page, Hkv, D = _pools(k_cache, v_cache, q.dtype)
+    B, Lq, H, _ = q.shape
+    _need(q, "q", (B, Lq, H, D))
+    P = block_table.shape[-1]
+    _need(block_table, "block_table", (B, P), torch.int32)
+    _need(lens, "lens", (B,), torch.int32)
+    out, lse = _decode_outputs(q, B, Lq, H, out, lse)
+    wstride = 0
+    if weights is not None:
+        wstride = _row_stride(weights, "weights", B, Hkv, P * page)
+    _on_current_device(q, k_cache, v_cache, block_table, lens, weights, out, lse, workspace)
+    if workspace is None:
+        n = paged_decode_workspace_size(B, Lq, H, Hkv, D, page, P, weights is not None)
+        workspace = torch.empty(max(n, 16), device=q.device, dtype=torch.uint8)
+    st = _lib.load().fa_paged_decode(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _page_stride(k_cache),
+        _page_stride(v_cache), block_table.data_ptr(), lens.data_ptr(), out.data_ptr(),
+        lse.data_ptr(), _ptr(weights), wstride, workspace.data_ptr(), _nbytes(workspace), B, Lq, H,
+        Hkv, D, page, P, num_pages, window, sinks, _dtype_code(q), _stream(stream))
+    _lib.check("fa_paged_decode", st)
+    return out, lse
+
+
 def workspace_size(B: int, L: int, H: int, D: int) -> int:
     """Bytes of the fp32 dQ accumulator the backward needs."""
     return int(_lib.load().fa_bwd_workspace_size(B, L, H, D))
@@ -293,6 +409,7 @@ def window_bwd(q, k, v, do, lse, delta, window: int, sinks: int = 0, dq=None, dk
     _need(dq_accum, "dq_accum", dtype=torch.float32)
     if dq_accum.numel() * 4 < workspace_size(B, L, H, D):
         raise ValueError("dq_accum is smaller than workspace_size()")
+    _on_current_device(q, k, v, do, lse, delta, dq, dk, dv, dq_accum)
     st = _lib.load().fa_window_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), do.data_ptr(),
                                    lse.data_ptr(), delta.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                                    dv.data_ptr(), dq_accum.data_ptr(), 0 if accum_zeroed else 1, B,

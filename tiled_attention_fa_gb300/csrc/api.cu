@@ -11,6 +11,9 @@ unsigned int g_last_site = 0;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Index arrays (tables, lengths) need their element's alignment only.
+bool ints_ok(const int* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 bool ptr_ok(const void* p) { return p != nullptr && aligned16(p); }
 
 // Lq query rows, Lk key rows (equal for the square entry points).
@@ -224,10 +227,105 @@ fa_status fa_decode_merge(const void* workspace, size_t workspace_bytes, void* O
                               static_cast<cudaStream_t>(stream));
 }
 
+namespace {
+// The pools and tables shared by every paged call.
+fa_status check_pool(int B, int Hkv, int D, int page, int max_pages, int num_pages,
+                     long long k_page_stride, long long v_page_stride, int dtype) {
+  if (B < 1 || Hkv < 1 || page < 1 || max_pages < 1 || num_pages < 1) return FA_ERR_INVALID_ARG;
+  if (B > (1 << 20) || Hkv > (1 << 20)) return FA_ERR_INVALID_ARG;
+  if (dtype != FA_F16 && dtype != FA_BF16) return FA_ERR_UNSUPPORTED;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  if (page != 16 && page != 32 && page != 64 && page != 128 && page != 256) return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_pages) * page > (1ll << 30)) return FA_ERR_INVALID_ARG;
+  const long long rows = static_cast<long long>(page) * Hkv * D;
+  for (long long st : {k_page_stride, v_page_stride})
+    if (st < rows || st % 8 != 0 || st >= (1ll << 38)) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+}  // namespace
+
+size_t fa_paged_decode_workspace_size(int B, int Lq, int H, int Hkv, int D, int page, int max_pages,
+                                      int weights) {
+  if (B < 1 || Lq < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || (D != 64 && D != 128) || page < 1 ||
+      max_pages < 1 || static_cast<long long>(H / Hkv) * Lq > 128)
+    return 0;
+  return fa::paged_decode_workspace_size(B, Lq, static_cast<long long>(max_pages) * page, H, Hkv, D,
+                                         weights != 0);
+}
+
+fa_status fa_paged_decode(const void* Q, const void* K, const void* V, long long k_page_stride,
+                          long long v_page_stride, const int* block_table, const int* lens, void* O,
+                          float* LSE, float* weights, long long weights_stride, void* workspace,
+                          size_t workspace_bytes, int B, int Lq, int H, int Hkv, int D, int page,
+                          int max_pages, int num_pages, int window, int sinks, int dtype,
+                          void* stream) {
+  fa_status st = check_shape(B, Lq, Lq, H, Hkv, D, dtype);
+  if (st != FA_OK) return st;
+  st = check_pool(B, Hkv, D, page, max_pages, num_pages, k_page_stride, v_page_stride, dtype);
+  if (st != FA_OK) return st;
+  if (window < 0 || sinks < 0) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(H / Hkv) * Lq > 128) return FA_ERR_UNSUPPORTED;
+  if (!ptr_ok(Q) || !ptr_ok(K) || !ptr_ok(V) || !ints_ok(block_table) || !ints_ok(lens) ||
+      !ptr_ok(O) || !ptr_ok(LSE) || !ptr_ok(workspace))
+    return FA_ERR_INVALID_ARG;
+  if (weights != nullptr &&
+      (!aligned16(weights) || weights_stride < static_cast<long long>(max_pages) * page))
+    return FA_ERR_INVALID_ARG;
+  fa::PagedDecodeArgs a;
+  a.Q = Q;
+  a.K = K;
+  a.V = V;
+  a.table = block_table;
+  a.lens = lens;
+  a.O = O;
+  a.LSE = LSE;
+  a.weights = weights;
+  a.weights_stride = weights_stride;
+  a.k_page_stride = k_page_stride;
+  a.v_page_stride = v_page_stride;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  a.B = B;
+  a.Lq = Lq;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.page = page;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  a.window = window;
+  a.sinks = sinks;
+  a.dtype = dtype;
+  return fa::run_paged_decode(a, static_cast<cudaStream_t>(stream));
+}
+
+fa_status fa_paged_write(const void* K, const void* V, void* K_pool, void* V_pool,
+                         long long k_page_stride, long long v_page_stride, const int* block_table,
+                         const int* start, const int* counts, float* weights,
+                         long long weights_stride, const float* new_weights, int B, int L, int Hkv,
+                         int D, int page, int max_pages, int num_pages, int dtype, void* stream) {
+  fa_status st = check_shape(B, L, L, Hkv, Hkv, D, dtype);
+  if (st != FA_OK) return st;
+  st = check_pool(B, Hkv, D, page, max_pages, num_pages, k_page_stride, v_page_stride, dtype);
+  if (st != FA_OK) return st;
+  if (!ptr_ok(K) || !ptr_ok(V) || !ptr_ok(K_pool) || !ptr_ok(V_pool) || !ints_ok(block_table) ||
+      !ints_ok(start))
+    return FA_ERR_INVALID_ARG;
+  if (counts != nullptr && !ints_ok(counts)) return FA_ERR_INVALID_ARG;
+  if (weights == nullptr && new_weights != nullptr) return FA_ERR_INVALID_ARG;
+  if (weights != nullptr &&
+      (!aligned16(weights) || !aligned16(new_weights) ||
+       weights_stride < static_cast<long long>(max_pages) * page))
+    return FA_ERR_INVALID_ARG;
+  return fa::run_paged_write(K, V, K_pool, V_pool, k_page_stride, v_page_stride, block_table, start,
+                             counts, weights, weights_stride, new_weights, B, L, Hkv, D, page,
+                             max_pages, num_pages, static_cast<cudaStream_t>(stream));
+}
+
 fa_status fa_check_device_error(void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned int words[3] = {fa::fwd_read_error(s), fa::bwd_read_error(s),
-                                 fa::decode_read_error(s)};
+  const unsigned int words[4] = {fa::fwd_read_error(s), fa::bwd_read_error(s),
+                                 fa::decode_read_error(s), fa::paged_read_error(s)};
   unsigned int site = 0;
   for (unsigned int w : words) {
     if (w == 0xFFFFFFFFu) return FA_ERR_CUDA;

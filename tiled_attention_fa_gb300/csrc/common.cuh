@@ -87,6 +87,22 @@ inline bool make_bshd_map_e4m3(CUtensorMap* map, const void* ptr, int B, int L, 
   return r == CUDA_SUCCESS;
 }
 
+// Packed-Q tensor map: dims {D, H, Lq, B}, box {64, g, Lq, 1}, so one load
+// brings a K/V head's g query heads for all Lq queries, row = query * g + head.
+inline bool make_group_map(CUtensorMap* map, const void* Q, int B, int Lq, int H, int g, int D, bool bf16) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)Lq, (cuuint64_t)B};
+  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2, (cuuint64_t)Lq * H * D * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)g, (cuuint32_t)Lq, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  4, const_cast<void*>(Q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 inline int sm_count() {
   int dev = 0, n = 0;
   cudaGetDevice(&dev);

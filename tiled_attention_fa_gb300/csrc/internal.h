@@ -58,6 +58,26 @@ fa_status run_decode_merge(const void* ws, size_t ws_bytes, void* O, float* LSE,
                            int Lk, int H, int Hkv, int D, int dtype, cudaStream_t s);
 unsigned int decode_read_error(cudaStream_t s);
 
+// Paged cache (paged.cu).
+struct PagedDecodeArgs {
+  const void *Q, *K, *V;
+  const int *table, *lens;
+  void* O;
+  float* LSE;
+  float* weights;
+  long long weights_stride, k_page_stride, v_page_stride;
+  void* workspace;
+  size_t workspace_bytes;
+  int B, Lq, H, Hkv, D, page, max_pages, num_pages, window, sinks, dtype;
+};
+size_t paged_decode_workspace_size(int B, int Lq, long long cap, int H, int Hkv, int D, bool weights);
+fa_status run_paged_decode(const PagedDecodeArgs& a, cudaStream_t s);
+fa_status run_paged_write(const void* K, const void* V, void* Kc, void* Vc, long long k_page,
+                          long long v_page, const int* table, const int* start, const int* counts,
+                          float* weights, long long wstride, const float* new_w, int B, int L,
+                          int Hkv, int D, int page, int max_pages, int num_pages, cudaStream_t s);
+unsigned int paged_read_error(cudaStream_t s);
+
 inline int padded_len(int L) { return (L + 127) / 128 * 128; }
 
 }  // namespace fa
