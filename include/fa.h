@@ -191,6 +191,48 @@ fa_status fa_paged_decode(const void* Q, const void* K_pool, const void* V_pool,
                           int window, int sinks, int dtype, void* stream);
 
 /*
+ * Key weights: how much attention each key of a prompt has received,
+ *   W[b, hkv, j] = sum over the heads h of the group and the queries i that
+ *                  see key j of exp(q_i . k_j / sqrt(D) - LSE[b, h, i]),
+ * the column sums of the softmax whose LSE a forward call left (fa_fwd,
+ * fa_fwd_kv, fa_window_fwd).  Q [B, Lq, H, D], K [B, Lk, Hkv, D], LSE
+ * [B, H, Lq], W [B, Hkv, Lk] fp32, written in full.  The mask is fa_fwd_kv's,
+ * or with window > 0 (causal calls only, FA_ERR_INVALID_ARG otherwise)
+ * fa_window_fwd's.  A query whose LSE is -inf adds nothing.  All sums are fp32
+ * in a fixed order: the result does not depend on timing.  `workspace`:
+ * fa_key_weights_workspace_size() bytes, asked with the device that runs the
+ * call current; no initialisation needed, not shared between calls that
+ * overlap on the GPU.
+ */
+size_t fa_key_weights_workspace_size(void);
+fa_status fa_key_weights(const void* Q, const void* K, const float* LSE, float* W, void* workspace,
+                         size_t workspace_bytes, int B, int Lq, int Lk, int H, int Hkv, int D,
+                         int causal, int window, int sinks, int dtype, void* stream);
+
+/*
+ * Cut the paged caches of a batch down to `keep` keys per sequence and K/V
+ * head by accumulated attention weight.  A sequence of n = lens[b] <= keep
+ * keys survives whole; of a longer one each head keeps its first `sinks` keys,
+ * its last `recent`, and of those between the keep - sinks - recent heaviest
+ * by `weights` (NaN counts as heaviest, ties go to the lower position);
+ * sinks + recent <= keep.  The survivors move, in their order, to positions
+ * 0, 1, ... of the pages in dst_table [B, dst_pages] (dst_pages * page >=
+ * keep) of the same pools.  The old pages and `weights` stay as they are, so
+ * pages that sequences share are safe; the pages of dst_table must be pages
+ * that no sequence of the call reads, each listed once.
+ * Written in full: kept [B, Hkv, keep] int32 (old positions, ascending; -1
+ * behind the last), new_lens [B] int32 = min(n, keep), new_weights
+ * [B, Hkv, dst_pages * page] fp32 (the survivors' weights, 0 behind them).
+ * No workspace.  B * Hkv <= 65535 (FA_ERR_UNSUPPORTED otherwise).
+ */
+fa_status fa_paged_evict(void* K_pool, void* V_pool, long long k_page_stride,
+                         long long v_page_stride, const int* block_table, const int* lens,
+                         const float* weights, long long weights_stride, const int* dst_table,
+                         int keep, int sinks, int recent, int* kept, int* new_lens,
+                         float* new_weights, int B, int Hkv, int D, int page, int max_pages,
+                         int dst_pages, int num_pages, int dtype, void* stream);
+
+/*
  * Backward preprocess: Delta[b, h, i] = sum_d O[b, i, h, d] * dO[b, i, h, d]
  * (fp32 accumulation), the per-row term of the softmax gradient.  Page
  * "TileLang与机器学习训练：反向传播算子优化案例", section 算子拆分与流水线设计

@@ -72,3 +72,27 @@ def test_paged_write(lib):
                dict(kst=2040), dict(L=0), dict(max_pages=0)):
         assert call(**kw) == INVALID, kw
     assert call(D=96, kst=1 << 20, vst=1 << 20) == UNSUPPORTED and call(page=17) == UNSUPPORTED
+
+
+def test_key_weights(lib):
+    names = "Q K LSE W ws ws_bytes B Lq Lk H Hkv D causal window sinks dtype".split()
+    call = caller(lib.fa_key_weights, names, [FAKE] * 5 + [1 << 30, 1, 50, 70, 4, 2, 64, 1, 0, 0, 0])
+    for kw in (dict(Q=None), dict(W=FAKE + 4), dict(ws=None), dict(Lk=49), dict(window=-1), dict(sinks=-1),
+               dict(window=5, causal=0), dict(H=3)):
+        assert call(**kw) == INVALID, kw
+    assert call(D=32) == UNSUPPORTED and call(dtype=9) == UNSUPPORTED
+    assert call(ws_bytes=0) == SMALL and lib.fa_key_weights_workspace_size() > 0
+
+
+def test_paged_evict(lib):
+    names = ("K V kst vst table lens w wst dst keep sinks recent kept new_lens nw B Hkv D page max_pages dst_pages "
+             "num_pages dtype").split()
+    call = caller(lib.fa_paged_evict, names,
+                  [FAKE, FAKE, 2048, 2048, FAKE, FAKE, FAKE, 160, FAKE + 64, 32, 4, 8, FAKE, FAKE, FAKE, 2, 2, 64, 16, 10,
+                   2, 30, 0])
+    for kw in (dict(K=None), dict(table=None), dict(w=None), dict(w=FAKE + 4), dict(wst=159), dict(dst=None),
+               dict(dst=FAKE), dict(keep=0), dict(keep=33), dict(sinks=-1), dict(recent=-1), dict(recent=29), dict(kept=None),
+               dict(new_lens=None), dict(nw=None), dict(dst_pages=0), dict(kst=2040)):
+        assert call(**kw) == INVALID, kw
+    assert call(D=32) == UNSUPPORTED and call(page=48, kst=1 << 20, vst=1 << 20) == UNSUPPORTED
+    assert call(B=1 << 15, Hkv=2) == UNSUPPORTED

@@ -25,8 +25,11 @@ from .api import (  # noqa: F401
     decode_workspace_size,
     fwd,
     fwd_fp8,
+    key_weights,
+    key_weights_workspace_size,
     paged_decode,
     paged_decode_workspace_size,
+    paged_evict,
     paged_write,
     window_attention_backward,
     window_bwd,
@@ -38,4 +41,5 @@ __all__ = ["fwd", "bwd_preprocess", "bwd", "attention_backward", "bwd_main", "bw
            "alloc_workspace", "check_device_error", "HostRunner", "HostPipeline", "decode", "decode_workspace_size",
            "decode_slices", "decode_merge", "alloc_decode_workspace", "DecodeHostRunner", "fwd_fp8", "Fp8HostRunner",
            "window_fwd", "window_bwd", "window_attention_backward",
-           "paged_write", "paged_decode", "paged_decode_workspace_size"]
+           "paged_write", "paged_decode", "paged_decode_workspace_size", "key_weights",
+           "key_weights_workspace_size", "paged_evict"]

@@ -45,6 +45,10 @@ _SIGS = {
     "fa_paged_decode_workspace_size": ([_i] * 8, ctypes.c_size_t),
     "fa_paged_decode": ([_vp] * 3 + [_ll, _ll] + [_vp] * 5 + [_ll, _vp, ctypes.c_size_t] + [_i] * 11
                         + [_vp], _i),
+    "fa_key_weights_workspace_size": ([], ctypes.c_size_t),
+    "fa_key_weights": ([_vp] * 5 + [ctypes.c_size_t] + [_i] * 10 + [_vp], _i),
+    "fa_paged_evict": ([_vp] * 2 + [_ll, _ll] + [_vp] * 3 + [_ll, _vp] + [_i] * 3 + [_vp] * 3
+                       + [_i] * 8 + [_vp], _i),
     "fa_check_device_error": ([_vp], _i),
     "fa_last_error_site": ([], ctypes.c_uint),
     "fa_selftest_bounded_wait": ([ctypes.c_ulonglong, _vp], _i),

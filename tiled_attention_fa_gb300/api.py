@@ -320,6 +320,78 @@ def paged_decode(q, k_cache, v_cache, block_table, lens, window: int = 0, sinks:
     return out, lse
 
 
+def paged_evict(k_cache, v_cache, block_table, lens, weights, dst_table, keep: int, sinks: int = 0,
+                recent: int = 0, kept=None, new_lens=None, new_weights=None, stream=None):
+    """Cut every sequence's paged keys and values down to ``keep`` per K/V
+    head: its first ``sinks``, its last ``recent`` and the heaviest others by
+    ``weights`` [B, Hkv, >= P * page] fp32 (ties to the lower position).  The
+    survivors move, in their order, into the pages of dst_table [B, P2] int32
+    (P2 * page >= keep), which no sequence of the call may read from; the old
+    pages stay as they are.
+    Returns kept [B, Hkv, keep] int32 (old positions, -1 behind the last),
+    new_lens [B] int32 = min(lens, keep) and new_weights [B, Hkv, P2 * page]
+    (zero behind the survivors)."""
+    num_pages, page, Hkv, D = _pools(k_cache, v_cache, k_cache.dtype)
+    B, P = block_table.shape
+    P2 = dst_table.shape[-1]
+    _need(block_table, "block_table", (B, P), torch.int32)
+    _need(lens, "lens", (B,), torch.int32)
+    _need(dst_table, "dst_table", (B, P2), torch.int32)
+    wstride = _row_stride(weights, "weights", B, Hkv, P * page)
+    if keep < 1:
+        raise ValueError("keep must be at least 1")
+    dev = k_cache.device
+    if kept is None:
+        kept = torch.empty(B, Hkv, keep, device=dev, dtype=torch.int32)
+    if new_lens is None:
+        new_lens = torch.empty(B, device=dev, dtype=torch.int32)
+    if new_weights is None:
+        new_weights = torch.empty(B, Hkv, P2 * page, device=dev, dtype=torch.float32)
+    _need(kept, "kept", (B, Hkv, keep), torch.int32)
+    _need(new_lens, "new_lens", (B,), torch.int32)
+    _need(new_weights, "new_weights", (B, Hkv, P2 * page), torch.float32)
+    _on_current_device(k_cache, v_cache, block_table, lens, weights, dst_table, kept, new_lens,
+                       new_weights)
+    st = _lib.load().fa_paged_evict(
+        k_cache.data_ptr(), v_cache.data_ptr(), _page_stride(k_cache), _page_stride(v_cache),
+        block_table.data_ptr(), lens.data_ptr(), weights.data_ptr(), wstride, dst_table.data_ptr(),
+        keep, sinks, recent, kept.data_ptr(), new_lens.data_ptr(), new_weights.data_ptr(), B, Hkv, D,
+        page, P, P2, num_pages, _dtype_code(k_cache), _stream(stream))
+    _lib.check("fa_paged_evict", st)
+    return kept, new_lens, new_weights
+
+
+def key_weights_workspace_size() -> int:
+    """Bytes of the workspace ``key_weights`` needs on the current device."""
+    return int(_lib.load().fa_key_weights_workspace_size())
+
+
+def key_weights(q, k, lse, causal: bool = False, window: int = 0, sinks: int = 0, out=None,
+                workspace=None, stream=None):
+    """The attention each key has received: W [B, Hkv, Lk] fp32, the sum over
+    the group's heads and the queries of exp(q . k / sqrt(D) - LSE), where
+    ``lse`` [B, H, Lq] is what ``fwd`` or (window > 0, causal) ``window_fwd``
+    gave for q [B, Lq, H, D] and k [B, Lk, Hkv, D] under the same mask.
+    ``workspace`` (a CUDA byte tensor of at least
+    ``key_weights_workspace_size`` bytes) is allocated when not given."""
+    B, L, H, D = q.shape
+    Lk, Hkv = k.shape[1], k.shape[2]
+    _need(q, "q")
+    _need(k, "k", (B, Lk, Hkv, D), q.dtype)
+    _need(lse, "lse", (B, H, L), torch.float32)
+    if out is None:
+        out = torch.empty(B, Hkv, Lk, device=q.device, dtype=torch.float32)
+    _need(out, "out", (B, Hkv, Lk), torch.float32)
+    _on_current_device(q, k, lse, out, workspace)
+    if workspace is None:
+        workspace = torch.empty(key_weights_workspace_size(), device=q.device, dtype=torch.uint8)
+    st = _lib.load().fa_key_weights(q.data_ptr(), k.data_ptr(), lse.data_ptr(), out.data_ptr(),
+                                    workspace.data_ptr(), _nbytes(workspace), B, L, Lk, H, Hkv, D,
+                                    int(bool(causal)), window, sinks, _dtype_code(q), _stream(stream))
+    _lib.check("fa_key_weights", st)
+    return out
+
+
 def workspace_size(B: int, L: int, H: int, D: int) -> int:
     """Bytes of the fp32 dQ accumulator the backward needs."""
     return int(_lib.load().fa_bwd_workspace_size(B, L, H, D))

@@ -322,10 +322,71 @@ fa_status fa_paged_write(const void* K, const void* V, void* K_pool, void* V_poo
                              max_pages, num_pages, static_cast<cudaStream_t>(stream));
 }
 
+fa_status fa_paged_evict(void* K_pool, void* V_pool, long long k_page_stride,
+                         long long v_page_stride, const int* block_table, const int* lens,
+                         const float* weights, long long weights_stride, const int* dst_table,
+                         int keep, int sinks, int recent, int* kept, int* new_lens,
+                         float* new_weights, int B, int Hkv, int D, int page, int max_pages,
+                         int dst_pages, int num_pages, int dtype, void* stream) {
+  fa_status st = check_pool(B, Hkv, D, page, max_pages, num_pages, k_page_stride, v_page_stride, dtype);
+  if (st != FA_OK) return st;
+  if (keep < 1 || sinks < 0 || recent < 0 || static_cast<long long>(sinks) + recent > keep)
+    return FA_ERR_INVALID_ARG;
+  if (dst_pages < 1 || static_cast<long long>(dst_pages) * page > (1ll << 30) ||
+      static_cast<long long>(dst_pages) * page < keep)
+    return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * Hkv > 65535) return FA_ERR_UNSUPPORTED;
+  if (!ptr_ok(K_pool) || !ptr_ok(V_pool) || !ints_ok(block_table) || !ints_ok(lens) ||
+      !ints_ok(dst_table) || !ints_ok(kept) || !ints_ok(new_lens) || !ptr_ok(weights) ||
+      !ptr_ok(new_weights) || dst_table == block_table)
+    return FA_ERR_INVALID_ARG;
+  if (weights_stride < static_cast<long long>(max_pages) * page) return FA_ERR_INVALID_ARG;
+  fa::PagedEvictArgs a;
+  a.K = K_pool;
+  a.V = V_pool;
+  a.table = block_table;
+  a.lens = lens;
+  a.dst_table = dst_table;
+  a.weights = weights;
+  a.kept = kept;
+  a.new_lens = new_lens;
+  a.new_weights = new_weights;
+  a.weights_stride = weights_stride;
+  a.k_page_stride = k_page_stride;
+  a.v_page_stride = v_page_stride;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.page = page;
+  a.max_pages = max_pages;
+  a.dst_pages = dst_pages;
+  a.num_pages = num_pages;
+  a.keep = keep;
+  a.sinks = sinks;
+  a.recent = recent;
+  return fa::run_paged_evict(a, static_cast<cudaStream_t>(stream));
+}
+
+size_t fa_key_weights_workspace_size(void) { return fa::key_weights_workspace_size(); }
+
+fa_status fa_key_weights(const void* Q, const void* K, const float* LSE, float* W, void* workspace,
+                         size_t workspace_bytes, int B, int Lq, int Lk, int H, int Hkv, int D,
+                         int causal, int window, int sinks, int dtype, void* stream) {
+  fa_status st = check_shape(B, Lq, Lk, H, Hkv, D, dtype);
+  if (st != FA_OK) return st;
+  if (causal && Lk < Lq) return FA_ERR_INVALID_ARG;
+  if (window < 0 || sinks < 0 || (window > 0 && !causal)) return FA_ERR_INVALID_ARG;
+  if (!ptr_ok(Q) || !ptr_ok(K) || !ptr_ok(LSE) || !ptr_ok(W) || !ptr_ok(workspace))
+    return FA_ERR_INVALID_ARG;
+  return fa::run_key_weights(Q, K, LSE, W, workspace, workspace_bytes, B, Lq, Lk, H, Hkv, D, causal,
+                             window, sinks, dtype, static_cast<cudaStream_t>(stream));
+}
+
 fa_status fa_check_device_error(void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned int words[4] = {fa::fwd_read_error(s), fa::bwd_read_error(s),
-                                 fa::decode_read_error(s), fa::paged_read_error(s)};
+  const unsigned int words[5] = {fa::fwd_read_error(s), fa::bwd_read_error(s),
+                                 fa::decode_read_error(s), fa::paged_read_error(s),
+                                 fa::weights_read_error(s)};
   unsigned int site = 0;
   for (unsigned int w : words) {
     if (w == 0xFFFFFFFFu) return FA_ERR_CUDA;

@@ -103,6 +103,22 @@ inline bool make_group_map(CUtensorMap* map, const void* Q, int B, int Lq, int H
   return r == CUDA_SUCCESS;
 }
 
+// Launch with the programmatic-dependency attribute: the kernel may be placed
+// while its predecessor still runs and waits for it with griddepcontrol.wait.
+template <typename... A, typename... P>
+inline bool launch_after(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...) == cudaSuccess;
+}
+
 inline int sm_count() {
   int dev = 0, n = 0;
   cudaGetDevice(&dev);

@@ -78,6 +78,25 @@ fa_status run_paged_write(const void* K, const void* V, void* Kc, void* Vc, long
                           int Hkv, int D, int page, int max_pages, int num_pages, cudaStream_t s);
 unsigned int paged_read_error(cudaStream_t s);
 
+// Eviction (evict.cu).
+struct PagedEvictArgs {
+  void *K, *V;
+  const int *table, *lens, *dst_table;
+  const float* weights;
+  int *kept, *new_lens;
+  float* new_weights;
+  long long weights_stride, k_page_stride, v_page_stride;
+  int B, Hkv, D, page, max_pages, dst_pages, num_pages, keep, sinks, recent;
+};
+fa_status run_paged_evict(const PagedEvictArgs& a, cudaStream_t s);
+
+// Key weights of a prompt (weights.cu).
+size_t key_weights_workspace_size();
+fa_status run_key_weights(const void* Q, const void* K, const float* LSE, float* W, void* ws,
+                          size_t ws_bytes, int B, int Lq, int Lk, int H, int Hkv, int D, int causal,
+                          int window, int sinks, int dtype, cudaStream_t s);
+unsigned int weights_read_error(cudaStream_t s);
+
 inline int padded_len(int L) { return (L + 127) / 128 * 128; }
 
 }  // namespace fa

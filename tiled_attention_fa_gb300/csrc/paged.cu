@@ -52,22 +52,6 @@ bool make_pool_map(CUtensorMap* map, const void* ptr, int pages, int page, int H
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Launch with the programmatic-dependency attribute: the kernel may be placed
-// while its predecessor still runs and waits for it with griddepcontrol.wait.
-template <typename... A, typename... P>
-bool launch_after(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...) == cudaSuccess;
-}
-
 template <int D, bool BF16, int R>
 fa_status launch_decode(const PagedDecodeArgs& a, PagedParams& p, int G, cudaStream_t s) {
   using Ly = PagedLayout<D, R>;

@@ -174,11 +174,6 @@ __device__ __forceinline__ float paged_rows_reduce(float (&x)[CW], uint32_t lane
   return v;
 }
 
-__device__ __forceinline__ void pdl_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Part of CTA blockIdx.x of the list of all tiles, computed by the whole CTA
 // (NT threads; sums: NT / 32 + 1 long longs, out: 4 ints of shared memory).
 // Returns the walk's start in `out` {b, hkv, k, n} and t0.

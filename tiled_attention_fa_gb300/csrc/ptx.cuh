@@ -408,6 +408,16 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// ------------------------------------------------------------------ dependent launches
+
+// Let the kernel launched after this one (with the programmatic-dependency
+// attribute) take its place on the SMs / wait for the kernels before this one
+// and see what they wrote.
+__device__ __forceinline__ void pdl_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------------------ misc
 
 // Fire-and-forget fp32 reduction of four consecutive floats into global memory.
