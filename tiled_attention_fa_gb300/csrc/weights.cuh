@@ -5,13 +5,21 @@
 //
 // The scores are recomputed transposed, S^T = K_j Q_i^T, so a thread owns a key
 // and adds up its row of exponentials; no maximum is needed, as LSE bounds
-// every exponent by 0.  Per 128 x 128 tile the tensor core takes about 64
-// cycles per 16 head dims and the exponential unit 512 (32 results per clock):
-// at D = 128 the two are level, and the kernel runs both at once.
-//   warps 0-3, 4-7  exponentials of the even / odd tiles (thread = key)
-//   warp  8         TMA producer: K_j per item (two slots), then Q_i with its
-//                   LSE through a ring of four
-//   warp  9         TMEM allocation and MMA issue, S^T in four TMEM buffers
+// every exponent by 0.  At D = 128 a 128 x 128 step costs the tensor core, the
+// exponential unit (32 results per clock) 512 cycles each and the shared memory
+// 768 (K_j and Q_i read by the MMAs, Q_i written); the kernel keeps all three
+// going at once.
+//   warps 0-15  exponentials: four groups of four warps, group w takes the
+//               steps w, w + 4, ... from TMEM buffer w (thread = key).  It takes
+//               four: a group spends as long on barriers and on its own next
+//               MMA as on exponentials
+//   warp  16    TMA producer: K_j per item (two slots), Q_i through a ring
+//   warp  17    TMEM allocation, MMA issue
+//   warp  18    -LSE * log2e of each step's 128 queries into shared memory; its
+//               arrival and the MMA's complete the same barrier
+// Each role walks item by item and counts its steps in a tight inner loop: with
+// one general step iterator (some 60 instructions a step, in warps that issue
+// one every few cycles) a step took 1180 cycles.
 // Work: an item is one (batch, K/V head, 128-key tile), its steps the group's
 // heads times the Q tiles that see it.  Under causal masking items differ by
 // the whole length, so the steps of all items form one list and CTA c takes
@@ -60,34 +68,43 @@ __host__ __device__ inline void kw_range(const KwParams& p, int j, int& i0, int&
   }
 }
 
+// Walk over the items of one part.  Step s of the item (s < n) is head
+// (off + s) / per of the group and Q tile i0 + (off + s) % per.
 struct KwWalk {
-  int bh, j, h, i, i0, i1;  // item (bh, j), head of the group, Q tile
-  int rem, item;
-  bool first;  // first step of the item in this part
+  int n;        // steps of this item in the part (0: the part is done)
+  int off;      // steps of the item before this part
+  int i0, per;  // Q tiles [i0, i0 + per)
+  int rem;      // steps of the part behind this item
+  int item;     // items of the part before this one
+  bool ends;    // the item's last step lies in this part
+  int bh, j;
 
-  __device__ __forceinline__ bool last(const KwParams& p) const {
-    return rem == 1 || (i + 1 == i1 && h + 1 == p.g);
+  __device__ __forceinline__ void enter(const KwParams& p, int from, int left) {
+    int i1;
+    kw_range(p, j, i0, i1);
+    per = i1 - i0;
+    off = from;
+    const int all = per * p.g - off;
+    n = min(all, left);
+    ends = all <= left;
+    rem = left - n;
   }
   __device__ __forceinline__ void next(const KwParams& p) {
-    --rem;
-    first = false;
-    if (++i < i1) return;
-    i = i0;
-    if (++h < p.g || rem <= 0) return;
-    h = 0;
-    first = true;
     ++item;
+    if (rem == 0) {
+      n = 0;
+      return;
+    }
     do {
       if (++j == p.n_kv) {
         j = 0;
         if (++bh >= p.B * p.Hkv) {
-          rem = 0;
+          n = 0;
           return;
         }
       }
-      kw_range(p, j, i0, i1);
-    } while (i0 >= i1);
-    i = i0;
+      enter(p, 0, rem);
+    } while (per == 0);
   }
 };
 
@@ -96,19 +113,20 @@ struct KwLayout {
   static constexpr int KCH = D / 64;
   static constexpr uint32_t CHUNK = 128u * 128u;
   static constexpr uint32_t TILE = KCH * CHUNK;
-  static constexpr int STAGES = 4, STATS = 8, COMB = 8;
+  static constexpr int STAGES = D == 64 ? 8 : 4, COMB = 16;
   static constexpr uint32_t K_OFF = 0;                       // two slots
   static constexpr uint32_t Q_OFF = 2 * TILE;                // STAGES tiles
-  static constexpr uint32_t STAT_OFF = Q_OFF + STAGES * TILE;  // [STATS][128] -LSE * log2e
-  static constexpr uint32_t COMB_OFF = STAT_OFF + STATS * 512u;  // [COMB][128] sums of warps 4-7
-  static constexpr uint32_t BAR_OFF = COMB_OFF + COMB * 512u;
+  static constexpr int NG = 4;                               // groups, S buffers
+  static constexpr uint32_t STAT_OFF = Q_OFF + STAGES * TILE;  // [NG][128] -LSE * log2e
+  static constexpr uint32_t COMB_OFF = STAT_OFF + NG * 512u;   // [COMB][NG - 1][128] sums
+  static constexpr uint32_t BAR_OFF = COMB_OFF + COMB * (NG - 1) * 512u;
   static constexpr int B_KFULL = 0, B_KEMPTY = 2, B_QFULL = 4, B_QEMPTY = B_QFULL + STAGES,
-                       B_SFULL = B_QEMPTY + STAGES, B_SEMPTY = B_SFULL + 4, B_CFULL = B_SEMPTY + 4,
+                       B_SFULL = B_QEMPTY + STAGES, B_SEMPTY = B_SFULL + NG, B_CFULL = B_SEMPTY + NG,
                        B_DONE = B_CFULL + COMB, NBAR = B_DONE + 1;
   static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
-  static constexpr uint32_t SMEM_USED = MISC_OFF + 160;
+  static constexpr uint32_t SMEM_USED = MISC_OFF + 192;
   static constexpr uint32_t SMEM_ALLOC = SMEM_USED + 1024;
-  static constexpr int NTHREADS = 320;
+  static constexpr int NTHREADS = 128 * NG + 96;
   static_assert(SMEM_ALLOC <= 232448, "shared memory");
 };
 
@@ -164,21 +182,16 @@ __device__ __forceinline__ void kw_plan(const KwParams& p, int c, int G, long lo
 
 __device__ __forceinline__ KwWalk kw_walk(const KwParams& p, const int* plan) {
   KwWalk w;
-  w.rem = plan[3];
   w.bh = plan[0];
   w.j = plan[1];
   w.item = 0;
-  w.first = true;
-  if (w.rem > 0) {
-    kw_range(p, w.j, w.i0, w.i1);
-    w.h = plan[2] / (w.i1 - w.i0);
-    w.i = w.i0 + plan[2] % (w.i1 - w.i0);
-  }
+  w.n = w.rem = 0;
+  if (plan[3] > 0) w.enter(p, plan[2], plan[3]);
   return w;
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(608, 1)
     fa_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ,
                           const __grid_constant__ CUtensorMap tmK, const KwParams p) {
   using Ly = KwLayout<D>;
@@ -208,16 +221,16 @@ __global__ void __launch_bounds__(320, 1)
       mbar_init(bar(Ly::B_QFULL + s), 1);
       mbar_init(bar(Ly::B_QEMPTY + s), 1);
     }
-    for (int s = 0; s < 4; ++s) {
-      mbar_init(bar(Ly::B_SFULL + s), 1);
+    for (int s = 0; s < Ly::NG; ++s) {
+      mbar_init(bar(Ly::B_SFULL + s), 2);  // the MMA and the LSE warp
       mbar_init(bar(Ly::B_SEMPTY + s), 4);
     }
-    for (int s = 0; s < Ly::COMB; ++s) mbar_init(bar(Ly::B_CFULL + s), 4);
+    for (int s = 0; s < Ly::COMB; ++s) mbar_init(bar(Ly::B_CFULL + s), 4 * (Ly::NG - 1));
     mbar_init(bar(Ly::B_DONE), 1);
     ab->flag = 0;
     fence_barrier_init();
   }
-  if (warp == 9) {
+  if (warp == 17) {
     tmem_alloc(base + Ly::MISC_OFF, 512);
     tmem_relinquish();
   }
@@ -226,88 +239,128 @@ __global__ void __launch_bounds__(320, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 8) {
+  KwWalk w = kw_walk(p, plan);
+  if (warp == 16) {
     // ------------------------------------------------------------ producer
     bool ok = true;
-    int i = 0;
-    uint32_t kcnt = 0;
-    KwWalk w = kw_walk(p, plan);
-    for (; w.rem > 0; ++i, w.next(p)) {
+    uint32_t stage = 0, phase = 0;
+    int done = 0;
+    for (; ok && w.n > 0; w.next(p)) {
       const int b = w.bh / p.Hkv, hkv = w.bh - b * p.Hkv;
-      if (w.first) {
-        const uint32_t slot = kcnt & 1, round = kcnt >> 1;
-        if (round > 0 && !mbar_wait_warp(bar(Ly::B_KEMPTY + slot), (round - 1) & 1, ab, err, 1101)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar(Ly::B_KFULL + slot), Ly::TILE);
-          for (int c = 0; c < Ly::KCH; ++c)
-            tma_load_4d(base + Ly::K_OFF + slot * Ly::TILE + c * Ly::CHUNK, &tmK,
-                        bar(Ly::B_KFULL + slot), c * 64, hkv, w.j * 128, b);
-        }
-        ++kcnt;
-      }
-      const uint32_t stage = i % Ly::STAGES, round = i / Ly::STAGES;
-      if (round > 0 && !mbar_wait_warp(bar(Ly::B_QEMPTY + stage), (round - 1) & 1, ab, err, 1102)) {
+      const uint32_t slot = w.item & 1;
+      if (w.item >= 2 && !mbar_wait_warp(bar(Ly::B_KEMPTY + slot), ((w.item >> 1) - 1) & 1, ab, err, 1101)) {
         ok = false;
         break;
       }
-      const int h = hkv * p.g + w.h;
-      // -LSE * log2e of the 128 queries; a query past the end, or one that
-      // sees nothing (LSE = -inf), gets -inf and adds nothing.  The slot's
-      // last readers, of step i - 8, are done: the MMA of step i - 4, whose
-      // completion freed this stage, wrote the S buffer they had emptied.
-      float* st = stats + (i % Ly::STATS) * 128;
-      const size_t row0 = (static_cast<size_t>(b) * p.H + h) * p.Lq;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int q = w.i * 128 + lane + 32 * u;
-        const float v = q < p.Lq ? p.LSE[row0 + q] : -INFINITY;
-        st[lane + 32 * u] = v == -INFINITY ? -INFINITY : -v * 1.4426950408889634f;
-      }
-      __syncwarp();
       if (lane == 0) {
-        mbar_arrive_expect_tx(bar(Ly::B_QFULL + stage), Ly::TILE);
+        mbar_arrive_expect_tx(bar(Ly::B_KFULL + slot), Ly::TILE);
         for (int c = 0; c < Ly::KCH; ++c)
-          tma_load_4d(base + Ly::Q_OFF + stage * Ly::TILE + c * Ly::CHUNK, &tmQ,
-                      bar(Ly::B_QFULL + stage), c * 64, h, w.i * 128, b);
+          tma_load_4d(base + Ly::K_OFF + slot * Ly::TILE + c * Ly::CHUNK, &tmK,
+                      bar(Ly::B_KFULL + slot), c * 64, hkv, w.j * 128, b);
+      }
+      int h = w.off / w.per, i = w.i0 + w.off - h * w.per;
+      h += hkv * p.g;
+      for (int s = 0; s < w.n; ++s) {
+        if (!mbar_wait_warp(bar(Ly::B_QEMPTY + stage), phase ^ 1u, ab, err, 1102)) { ok = false; break; }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(Ly::B_QFULL + stage), Ly::TILE);
+#pragma unroll
+          for (int c = 0; c < Ly::KCH; ++c)
+            tma_load_4d(base + Ly::Q_OFF + stage * Ly::TILE + c * Ly::CHUNK, &tmQ,
+                        bar(Ly::B_QFULL + stage), c * 64, h, i * 128, b);
+        }
+        ++done;
+        if (++stage == Ly::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (++i == w.i0 + w.per) {
+          i = w.i0;
+          ++h;
+        }
       }
     }
     if (!ok && lane == 0) {
-      for (uint32_t c = kcnt > 2 ? kcnt - 2 : 0; c < kcnt; ++c)
+      // Unwinding: let copies in flight land.
+      for (int c = w.item > 1 ? w.item - 1 : 0; c <= w.item; ++c)
         mbar_wait_drain(bar(Ly::B_KFULL + (c & 1)), (c >> 1) & 1);
-      for (int c = i > Ly::STAGES ? i - Ly::STAGES : 0; c < i; ++c)
+      for (int c = done > Ly::STAGES ? done - Ly::STAGES : 0; c < done; ++c)
         mbar_wait_drain(bar(Ly::B_QFULL + c % Ly::STAGES), (c / Ly::STAGES) & 1);
     }
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ------------------------------------------------------------ MMA issuer
     bool ok = true;
-    int i = 0;
-    for (KwWalk w = kw_walk(p, plan); w.rem > 0; ++i, w.next(p)) {
-      const uint32_t kslot = w.item & 1, stage = i % Ly::STAGES, buf = i & 3;
-      if (w.first && !mbar_wait_warp(bar(Ly::B_KFULL + kslot), (w.item >> 1) & 1, ab, err, 1103)) { ok = false; break; }
-      if (!mbar_wait_warp(bar(Ly::B_QFULL + stage), (i / Ly::STAGES) & 1, ab, err, 1104)) { ok = false; break; }
-      if (i >= 4 && !mbar_wait_warp(bar(Ly::B_SEMPTY + buf), ((i >> 2) - 1) & 1, ab, err, 1105)) { ok = false; break; }
-      tc_fence_after();
-      const uint64_t kd = sdesc_sw128(base + Ly::K_OFF + kslot * Ly::TILE, 16, 1024);
-      const uint64_t qd = sdesc_sw128(base + Ly::Q_OFF + stage * Ly::TILE, 16, 1024);
-      if (elect_one()) {
+    uint32_t stage = 0, phase = 0, buf = 0, use = 0;  // use: rounds of the S buffers
+    for (; ok && w.n > 0; w.next(p)) {
+      const uint32_t slot = w.item & 1;
+      if (!mbar_wait_warp(bar(Ly::B_KFULL + slot), (w.item >> 1) & 1, ab, err, 1103)) { ok = false; break; }
+      const uint64_t kd = sdesc_sw128(base + Ly::K_OFF + slot * Ly::TILE, 16, 1024);
+      for (int s = 0; s < w.n; ++s) {
+        if (!mbar_wait_warp(bar(Ly::B_QFULL + stage), phase, ab, err, 1104)) { ok = false; break; }
+        const uint64_t qd = sdesc_sw128(base + Ly::Q_OFF + stage * Ly::TILE, 16, 1024);
+        if (!mbar_wait_warp(bar(Ly::B_SEMPTY + buf), (use & 1) ^ 1u, ab, err, 1105)) { ok = false; break; }
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t off = ((k >> 2) * Ly::CHUNK + (k & 3) * 32u) >> 4;
-          mma_ss(tmem + 128 * buf, kd + off, qd + off, IDESC_S, k > 0 ? 1u : 0u);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = ((k >> 2) * Ly::CHUNK + (k & 3) * 32u) >> 4;
+            mma_ss(tmem + 128 * buf, kd + off, qd + off, IDESC_S, k > 0 ? 1u : 0u);
+          }
+          tc_commit(bar(Ly::B_SFULL + buf));
+          tc_commit(bar(Ly::B_QEMPTY + stage));
+          if (s + 1 == w.n) tc_commit(bar(Ly::B_KEMPTY + slot));
         }
-        tc_commit(bar(Ly::B_SFULL + buf));
-        tc_commit(bar(Ly::B_QEMPTY + stage));
-        if (w.last(p)) tc_commit(bar(Ly::B_KEMPTY + kslot));
+        __syncwarp();
+        if (++buf == Ly::NG) {
+          buf = 0;
+          ++use;
+        }
+        if (++stage == Ly::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      __syncwarp();
     }
-    (void)ok;
     if (elect_one()) tc_commit(bar(Ly::B_DONE));
     __syncwarp();
     mbar_wait_drain(bar(Ly::B_DONE), 0);
+  } else if (warp == 18) {
+    // ------------------------------------------------------------ LSE of the queries
+    // Read one step ahead.  A query past the end, or one that sees nothing
+    // (LSE = -inf), gets -inf and adds nothing.
+    bool ok = true;
+    uint32_t buf = 0, use = 0;
+    for (; ok && w.n > 0; w.next(p)) {
+      int h = w.off / w.per, i = w.i0 + w.off - h * w.per;
+      const float* row = p.LSE + (static_cast<size_t>(w.bh) * p.g + h) * p.Lq;
+      float next[4];
+      auto fetch = [&]() {
+        const int q0 = i * 128 + lane;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) next[u] = q0 + 32 * u < p.Lq ? row[q0 + 32 * u] : -INFINITY;
+        if (++i == w.i0 + w.per) {
+          i = w.i0;
+          row += p.Lq;
+        }
+      };
+      fetch();
+      for (int s = 0; s < w.n; ++s) {
+        float cur[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          cur[u] = next[u] == -INFINITY ? -INFINITY : -next[u] * 1.4426950408889634f;
+        if (s + 1 < w.n) fetch();
+        if (!mbar_wait_warp(bar(Ly::B_SEMPTY + buf), (use & 1) ^ 1u, ab, err, 1108)) { ok = false; break; }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) stats[buf * 128 + lane + 32 * u] = cur[u];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Ly::B_SFULL + buf));
+        if (++buf == Ly::NG) {
+          buf = 0;
+          ++use;
+        }
+      }
+    }
   } else {
     // ------------------------------------------------------------ exponentials and sums
     const int wg = warp >> 2, t = threadIdx.x & 127;
@@ -315,106 +368,115 @@ __global__ void __launch_bounds__(320, 1)
     const float sl2 = p.sl2;
     const uint64_t sl2x2 = f2_pack(sl2, sl2);
     bool ok = true;
-    int i = 0, first_open = 0, last_item = -1, last_slot = 0;
-    KwWalk w = kw_walk(p, plan);
-    const int total = w.rem;
-    bool starts = total > 0 && w.h == 0 && w.i == w.i0;  // the item's first step is in this part
-    float sum = 0.f;
-    for (; ok && w.rem > 0; ++i) {
-      if (w.first) {
-        sum = 0.f;
-        if (w.item > 0) starts = true;
-      }
-      const int buf = i & 3;
+    int first_open = 0, last_item = -1, last_slot = 0;
+    const uint32_t tS = tmem + lane_off + 128 * wg;
+    const float* st = stats + wg * 128;
+    uint32_t use = 0;
+    const int total = w.n + w.rem;
+    int skip = wg;  // steps until this group's next one
+    for (; ok && w.n > 0; w.next(p)) {
       const int key = w.j * 128 + t;
-      if ((i & 1) == wg) {
-        if (!mbar_wait_warp(bar(Ly::B_SFULL + buf), (i >> 2) & 1, ab, err, 1106)) { ok = false; break; }
+      float sum = 0.f;
+      const int d0 = key - p.past;
+      const bool windowed = p.window && key >= p.sinks;
+      int s = skip;
+      int i = w.i0 + (w.off + skip) % w.per;  // Q tile of step s
+      for (; s < w.n; s += Ly::NG) {
+        if (!mbar_wait_warp(bar(Ly::B_SFULL + wg), use & 1, ab, err, 1106)) { ok = false; break; }
+        ++use;
         tc_fence_after();
         // Query columns [lo, hi) see this key.
-        const int d = key - p.past - w.i * 128;
+        const int d = d0 - i * 128;
         int lo = 0, hi = 128;
         if (p.causal) lo = max(0, d);
-        if (p.window && key >= p.sinks) hi = min(hi, d + p.window);
-        const bool full = lo <= 0 && hi >= 128;
-        const float* st = stats + (i % Ly::STATS) * 128;
+        if (windowed) hi = min(hi, d + p.window);
         uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-        uint32_t sv[64];
-        auto chunk = [&](int c, const uint32_t* s, auto masked) {
+        uint32_t sv[32];
+        auto chunk = [&](int c, const uint32_t* x, auto masked) {
           const uint4* nl4 = reinterpret_cast<const uint4*>(st + c);
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
             const uint4 l4 = nl4[u];
             float a[4], e[4];
-            f2_unpack(ffma2(f2_pack(__uint_as_float(s[4 * u]), __uint_as_float(s[4 * u + 1])), sl2x2,
+            f2_unpack(ffma2(f2_pack(__uint_as_float(x[4 * u]), __uint_as_float(x[4 * u + 1])), sl2x2,
                             f2_pack(__uint_as_float(l4.x), __uint_as_float(l4.y))), a[0], a[1]);
-            f2_unpack(ffma2(f2_pack(__uint_as_float(s[4 * u + 2]), __uint_as_float(s[4 * u + 3])), sl2x2,
+            f2_unpack(ffma2(f2_pack(__uint_as_float(x[4 * u + 2]), __uint_as_float(x[4 * u + 3])), sl2x2,
                             f2_pack(__uint_as_float(l4.z), __uint_as_float(l4.w))), a[2], a[3]);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              e[x] = ex2(a[x]);
+            for (int y = 0; y < 4; ++y) {
+              e[y] = ex2(a[y]);
               if constexpr (decltype(masked)::value) {
-                const int q = c + 4 * u + x;
-                e[x] = (q >= lo && q < hi) ? e[x] : 0.f;
+                const int q = c + 4 * u + y;
+                e[y] = (q >= lo && q < hi) ? e[y] : 0.f;
               }
             }
             acc[2 * (u & 1)] = fadd2(acc[2 * (u & 1)], f2_pack(e[0], e[1]));
             acc[2 * (u & 1) + 1] = fadd2(acc[2 * (u & 1) + 1], f2_pack(e[2], e[3]));
           }
         };
-        const uint32_t tS = tmem + lane_off + 128 * buf;
-        // Two chunks of 32 columns in flight.
-        tmem_ld32(tS, sv);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld_wait32(sv + 32 * (c & 1));
-          if (c < 3) tmem_ld32(tS + 32 * (c + 1), sv + 32 * ((c + 1) & 1));
-          if (full)
-            chunk(32 * c, sv + 32 * (c & 1), std::false_type{});
-          else
-            chunk(32 * c, sv + 32 * (c & 1), std::true_type{});
+        // Not unrolled: four groups and two versions of the loop share the
+        // instruction cache.
+        if (__all_sync(0xffffffffu, lo <= 0 && hi >= 128)) {
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            tmem_ld32(tS + c, sv);
+            tmem_ld_wait32(sv);
+            chunk(c, sv, std::false_type{});
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            tmem_ld32(tS + c, sv);
+            tmem_ld_wait32(sv);
+            chunk(c, sv, std::true_type{});
+          }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(Ly::B_SEMPTY + buf));
+        if (lane == 0) mbar_arrive(bar(Ly::B_SEMPTY + wg));
         float x[8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) f2_unpack(acc[u], x[2 * u], x[2 * u + 1]);
+        for (int y = 0; y < 4; ++y) f2_unpack(acc[y], x[2 * y], x[2 * y + 1]);
         sum += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+        i += Ly::NG;
+        while (i >= w.i0 + w.per) i -= w.per;
       }
-      if (w.last(p)) {
-        // The item's end in this part: warps 4-7 hand their sums to warps 0-3.
-        // (A slot is used again eight items later; the four S buffers keep the
-        // two groups less than that apart.)
-        const int cs = w.item % Ly::COMB;
-        if (wg == 1) {
-          comb[cs * 128 + t] = sum;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(Ly::B_CFULL + cs));
+      if (!ok) break;
+      skip = s - w.n;
+      // The item's end in this part: groups 1-3 hand their sums to group 0.  A
+      // slot is used again 16 items, so at least 16 steps, later, and no group
+      // is that far ahead: group 0's next step is at most four past this item's
+      // end, the S buffers let the others finish three more, and walk over
+      // three that are not theirs.
+      const int cs = w.item % Ly::COMB;
+      float* cb = comb + cs * (Ly::NG - 1) * 128 + t;
+      if (wg != 0) {
+        cb[(wg - 1) * 128] = sum;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Ly::B_CFULL + cs));
+      } else {
+        if (!mbar_wait_warp(bar(Ly::B_CFULL + cs), (w.item / Ly::COMB) & 1, ab, err, 1107)) { ok = false; break; }
+        const float v = (sum + cb[0]) + (cb[128] + cb[256]);
+        const bool starts = w.off == 0;
+        if (starts && w.ends) {
+          if (key < p.Lk) p.W[static_cast<size_t>(w.bh) * p.Lk + key] = v;
         } else {
-          if (!mbar_wait_warp(bar(Ly::B_CFULL + cs), (w.item / Ly::COMB) & 1, ab, err, 1107)) { ok = false; break; }
-          const float v = sum + comb[cs * 128 + t];
-          const bool ends = w.i + 1 == w.i1 && w.h + 1 == p.g;
-          if (starts && ends) {
-            if (key < p.Lk) p.W[static_cast<size_t>(w.bh) * p.Lk + key] = v;
-          } else {
-            const int slot = 2 * blockIdx.x + (w.item > 0 ? 1 : 0);
-            p.part[static_cast<size_t>(slot) * 128 + t] = v;
-            if (w.item == 0 && !ends) first_open = 1;
-            if (starts) {
-              last_item = w.bh * p.n_kv + w.j;
-              last_slot = slot;
-            }
+          const int slot = 2 * blockIdx.x + (w.item > 0 ? 1 : 0);
+          p.part[static_cast<size_t>(slot) * 128 + t] = v;
+          if (w.item == 0 && !w.ends) first_open = 1;
+          if (starts) {
+            last_item = w.bh * p.n_kv + w.j;
+            last_slot = slot;
           }
         }
       }
-      w.next(p);
     }
     if (threadIdx.x == 0) p.meta[blockIdx.x] = KwMeta{ok ? total : 0, first_open, ok ? last_item : -1, last_slot};
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
