@@ -291,17 +291,24 @@ fa_status fa_bwd_kv(const void* Q, const void* K, const void* V, const void* O, 
  * itself, so no row is empty.  Work and reads grow with
  * Lq * (window + sinks), not with Lq * Lk.  K and V must be finite in every
  * position, as for fa_fwd: a hidden key's V is multiplied by a zero weight.
- * Everything else (layouts, dtypes, limits, the fp32 dQ accumulator, Delta
- * from fa_bwd_preprocess) is as for fa_fwd_kv and fa_bwd_kv; dK and dV of keys
- * that no query sees are zero.
+ * Everything else (layouts, dtypes, limits, Delta from fa_bwd_preprocess) is
+ * as for fa_fwd_kv and fa_bwd_kv; dK and dV of keys that no query sees are
+ * zero.  The backward's workspace holds fa_window_bwd_workspace_size bytes
+ * (FA_ERR_SCRATCH_TOO_SMALL when smaller): first the fp32 dQ accumulator of
+ * fa_bwd_workspace_size(B, Lq, H, D) bytes, which must hold zeros on entry
+ * (fa_bwd_preprocess sets them) unless zero_accum, then the parts of the sink
+ * keys' dK and dV, which need no initialisation.
  */
 fa_status fa_window_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE, int B,
                         int Lq, int Lk, int H, int Hkv, int D, int window, int sinks, int dtype,
                         void* stream);
+size_t fa_window_bwd_workspace_size(int B, int Lq, int Lk, int H, int Hkv, int D, int window,
+                                    int sinks);
 fa_status fa_window_bwd(const void* Q, const void* K, const void* V, const void* dO,
                         const float* LSE, const float* Delta, void* dQ, void* dK, void* dV,
-                        float* dq_accum, int zero_accum, int B, int Lq, int Lk, int H, int Hkv,
-                        int D, int window, int sinks, int dtype, void* stream);
+                        float* workspace, size_t workspace_bytes, int zero_accum, int B, int Lq,
+                        int Lk, int H, int Hkv, int D, int window, int sinks, int dtype,
+                        void* stream);
 
 /*
  * The two stages fa_bwd runs, for callers that schedule or time them apart:

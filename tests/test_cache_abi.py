@@ -33,14 +33,19 @@ INVALID, UNSUPPORTED, SMALL = _lib.FA_ERR_INVALID_ARG, _lib.FA_ERR_UNSUPPORTED, 
 def test_window(lib):
     fwd = caller(lib.fa_window_fwd, "Q K V O LSE B Lq Lk H Hkv D window sinks dtype".split(),
                  [FAKE] * 5 + [1, 100, 200, 4, 2, 64, 50, 4, 0])
-    bwd = caller(lib.fa_window_bwd, "Q K V dO LSE Delta dQ dK dV acc zero B Lq Lk H Hkv D window sinks dtype".split(),
-                 [FAKE] * 10 + [1, 1, 100, 200, 4, 2, 64, 50, 4, 0])
+    bwd = caller(lib.fa_window_bwd, "Q K V dO LSE Delta dQ dK dV acc bytes zero B Lq Lk H Hkv D window sinks dtype".split(),
+                 [FAKE] * 10 + [1 << 40, 1, 1, 100, 200, 4, 2, 64, 50, 4, 0])
     for call in (fwd, bwd):
         for kw in (dict(Q=None), dict(K=FAKE + 8), dict(LSE=None), dict(window=0), dict(sinks=-1), dict(Lk=99),
                    dict(H=3), dict(B=0)):
             assert call(**kw) == INVALID, kw
         assert call(D=96) == UNSUPPORTED and call(dtype=5) == UNSUPPORTED
     assert bwd(acc=None) == INVALID and bwd(dK=None) == INVALID
+    size = lib.fa_window_bwd_workspace_size
+    assert size(1, 100, 200, 4, 2, 64, 50, 0) == lib.fa_bwd_workspace_size(1, 100, 4, 64)
+    need = size(1, 1000, 1000, 4, 2, 64, 50, 4)
+    assert need > lib.fa_bwd_workspace_size(1, 1000, 4, 64) and bwd(Lq=1000, Lk=1000, bytes=need - 1) == SMALL
+    assert size(1, 100, 99, 4, 2, 64, 50, 0) == 0 and size(1, 100, 100, 4, 2, 64, 0, 0) == 0
 
 
 def test_paged_decode(lib):

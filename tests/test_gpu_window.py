@@ -124,7 +124,7 @@ def test_captured_and_replayed(cuda_lib):
     a, b = (make_qkv_kv(*args, seed, with_do=True) for seed in (1, 2))
     bufs = [x.cuda() for x in a]
     o, lse = fa.window_fwd(*bufs[:3], 100, 4)
-    acc = fa.alloc_workspace(2, 300, 4, 128, "cuda")
+    acc = fa.alloc_window_workspace(2, 300, 300, 4, 2, 128, 100, 4, "cuda")
     fa.window_attention_backward(*bufs[:3], o, lse, bufs[3], 100, 4, dq_accum=acc)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
@@ -167,5 +167,10 @@ def test_refusals(cuda_lib):
         fa.window_fwd(q, k[:, :4].contiguous(), v[:, :4].contiguous(), 4)    # more queries than keys
     with pytest.raises(ValueError):
         fa.window_fwd(q, k[:, :4], v, 4)
+    big = torch.zeros(1, 600, 2, 64, dtype=torch.float16, device="cuda")
+    lse = torch.zeros(1, 2, 600, device="cuda")
+    with pytest.raises(_lib.FAError) as e:                       # no room for the sink keys' parts
+        fa.window_bwd(big, big, big, big, lse, lse, 100, 4, dq_accum=fa.alloc_workspace(1, 600, 2, 64, "cuda"))
+    assert e.value.status == _lib.FA_ERR_SCRATCH_TOO_SMALL
     with pytest.raises(TypeError):
         fa.window_fwd(q.cpu(), k, v, 4)

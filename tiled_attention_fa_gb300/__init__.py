@@ -31,15 +31,18 @@ from .api import (  # noqa: F401
     paged_decode_workspace_size,
     paged_evict,
     paged_write,
+    alloc_window_workspace,
     window_attention_backward,
     window_bwd,
     window_fwd,
+    window_workspace_size,
     workspace_size,
 )
 
 __all__ = ["fwd", "bwd_preprocess", "bwd", "attention_backward", "bwd_main", "bwd_postprocess", "workspace_size",
            "alloc_workspace", "check_device_error", "HostRunner", "HostPipeline", "decode", "decode_workspace_size",
            "decode_slices", "decode_merge", "alloc_decode_workspace", "DecodeHostRunner", "fwd_fp8", "Fp8HostRunner",
-           "window_fwd", "window_bwd", "window_attention_backward",
+           "window_fwd", "window_bwd", "window_attention_backward", "window_workspace_size",
+           "alloc_window_workspace",
            "paged_write", "paged_decode", "paged_decode_workspace_size", "key_weights",
            "key_weights_workspace_size", "paged_evict"]

@@ -33,7 +33,8 @@ _SIGS = {
     "fa_bwd_workspace_size": ([_i, _i, _i, _i], ctypes.c_size_t),
     "fa_bwd": ([_vp] * 11 + [_i] * 8 + [_vp], _i),
     "fa_window_fwd": ([_vp] * 5 + [_i] * 9 + [_vp], _i),
-    "fa_window_bwd": ([_vp] * 10 + [_i] * 10 + [_vp], _i),
+    "fa_window_bwd_workspace_size": ([_i] * 8, ctypes.c_size_t),
+    "fa_window_bwd": ([_vp] * 10 + [ctypes.c_size_t] + [_i] * 10 + [_vp], _i),
     "fa_bwd_main": ([_vp] * 9 + [_i] * 8 + [_vp], _i),
     "fa_bwd_postprocess": ([_vp, _vp] + [_i] * 5 + [_vp], _i),
     "fa_bwd_noalloc": ([_vp] * 10 + [_i] * 7 + [_vp], _i),

@@ -465,9 +465,25 @@ def bwd(q, k, v, o, do, lse, delta, causal: bool = False, dq=None, dk=None, dv=N
     return dq, dk, dv
 
 
+def window_workspace_size(B: int, Lq: int, Lk: int, H: int, Hkv: int, D: int, window: int,
+                          sinks: int = 0) -> int:
+    """Bytes of the workspace ``window_bwd`` needs: the fp32 dQ accumulator and
+    the parts of the sink keys' gradients."""
+    return int(_lib.load().fa_window_bwd_workspace_size(B, Lq, Lk, H, Hkv, D, window, sinks))
+
+
+def alloc_window_workspace(B: int, Lq: int, Lk: int, H: int, Hkv: int, D: int, window: int, sinks: int,
+                           device) -> torch.Tensor:
+    n = window_workspace_size(B, Lq, Lk, H, Hkv, D, window, sinks) // 4
+    return torch.empty(max(n, 4), device=device, dtype=torch.float32)
+
+
 def window_bwd(q, k, v, do, lse, delta, window: int, sinks: int = 0, dq=None, dk=None, dv=None,
                dq_accum=None, accum_zeroed: bool = False, stream=None):
-    """dQ, dK, dV of ``window_fwd``; ``delta`` and ``dq_accum`` as for ``bwd``."""
+    """dQ, dK, dV of ``window_fwd``; ``delta`` as for ``bwd``.  ``dq_accum`` is
+    the fp32 workspace of ``window_workspace_size`` bytes; unless
+    ``accum_zeroed`` (fa_bwd_preprocess zeroed its accumulator) the call zeroes
+    that part first."""
     B, L, H, D = q.shape
     Lk, Hkv = k.shape[1], k.shape[2]
     _need(q, "q")
@@ -482,16 +498,14 @@ def window_bwd(q, k, v, do, lse, delta, window: int, sinks: int = 0, dq=None, dk
     _need(dk, "dk", k.shape, q.dtype)
     _need(dv, "dv", v.shape, q.dtype)
     if dq_accum is None:
-        dq_accum = alloc_workspace(B, L, H, D, q.device)
+        dq_accum = alloc_window_workspace(B, L, Lk, H, Hkv, D, window, sinks, q.device)
         accum_zeroed = False
     _need(dq_accum, "dq_accum", dtype=torch.float32)
-    if dq_accum.numel() * 4 < workspace_size(B, L, H, D):
-        raise ValueError("dq_accum is smaller than workspace_size()")
     _on_current_device(q, k, v, do, lse, delta, dq, dk, dv, dq_accum)
     st = _lib.load().fa_window_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), do.data_ptr(),
                                    lse.data_ptr(), delta.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-                                   dv.data_ptr(), dq_accum.data_ptr(), 0 if accum_zeroed else 1, B,
-                                   L, Lk, H, Hkv, D, window, sinks, _dtype_code(q),
+                                   dv.data_ptr(), dq_accum.data_ptr(), dq_accum.numel() * 4,
+                                   0 if accum_zeroed else 1, B, L, Lk, H, Hkv, D, window, sinks, _dtype_code(q),
                                    _stream(stream))
     _lib.check("fa_window_bwd", st)
     return dq, dk, dv
@@ -502,7 +516,7 @@ def window_attention_backward(q, k, v, o, lse, do, window: int, sinks: int = 0, 
     """``attention_backward`` for ``window_fwd``: preprocess + backward in one call."""
     B, L, H, D = q.shape
     if dq_accum is None:
-        dq_accum = alloc_workspace(B, L, H, D, q.device)
+        dq_accum = alloc_window_workspace(B, L, k.shape[1], H, k.shape[2], D, window, sinks, q.device)
     delta = bwd_preprocess(o, do, dq_accum=dq_accum, stream=stream)
     dq, dk, dv = window_bwd(q, k, v, do, lse, delta, window, sinks, dq_accum=dq_accum,
                             accum_zeroed=True, stream=stream)

@@ -132,18 +132,27 @@ fa_status fa_window_fwd(const void* Q, const void* K, const void* V, void* O, fl
                             static_cast<cudaStream_t>(stream));
 }
 
+size_t fa_window_bwd_workspace_size(int B, int Lq, int Lk, int H, int Hkv, int D, int window,
+                                    int sinks) {
+  if (check_shape(B, Lq, Lk, H, Hkv, D, FA_F16) != FA_OK || Lk < Lq || window < 1 || sinks < 0)
+    return 0;
+  return fa::window_bwd_workspace_size(B, Lq, Lk, H, Hkv, D, window, sinks);
+}
+
 fa_status fa_window_bwd(const void* Q, const void* K, const void* V, const void* dO,
                         const float* LSE, const float* Delta, void* dQ, void* dK, void* dV,
-                        float* dq_accum, int zero_accum, int B, int Lq, int Lk, int H, int Hkv,
-                        int D, int window, int sinks, int dtype, void* stream) {
+                        float* workspace, size_t workspace_bytes, int zero_accum, int B, int Lq,
+                        int Lk, int H, int Hkv, int D, int window, int sinks, int dtype,
+                        void* stream) {
   fa_status st = check_shape(B, Lq, Lk, H, Hkv, D, dtype);
   if (st != FA_OK) return st;
   if (Lk < Lq || window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
   if (!ptr_ok(Q) || !ptr_ok(K) || !ptr_ok(V) || !ptr_ok(dO) || !ptr_ok(LSE) || !ptr_ok(Delta) ||
-      !ptr_ok(dQ) || !ptr_ok(dK) || !ptr_ok(dV) || !ptr_ok(dq_accum))
+      !ptr_ok(dQ) || !ptr_ok(dK) || !ptr_ok(dV) || !ptr_ok(workspace))
     return FA_ERR_INVALID_ARG;
-  return fa::run_window_bwd(Q, K, V, dO, LSE, Delta, dQ, dK, dV, dq_accum, zero_accum, B, Lq, Lk, H,
-                            Hkv, D, window, sinks, dtype, static_cast<cudaStream_t>(stream));
+  return fa::run_window_bwd(Q, K, V, dO, LSE, Delta, dQ, dK, dV, workspace, workspace_bytes,
+                            zero_accum, B, Lq, Lk, H, Hkv, D, window, sinks, dtype,
+                            static_cast<cudaStream_t>(stream));
 }
 
 fa_status fa_bwd_main(const void* Q, const void* K, const void* V, const void* dO,

@@ -51,12 +51,57 @@ static double l2_bytes() {
   return n;
 }
 
+namespace {
+
+// The window's units (see BwdParams); p holds Lq, Lk, past, n_kv, n_q, Hkv.
+void plan_window(BwdParams& p, int B, int window, int sinks) {
+  p.window = window < p.Lk ? window : p.Lk;  // as good as every key when larger
+  p.sinks = sinks < p.Lk ? sinks : p.Lk;
+  p.n_sink = (p.sinks + 127) / 128;
+  p.srows = p.sinks < 128 ? p.sinks : 128;
+  p.chunk = (p.window + 254) / 128;  // Q tiles a window tile is seen by: equal units
+  int most = 0;
+  for (int j = 0; j < p.n_sink; ++j) {
+    int lo, reach;
+    bwd_win_range(p, j, lo, reach);
+    const int left = p.n_q - reach;
+    most = left > most ? left : most;
+  }
+  p.n_rest = (most + p.chunk - 1) / p.chunk;
+  p.n_items = B * p.Hkv * (p.n_kv + p.n_sink * p.n_rest);
+}
+
+size_t dq_bytes(int B, int L, int H, int D) {
+  return (static_cast<size_t>(B) * H * padded_len(L) * D * sizeof(float) + 255) / 256 * 256;
+}
+
+BwdParams window_plan(int B, int Lq, int Lk, int Hkv, int window, int sinks) {
+  BwdParams p = {};
+  p.Lq = Lq;
+  p.Lk = Lk;
+  p.past = Lk - Lq;
+  p.Hkv = Hkv;
+  p.n_kv = (Lk + 127) / 128;
+  p.n_q = (Lq + 127) / 128;
+  plan_window(p, B, window, sinks);
+  return p;
+}
+
+}  // namespace
+
+size_t window_bwd_workspace_size(int B, int Lq, int Lk, int H, int Hkv, int D, int window, int sinks) {
+  const BwdParams p = window_plan(B, Lq, Lk, Hkv, window, sinks);
+  const size_t slots = p.n_rest ? static_cast<size_t>(B) * Hkv * p.n_sink * (1 + p.n_rest) : 0;
+  return dq_bytes(B, Lq, H, D) + slots * 2 * p.srows * D * sizeof(float);
+}
+
 // window > 0 (WIN, causal calls only): the backward of run_window_fwd.
 template <int D, bool BF16, bool WIN = false>
 static fa_status launch_bwd(const void* Q, const void* K, const void* V, const void* dO,
                             const float* LSE, const float* Delta, void* dK, void* dV,
                             float* dq_accum, int zero_accum, int B, int Lq, int Lk, int H,
-                            int Hkv, int causal, cudaStream_t s, int window = 0, int sinks = 0) {
+                            int Hkv, int causal, cudaStream_t s, int window = 0, int sinks = 0,
+                            float* sink_part = nullptr) {
   using Ly = BwdLayout<D>;
   const int Lpad = padded_len(Lq);
   if (zero_accum &&
@@ -104,23 +149,11 @@ static fa_status launch_bwd(const void* Q, const void* K, const void* V, const v
       p.n_units = (p.n_items + sm - 1) / sm * sm;
     }
   }
-  p.window = window < Lk ? window : Lk;  // as good as every key when larger
-  p.sinks = sinks < Lk ? sinks : Lk;
-  p.n_long = p.cost_long = p.cost_win = 0;
   if (WIN) {
+    plan_window(p, B, window, sinks);
     p.ipu = 1;
-    p.n_long = B * Hkv * ((p.sinks + 127) / 128);
-    const int grid = p.n_items < sm_count() ? p.n_items : sm_count();
-    // Q tiles per K/V tile and query head; one tile per CTA when they are few.
-    const bool few = p.n_items <= grid;
-    p.cost_long = few ? 1 : p.n_q;
-    p.cost_win = few ? 1 : (p.n_q < (p.window + 254) / 128 ? p.n_q : (p.window + 254) / 128);
-    int most = 0;
-    for (int c = 0; c < grid; ++c) {
-      const int n = bwd_win_start(p, grid, c + 1) - bwd_win_start(p, grid, c);
-      most = n > most ? n : most;
-    }
-    p.n_units = most * grid;
+    p.n_units = p.n_items;
+    p.sink_part = sink_part;
   }
   p.scale = 1.f / sqrtf(static_cast<float>(D));
   p.sl2 = 1.4426950408889634f * p.scale;
@@ -181,24 +214,43 @@ fa_status run_bwd_main(const void* Q, const void* K, const void* V, const void* 
                                        Lq, Lk, H, Hkv, causal, s);
 }
 
+template <int D, bool BF16>
+static fa_status launch_window_bwd(const void* Q, const void* K, const void* V, const void* dO,
+                                   const float* LSE, const float* Delta, void* dQ, void* dK,
+                                   void* dV, float* ws, int zero_accum, int B, int Lq, int Lk,
+                                   int H, int Hkv, int window, int sinks, cudaStream_t s) {
+  BwdParams p = window_plan(B, Lq, Lk, Hkv, window, sinks);
+  p.dK = dK;
+  p.dV = dV;
+  p.scale = 1.f / sqrtf(static_cast<float>(D));
+  p.sink_part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + dq_bytes(B, Lq, H, D));
+  const fa_status st =
+      launch_bwd<D, BF16, true>(Q, K, V, dO, LSE, Delta, dK, dV, ws, zero_accum, B, Lq, Lk, H, Hkv,
+                                1, s, window, sinks, p.sink_part);
+  if (st != FA_OK) return st;
+  if (p.n_rest > 0 &&
+      !launch_after(fa_sink_sum_kernel<D, BF16>, dim3(B * Hkv * p.n_sink, (p.srows + 3) / 4),
+                    dim3(2 * D), s, p))
+    return FA_ERR_CUDA;
+  return launch_post<D, BF16>(ws, dQ, B, Lq, H, s);
+}
+
 fa_status run_window_bwd(const void* Q, const void* K, const void* V, const void* dO,
                          const float* LSE, const float* Delta, void* dQ, void* dK, void* dV,
-                         float* dq_accum, int zero_accum, int B, int Lq, int Lk, int H, int Hkv,
-                         int D, int window, int sinks, int dtype, cudaStream_t s) {
+                         float* ws, size_t ws_bytes, int zero_accum, int B, int Lq, int Lk, int H,
+                         int Hkv, int D, int window, int sinks, int dtype, cudaStream_t s) {
+  if (ws_bytes < window_bwd_workspace_size(B, Lq, Lk, H, Hkv, D, window, sinks))
+    return FA_ERR_SCRATCH_TOO_SMALL;
   const bool bf16 = dtype == FA_BF16;
-  fa_status st;
   if (D == 64)
-    st = bf16 ? launch_bwd<64, true, true>(Q, K, V, dO, LSE, Delta, dK, dV, dq_accum, zero_accum, B,
-                                           Lq, Lk, H, Hkv, 1, s, window, sinks)
-              : launch_bwd<64, false, true>(Q, K, V, dO, LSE, Delta, dK, dV, dq_accum, zero_accum,
-                                            B, Lq, Lk, H, Hkv, 1, s, window, sinks);
-  else
-    st = bf16 ? launch_bwd<128, true, true>(Q, K, V, dO, LSE, Delta, dK, dV, dq_accum, zero_accum,
-                                            B, Lq, Lk, H, Hkv, 1, s, window, sinks)
-              : launch_bwd<128, false, true>(Q, K, V, dO, LSE, Delta, dK, dV, dq_accum, zero_accum,
-                                             B, Lq, Lk, H, Hkv, 1, s, window, sinks);
-  if (st != FA_OK) return st;
-  return run_bwd_post(dq_accum, dQ, B, Lq, H, D, dtype, s);
+    return bf16 ? launch_window_bwd<64, true>(Q, K, V, dO, LSE, Delta, dQ, dK, dV, ws, zero_accum,
+                                              B, Lq, Lk, H, Hkv, window, sinks, s)
+                : launch_window_bwd<64, false>(Q, K, V, dO, LSE, Delta, dQ, dK, dV, ws, zero_accum,
+                                               B, Lq, Lk, H, Hkv, window, sinks, s);
+  return bf16 ? launch_window_bwd<128, true>(Q, K, V, dO, LSE, Delta, dQ, dK, dV, ws, zero_accum, B,
+                                             Lq, Lk, H, Hkv, window, sinks, s)
+              : launch_window_bwd<128, false>(Q, K, V, dO, LSE, Delta, dQ, dK, dV, ws, zero_accum,
+                                              B, Lq, Lk, H, Hkv, window, sinks, s);
 }
 
 fa_status run_bwd_post(const float* dq_accum, void* dQ, int B, int L, int H, int D, int dtype,

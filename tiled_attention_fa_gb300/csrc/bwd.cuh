@@ -89,10 +89,14 @@ struct BwdParams {
   float sl2;    // log2(e) / sqrt(D)
   float scale;  // 1 / sqrt(D)
   // WIN only: query position a sees key j iff j <= a and (j > a - window or
-  // j < sinks); n_long K/V tiles of all heads hold sink keys and cost cost_long
-  // Q tiles each, the others cost_win (see bwd_unit_item).
+  // j < sinks).  The n_sink K/V tiles of a head that hold sink keys are seen by
+  // every later query; the Q tiles past their windows form n_rest further units
+  // each, of `chunk` Q tiles, whose dK, dV of the sink keys (at most srows a
+  // tile) go to sink_part [B * Hkv, n_sink, 1 + n_rest, 2, srows, D] (slot 0:
+  // the tile's own unit) and are added up by fa_sink_sum_kernel.
   int window, sinks;
-  int n_long, cost_long, cost_win;
+  int n_sink, n_rest, chunk, srows;
+  float* sink_part;
 };
 
 template <int D>
@@ -163,12 +167,53 @@ struct BwdItem {
   int b, hkv, j;
   int i0;      // first Q tile visited
   int per;     // Q tiles visited per query head
+  int slot;    // WIN: sink_part slot of its sink keys, or -1
+  bool rest;   // WIN: a sink tile's Q tiles past its window
   int ntiles;  // (query heads of the group) x (Q tiles visited)
 };
+
+// Q tiles [lo, reach) whose windows touch K/V tile j (reach >= lo; no query may
+// see the tile at all).
+__host__ __device__ inline void bwd_win_range(const BwdParams& p, int j, int& lo, int& reach) {
+  const int d = j * 128 - p.past;
+  lo = d > 0 ? d / 128 : 0;
+  const int last = d + 126 + p.window;  // last query that sees a key of the tile
+  reach = last < 0 ? 0 : last / 128 + 1;
+  if (reach > p.n_q) reach = p.n_q;
+  if (reach < lo) reach = lo;
+}
 
 template <bool WIN>
 __device__ __forceinline__ BwdItem bwd_decode(int item, const BwdParams& p) {
   BwdItem it;
+  if constexpr (WIN) {
+    const int units = p.n_kv + p.n_sink * p.n_rest;  // of one (batch, K/V head)
+    const int bh = item / units;
+    int x = item - bh * units, r = 0;
+    it.rest = x >= p.n_kv;
+    if (it.rest) {
+      x -= p.n_kv;
+      r = x % p.n_rest;
+      x /= p.n_rest;
+    }
+    it.j = x;
+    it.b = bh / p.Hkv;
+    it.hkv = bh - it.b * p.Hkv;
+    int lo, reach;
+    bwd_win_range(p, it.j, lo, reach);
+    if (it.rest) {
+      it.i0 = reach + r * p.chunk;
+      it.per = max(0, min(p.chunk, p.n_q - it.i0));
+    } else {
+      it.i0 = lo;
+      it.per = reach - lo;
+    }
+    it.slot = (p.n_rest > 0 && it.j < p.n_sink)
+                  ? (bh * p.n_sink + it.j) * (1 + p.n_rest) + (it.rest ? 1 + r : 0)
+                  : -1;
+    it.ntiles = (p.H / p.Hkv) * it.per;
+    return it;
+  }
   it.j = item % p.n_kv;
   const int bh = item / p.n_kv;
   it.b = bh / p.Hkv;
@@ -176,27 +221,8 @@ __device__ __forceinline__ BwdItem bwd_decode(int item, const BwdParams& p) {
   // causal: the first Q tile holding a query that sees key j*128
   it.i0 = p.causal ? max(0, it.j * 128 - p.past) / 128 : 0;
   it.per = p.n_q - it.i0;
-  if constexpr (WIN) {
-    // A tile without sink keys is seen up to position j*128 + 127 + window - 1
-    // (by no query at all when that lies before the first one).
-    if (it.j * 128 >= p.sinks) {
-      const int last = it.j * 128 + 126 + p.window - p.past;  // last query that sees the tile
-      it.per = last < 0 ? 0 : max(0, min(p.n_q, last / 128 + 1) - it.i0);
-    }
-  }
   it.ntiles = (p.H / p.Hkv) * it.per;
   return it;
-}
-
-// WIN: start of CTA c's contiguous share of the K/V tiles (all heads' sink
-// tiles first, then the others head by head) when G CTAs split their total
-// cost evenly.
-__host__ __device__ inline int bwd_win_start(const BwdParams& p, int G, int c) {
-  const long long head = static_cast<long long>(p.n_long) * p.cost_long;
-  const long long all = head + static_cast<long long>(p.n_items - p.n_long) * p.cost_win;
-  const long long t = all * c / G;
-  return static_cast<int>(t < head ? (t + p.cost_long - 1) / p.cost_long
-                                   : p.n_long + (t - head + p.cost_win - 1) / p.cost_win);
 }
 
 // K/V tile s of work unit u of the persistent CTAs.  Under causal masking a
@@ -213,24 +239,13 @@ __host__ __device__ inline int bwd_win_start(const BwdParams& p, int G, int c) {
 // heads), round r of the CTAs takes the next gridDim.x of them, CTA c the c-th
 // in even rounds and the (gridDim.x-1-c)-th in odd ones.  The CTAs' loops
 // then run over rounds x gridDim.x units; positions past the tiles are empty.
-// With a window (WIN) every tile costs about the same except the tiles of the
-// sink keys, which every later query sees.  Those come first, then the others
-// head by head, and CTA c takes a contiguous share of the list that costs
-// 1/G of the whole (bwd_win_start): unit u is the (u / G)-th of CTA u % G.
+// With a window (WIN) every unit costs about the same; units are dealt out one
+// by one in the list's order, so the CTAs running together work on neighbouring
+// K/V tiles of a few heads and share their Q, dO and dQ tiles in L2.
 template <bool WIN>
 __device__ __forceinline__ bool bwd_unit_item(int u, int s, const BwdParams& p, int& item) {
   if constexpr (WIN) {
-    const int G = static_cast<int>(gridDim.x);
-    const int r = u / G, c = u - r * G;
-    int k = bwd_win_start(p, G, c) + r;
-    if (k >= bwd_win_start(p, G, c + 1)) return false;
-    const int per_head = p.n_long / (p.n_items / p.n_kv);  // sink tiles of one head
-    if (k < p.n_long) {
-      item = k / per_head * p.n_kv + k % per_head;
-    } else {
-      k -= p.n_long;
-      item = k / (p.n_kv - per_head) * p.n_kv + per_head + k % (p.n_kv - per_head);
-    }
+    item = u;
     return true;
   }
   if (p.snake) {
@@ -356,6 +371,7 @@ __global__ void __launch_bounds__(512, 1)
     int item;
     if (!bwd_unit_item<WIN>(u / p.ipu, u % p.ipu, p, item)) continue;
     const BwdItem it = bwd_decode<WIN>(item, p);
+    if (WIN && it.rest && it.ntiles == 0) continue;
     const int kvs = static_cast<int>(kv_cnt % Ly::KVS);
     const uint32_t kv_round = kv_cnt / Ly::KVS;
     if (kv_round > 0 &&
@@ -464,6 +480,7 @@ __global__ void __launch_bounds__(512, 1)
     int item;
     if (!bwd_unit_item<WIN>(u / p.ipu, u % p.ipu, p, item)) continue;
     const BwdItem it = bwd_decode<WIN>(item, p);
+    if (WIN && it.rest && it.ntiles == 0) continue;
     const int kvs = static_cast<int>(kv_cnt % Ly::KVS);
     if (!mbar_wait_warp(bar(Ly::B_KVFULL + kvs), (kv_cnt / Ly::KVS) & 1, ab, err, 501)) {
       ok = false;
@@ -600,6 +617,7 @@ __global__ void __launch_bounds__(512, 1)
     int item;
     if (!bwd_unit_item<WIN>(u / p.ipu, u % p.ipu, p, item)) continue;
     const BwdItem it = bwd_decode<WIN>(item, p);
+    if (WIN && it.rest && it.ntiles == 0) continue;
     const int kr = it.j * 128 + r;
     for (int n = 0; ok && n < it.ntiles; ++n, ++g) {
       int h, i;
@@ -720,6 +738,11 @@ __global__ void __launch_bounds__(512, 1)
       const uint32_t tsrc = tmem + lane_off + (hc == 0 ? Ly::TM_DK : Ly::TM_DV);
       T* row = reinterpret_cast<T*>(dst_base) +
                ((static_cast<size_t>(it.b) * p.Lk + kr) * p.Hkv + it.hkv) * D;
+      // WIN: sink keys' sums are joined over units, in fp32.
+      const bool joint = WIN && it.slot >= 0 && kr < p.sinks;
+      float* part = joint ? p.sink_part +
+                                ((static_cast<size_t>(it.slot) * 2 + hc) * p.srows + r) * D
+                          : nullptr;
 #pragma unroll
       for (int cc = 0; cc < D / 32; ++cc) {
         uint32_t o[32];
@@ -729,6 +752,14 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
           for (int u = 0; u < 32; ++u) o[u] = 0u;
         }
+        if (WIN && joint) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            reinterpret_cast<uint4*>(part + 32 * cc)[u] =
+                make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+          continue;
+        }
+        if (WIN && it.rest) continue;  // its other keys are their own unit's
         uint32_t pk[16];
 #pragma unroll
         for (int u = 0; u < 16; ++u)
@@ -755,6 +786,7 @@ __global__ void __launch_bounds__(512, 1)
     int item;
     if (!bwd_unit_item<WIN>(u / p.ipu, u % p.ipu, p, item)) continue;
     const BwdItem it = bwd_decode<WIN>(item, p);
+    if (WIN && it.rest && it.ntiles == 0) continue;
     for (int n = 0; n < it.ntiles; ++n, ++g) {
       int h, i;
       bwd_tile(it, p, n, h, i);
@@ -809,6 +841,31 @@ __global__ void __launch_bounds__(512, 1)
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, Ly::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------- sink keys
+// dK, dV of the sink keys: the sum of their units' fp32 parts, in the units'
+// order.  Block (bh, sink tile); thread = element of a row.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(2 * D) fa_sink_sum_kernel(const BwdParams p) {
+  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  pdl_wait();
+  const int j = blockIdx.x % p.n_sink, bh = blockIdx.x / p.n_sink;
+  const int b = bh / p.Hkv, hkv = bh - b * p.Hkv;
+  const int which = threadIdx.x / D, d = threadIdx.x - which * D;  // 0: dK, 1: dV
+  int lo, reach;
+  bwd_win_range(p, j, lo, reach);
+  const int units = 1 + (p.n_q - reach + p.chunk - 1) / p.chunk;  // its own, and the rest's
+  const size_t slot = static_cast<size_t>(2) * p.srows * D;
+  const float* src = p.sink_part + static_cast<size_t>(blockIdx.x) * (1 + p.n_rest) * slot +
+                     static_cast<size_t>(which) * p.srows * D + d;
+  T* dst = reinterpret_cast<T*>(which == 0 ? p.dK : p.dV) + hkv * D + d;
+  for (int r = blockIdx.y; r < min(128, p.sinks - j * 128); r += gridDim.y) {
+    float sum = 0.f;
+    for (int u = 0; u < units; ++u) sum += src[u * slot + static_cast<size_t>(r) * D];
+    dst[(static_cast<size_t>(b) * p.Lk + j * 128 + r) * p.Hkv * D] =
+        static_cast<T>(which == 0 ? sum * p.scale : sum);
   }
 }
 

@@ -32,8 +32,10 @@ fa_status run_bwd_post(const float* dq_accum, void* dQ, int B, int L, int H, int
                        cudaStream_t s);
 fa_status run_window_bwd(const void* Q, const void* K, const void* V, const void* dO,
                          const float* LSE, const float* Delta, void* dQ, void* dK, void* dV,
-                         float* dq_accum, int zero_accum, int B, int Lq, int Lk, int H, int Hkv,
-                         int D, int window, int sinks, int dtype, cudaStream_t s);
+                         float* ws, size_t ws_bytes, int zero_accum, int B, int Lq, int Lk, int H,
+                         int Hkv, int D, int window, int sinks, int dtype, cudaStream_t s);
+size_t window_bwd_workspace_size(int B, int Lq, int Lk, int H, int Hkv, int D, int window,
+                                 int sinks);
 unsigned int bwd_read_error(cudaStream_t s);
 fa_status run_bwd_noalloc(const void* Q, const void* K, const void* V, const void* dO,
                           const float* LSE, const float* Delta, void* dQ, void* dK, void* dV,
