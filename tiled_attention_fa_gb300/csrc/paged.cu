@@ -1,6 +1,9 @@
 // Host side of the paged cache: the decode launches (parts, join, weights)
 // and the write of new tokens.
+#include <atomic>
+#include <chrono>
 #include <cmath>
+#include <random>
 #include <type_traits>
 
 #include "common.cuh"
@@ -17,7 +20,7 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 int rows_class(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
 struct WsPlan {
-  size_t part_o, part_lse, scores, bytes;
+  size_t count, part_o, part_lse, scores, bytes;
 };
 
 WsPlan ws_plan(int B, int Lq, long long cap, int H, int Hkv, int D, bool weights, int sms) {
@@ -25,6 +28,8 @@ WsPlan ws_plan(int B, int Lq, long long cap, int H, int Hkv, int D, bool weights
   WsPlan w;
   if (sms < 1) sms = 1;
   size_t at = align256(sizeof(PagedMeta) * sms);
+  w.count = at;
+  at += align256(sizeof(unsigned long long) * sms);
   w.part_o = at;
   at += align256(2 * static_cast<size_t>(sms) * rows * D * sizeof(float));
   w.part_lse = at;
@@ -34,6 +39,20 @@ WsPlan ws_plan(int B, int Lq, long long cap, int H, int Hkv, int D, bool weights
     at += static_cast<size_t>(B) * Hkv * ((cap + 127) / 128) * rows * 128 * sizeof(float);
   w.bytes = at;
   return w;
+}
+
+// A number no other call of this process has, and no memory is likely to hold:
+// it marks the join's counters as this call's, so the workspace needs no
+// initialisation (48 bits, not 0).
+unsigned long long call_nonce() {
+  static std::atomic<unsigned long long> next{[] {
+    const unsigned long long t =
+        std::chrono::steady_clock::now().time_since_epoch().count() ^
+        (static_cast<unsigned long long>(std::random_device{}()) << 20);
+    return t * 0x9E3779B97F4A7C15ull;
+  }()};
+  const unsigned long long n = next.fetch_add(1) & 0xFFFFFFFFFFFFull;
+  return n ? n : next.fetch_add(1) & 0xFFFFFFFFFFFFull;
 }
 
 // K or V pool [pages, page, Hkv, D] with a free page stride, loaded as boxes
@@ -66,11 +85,10 @@ fa_status launch_decode(const PagedDecodeArgs& a, PagedParams& p, int G, cudaStr
     return FA_ERR_CUDA;
   kern<<<G, Ly::NTHREADS, Ly::SMEM_ALLOC, s>>>(tq, tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  if (!launch_after(fa_paged_join_kernel<D, BF16>, dim3(G), dim3(256), s, p, G)) return FA_ERR_CUDA;
   if (a.weights == nullptr) return FA_OK;
-  // Four blocks per part: the scores of a part lie together, and the adds of
-  // one key need no order.
-  return launch_after(fa_paged_weights_kernel, dim3(G, 4), dim3(128), s, p, a.weights,
+  // 16 blocks per part: the adds of one key need no order, and each block has
+  // one tile's reads in flight.
+  return launch_after(fa_paged_weights_kernel, dim3(G, 16), dim3(128), s, p, a.weights,
                       static_cast<long long>(a.weights_stride))
              ? FA_OK
              : FA_ERR_CUDA;
@@ -105,6 +123,8 @@ fa_status run_paged_decode(const PagedDecodeArgs& a, cudaStream_t s) {
   p.O = a.O;
   p.LSE = a.LSE;
   p.meta = reinterpret_cast<PagedMeta*>(ws);
+  p.count = reinterpret_cast<unsigned long long*>(ws + w.count);
+  p.nonce = call_nonce();
   p.part_o = reinterpret_cast<float*>(ws + w.part_o);
   p.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
   p.scores = a.weights != nullptr ? reinterpret_cast<float*>(ws + w.scores) : nullptr;
@@ -122,6 +142,7 @@ fa_status run_paged_decode(const PagedDecodeArgs& a, cudaStream_t s) {
   p.sl2 = 1.4426950408889634f / sqrtf(static_cast<float>(a.D));
   // One CTA per SM, fewer when even full sequences have fewer tiles.
   const long long most = static_cast<long long>(a.B) * a.Hkv * ((cap + 127) / 128);
+  if (most >= (1ll << 31) || sms >= 65536) return FA_ERR_UNSUPPORTED;
   const int G = most < sms ? static_cast<int>(most) : sms;
   const bool bf16 = a.dtype == FA_BF16;
   if (a.D == 64) return bf16 ? pick_rows<64, true>(a, p, G, s) : pick_rows<64, false>(a, p, G, s);

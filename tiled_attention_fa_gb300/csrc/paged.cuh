@@ -14,16 +14,25 @@
 //     the lengths are.  Lengths are read on the device: every CTA scans them
 //     once.  An item inside one CTA is written directly; only items cut by a
 //     part's border leave partials, at most two per CTA, so the workspace does
-//     not grow with the lengths.
-//   - one TMA ring of K and V tiles runs through the whole part, across items.
+//     not grow with the lengths.  The CTA that finishes last of an item's parts
+//     joins them (a counter per part tells it), so there is no second kernel.
+//   - one TMA ring of K and V tiles runs through the whole part, across items;
+//     page ids are read 32 at a time and a batch ahead, as one read per tile
+//     in the loader's way cost 700 cycles (of the 1440 that the K and V of a
+//     tile take to arrive at D = 64).
 //   - the products are transposed, S^T = K Q^T and O^T = V^T P^T: the 128 keys
 //     (or the head dims) fill the 128 rows of the MMA and the g * Lq packed
 //     query rows are its N, 16 at least.  A thread then owns one key and only
 //     as many scores as there are query rows, where Q K^T with the queries in
 //     128 padded rows makes every warp exponentiate 128 keys for a handful of
 //     live lanes.
-// Warps 0-3: softmax (thread = key of the tile), epilogue (thread = head dim);
-// warp 4: TMA producer; warp 5: TMEM allocation and MMA issue.
+//   - two groups of four softmax warps take the tiles in turn (up to 64 packed
+//     rows), each with a maximum, a sum and an O accumulator of its own that
+//     are joined at the item's end: a tile's chain from scores to P takes 1500
+//     cycles, as long as its K and V take to arrive at D = 64.
+// Warps 0-7 (0-3 for 128 rows): softmax (thread = key of the tile), epilogue
+// (thread = head dim); the next two warps: TMA producer; TMEM allocation and
+// MMA issue.
 // Row maxima are reduced over the 32 keys of a warp by a halving exchange
 // (lane r ends with row r), then over the four warps through shared memory;
 // a row's max moves only when it grew by more than 2^8 in exp2 units, as in
@@ -42,24 +51,21 @@
 
 namespace fa {
 
-// Meta record each CTA of the decode kernel leaves for the kernels after it.
+// What a CTA of the decode kernel leaves for the weights kernel: its part.
 struct PagedMeta {
-  long long t0;     // first tile of its part in the list of all tiles
-  int n;            // tiles in its part (0: nothing)
-  int b, hkv, k;    // first item and the first tile visited of it
-  int first_open;   // 1: the first item goes on in a later CTA
-  int last_bh;      // last item (b * Hkv + hkv) if it starts here and goes on later, else -1
-  int last_slot;    // its partial slot
-  int pad[7];
+  int t0, n;      // first tile of the part in the list of all tiles, and how many
+  int b, hkv, k;  // first item and the first tile visited of it
+  int pad[3];
 };
-static_assert(sizeof(PagedMeta) == 64, "one 64-byte record per CTA");
 
 struct PagedParams {
   const int* table;  // [B, max_pages]
   const int* lens;   // [B]
   void* O;           // [B, Lq, H, D]
   float* LSE;        // [B, H, Lq] natural log
-  PagedMeta* meta;   // [G]
+  PagedMeta* meta;   // [G], with scores
+  unsigned long long* count;  // [G] arrivals at the item that starts in part c and goes on:
+  unsigned long long nonce;   // nonce << 16 | arrivals, 0 again when all have come
   float* part_o;     // [2 G, rows, D]
   float* part_lse;   // [2 G, rows], log2 units
   float* scores;     // [tiles, rows, 128] raw scores for the weights, or NULL
@@ -76,48 +82,72 @@ struct PagedSeq {
   int ns, lo, cnt;
 };
 
-__device__ __forceinline__ PagedSeq paged_seq(int b, const PagedParams& p) {
+__device__ __forceinline__ PagedSeq paged_seq_of(int len, const PagedParams& p) {
   PagedSeq s;
-  s.n = min(max(p.lens[b], 0), p.cap);
+  s.n = min(max(len, 0), p.cap);
   s.wlo = p.window ? max(max(s.n - p.Lq, 0) - p.window + 1, 0) : 0;
   s.lo = s.wlo >> 7;
   s.ns = min((min(p.sinks, s.n) + 127) >> 7, s.lo);
   s.cnt = s.n > 0 ? s.ns + ((s.n + 127) >> 7) - s.lo : 0;
   return s;
 }
+__device__ __forceinline__ PagedSeq paged_seq(int b, const PagedParams& p) {
+  return paged_seq_of(p.lens[b], p);
+}
 
-// Walk over the tiles of one CTA's part.
+// Walk over the tiles of one CTA's part; a step costs a few instructions, an
+// item's start reads the length.
 struct PagedWalk {
-  int b, hkv, k;  // item and tile index within its list
+  int b, hkv, k;  // item, and tile's place in its list
+  int tile;       // the tile: keys [128 tile, 128 tile + 128)
+  int left;       // tiles of the item left in the part, this one included
   int rem;        // tiles left in the part, this one included
   int item;       // items begun before this one in the part
   bool first;     // first tile of its item in this part
   PagedSeq s;
 
-  __device__ __forceinline__ int tile() const { return k < s.ns ? k : s.lo + k - s.ns; }
-  __device__ __forceinline__ bool last() const { return rem == 1 || k + 1 == s.cnt; }
-  __device__ __forceinline__ void next(const PagedParams& p) {
-    --rem;
-    ++k;
+  __device__ __forceinline__ bool last() const { return left == 1; }
+  __device__ __forceinline__ void enter() {
+    tile = k < s.ns ? k : s.lo + k - s.ns;
+    left = min(s.cnt - k, rem);
+    first = true;
+  }
+  __device__ __forceinline__ void skip(const PagedParams& p, int n) {  // n <= left
+    rem -= n;
+    left -= n;
     first = false;
-    if (rem > 0 && k == s.cnt) {
+    if (left > 0) {
+      k += n;
+      tile = k < s.ns ? k : s.lo + k - s.ns;
+    } else if (rem > 0) {
       k = 0;
-      first = true;
       ++item;
       if (++hkv == p.Hkv) {
         hkv = 0;
         do {
-          ++b;
-          if (b >= p.B) {
+          if (++b >= p.B) {
             rem = 0;
             return;
           }
           s = paged_seq(b, p);
         } while (s.cnt == 0);
       }
+      enter();
     }
   }
+  __device__ __forceinline__ void next(const PagedParams& p) { skip(p, 1); }
 };
+
+// Part c of G of `total` tiles begins at tile:
+__device__ __forceinline__ int paged_part(int total, int G, int c) {
+  const int q = total / G, r = total - q * G;
+  return c * q + min(c, r);
+}
+// The part that holds tile t.
+__device__ __forceinline__ int paged_part_of(int total, int G, int t) {
+  const int q = total / G, r = total - q * G, big = r * (q + 1);
+  return t < big ? t / (q + 1) : r + (t - big) / q;
+}
 
 // R: query rows a thread processes (g * Lq rounded up); N: MMA columns.
 template <int D, int R>
@@ -129,18 +159,26 @@ struct PagedLayout {
   static constexpr uint32_t QCH = N * 128u;       // N rows x 64 columns
   static constexpr uint32_t QT = KCH * QCH;
   static constexpr uint32_t PT = 2 * QCH;         // N rows x 128 keys
+  static constexpr int NG = N <= 64 ? 2 : 1;      // softmax groups; K tiles loaded ahead of V
+  static constexpr int NB = 2 * NG;               // S buffers
+  static constexpr int PB = N <= 32 ? 4 : 2;      // P buffers
   static constexpr int QS = (D == 128 && N == 128) ? 1 : 2;
-  static constexpr int STAGES =
-      D == 128 ? (N == 16 ? 6 : N == 32 ? 5 : N == 64 ? 4 : 3) : (N <= 32 ? 12 : N == 64 ? 10 : 7);
+  static constexpr int STAGES = D == 128 ? (N == 16 ? 6 : N == 32 ? 5 : N == 64 ? 4 : 3)
+                                         : (N == 16 ? 12 : N <= 64 ? 10 : 7);
   static constexpr uint32_t RING_OFF = 0;
   static constexpr uint32_t Q_OFF = STAGES * TILE;
   static constexpr uint32_t P_OFF = Q_OFF + QS * QT;
-  static constexpr uint32_t ST_OFF = P_OFF + 2 * PT;  // wmax[2][4][N], mb[4][N], aux[4][N]
-  static constexpr uint32_t BAR_OFF = ST_OFF + 16u * N * 4u;
+  // fp32 exchange areas: per group wmax[2][4][N], mb[4][N], alpha[4][N]; then
+  // by item parity the groups' warps' row sums [2][4 NG][N] and maxima [2][NG][N]
+  static constexpr uint32_t ST_OFF = P_OFF + PB * PT;
+  static constexpr uint32_t SUM_OFF = ST_OFF + NG * 16u * N * 4u;
+  static constexpr uint32_t MAX_OFF = SUM_OFF + 8u * NG * N * 4u;
+  static constexpr uint32_t BAR_OFF = MAX_OFF + 2u * NG * N * 4u;
   static constexpr int B_QFULL = 0, B_QEMPTY = QS, B_KVFULL = 2 * QS, B_KVEMPTY = B_KVFULL + STAGES,
-                       B_SFULL = B_KVEMPTY + STAGES, B_PFULL = B_SFULL + 2, B_PVDONE = B_PFULL + 2,
+                       B_SFULL = B_KVEMPTY + STAGES, B_PFULL = B_SFULL + NB, B_PVDONE = B_PFULL + NB,
                        B_OFULL = B_PVDONE + 2, B_OEMPTY = B_OFULL + 2, B_XMAX = B_OEMPTY + 2,
-                       B_XSUM = B_XMAX + 1, B_DONE = B_XSUM + 1, NBAR = B_DONE + 1;
+                       B_XSUM = B_XMAX + NG, B_JOIN = B_XSUM + 2, B_DONE = B_JOIN + 2 * NG,
+                       NBAR = B_DONE + 1;
   static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;  // tmem slot, abort flag, plan
   static constexpr uint32_t USED = MISC_OFF + 128;
   // At D = 64 the PV product still takes 128 rows of V^T; rows 64-127 come
@@ -148,11 +186,13 @@ struct PagedLayout {
   // the last ring stage that much must still be shared memory of this CTA.
   static constexpr uint32_t SMEM_USED = (D == 64 && USED < Q_OFF + CHUNK) ? Q_OFF + CHUNK : USED;
   static constexpr uint32_t SMEM_ALLOC = SMEM_USED + 1024;
-  static constexpr uint32_t TM_S = 0, TM_O = 2 * N;
-  static constexpr uint32_t TMEM_COLS = 4 * N;
-  static constexpr int NTHREADS = 192;
+  static constexpr uint32_t TM_S = 0, TM_O = NB * N;  // O[item parity][group]
+  static constexpr uint32_t TMEM_COLS = (NB + 2 * NG) * N;
+  static constexpr int SW = 4 * NG;  // softmax warps; then the producer's and the issuer's
+  static constexpr int NTHREADS = 32 * SW + 64;
   static_assert(SMEM_ALLOC <= 232448, "shared memory");
-  static_assert(NBAR * 8 % 8 == 0 && BAR_OFF % 8 == 0 && ST_OFF % 16 == 0, "alignment");
+  static_assert(TMEM_COLS <= 512 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM");
+  static_assert(BAR_OFF % 8 == 0 && ST_OFF % 16 == 0, "alignment");
 };
 
 // Reduce x[i] (row i of CW) over the warp's lanes: lane r gets row r % CW.
@@ -174,50 +214,79 @@ __device__ __forceinline__ float paged_rows_reduce(float (&x)[CW], uint32_t lane
   return v;
 }
 
-// Part of CTA blockIdx.x of the list of all tiles, computed by the whole CTA
-// (NT threads; sums: NT / 32 + 1 long longs, out: 4 ints of shared memory).
-// Returns the walk's start in `out` {b, hkv, k, n} and t0.
+// Part c of G of the list of all tiles: the start and length of the walk in
+// `plan` {b, hkv, k, n}, t0 and the total in plan[4], plan[5].  Called by the
+// whole CTA (NT threads); `len` is lens[lane] for the small case, read early.
 template <int NT>
-__device__ __forceinline__ long long paged_plan(const PagedParams& p, int c, int G,
-                                                long long* sums, int* out) {
+__device__ __forceinline__ void paged_plan(const PagedParams& p, int c, int G, int len, int* sums,
+                                           int* plan) {
+  const uint32_t lane = lane_id();
+  if (p.B <= 32) {
+    // Every warp for itself is faster than once for all; warp 0 writes.
+    const int mine = static_cast<int>(lane) < p.B ? paged_seq_of(len, p).cnt * p.Hkv : 0;
+    int incl = mine;
+#pragma unroll
+    for (int h = 1; h < 32; h <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, h);
+      if (lane >= static_cast<uint32_t>(h)) incl += o;
+    }
+    const int total = __shfl_sync(0xffffffffu, incl, 31);
+    const int t0 = paged_part(total, G, c), n = paged_part(total, G, c + 1) - t0;
+    const int off = t0 - (incl - mine);
+    if (warp_id() == 0) {
+      if (n > 0 && off >= 0 && off < mine) {
+        const int cnt = mine / p.Hkv;
+        plan[0] = lane;
+        plan[1] = off / cnt;
+        plan[2] = off - off / cnt * cnt;
+      }
+      if (lane == 0) {
+        plan[3] = n;
+        plan[4] = t0;
+        plan[5] = total;
+      }
+    }
+    __syncthreads();
+    return;
+  }
   const int per = (p.B + NT - 1) / NT;
   const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += static_cast<long long>(paged_seq(b, p).cnt) * p.Hkv;
-  long long incl = mine;
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += paged_seq(b, p).cnt * p.Hkv;
+  int incl = mine;
 #pragma unroll
   for (int h = 1; h < 32; h <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, incl, h);
-    if (lane_id() >= static_cast<uint32_t>(h)) incl += o;
+    const int o = __shfl_up_sync(0xffffffffu, incl, h);
+    if (lane >= static_cast<uint32_t>(h)) incl += o;
   }
-  if (lane_id() == 31) sums[warp_id()] = incl;
-  if (threadIdx.x == 0) out[3] = 0;
+  if (lane == 31) sums[warp_id()] = incl;
   __syncthreads();
-  long long before = incl - mine, total = 0;
+  int before = incl - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
     if (w < static_cast<int>(warp_id())) before += sums[w];
     total += sums[w];
   }
-  const long long t0 = total * c / G, t1 = total * (c + 1) / G;
-  if (t1 > t0 && t0 >= before && t0 < before + mine) {
-    long long at = before;
+  const int t0 = paged_part(total, G, c), n = paged_part(total, G, c + 1) - t0;
+  if (threadIdx.x == 0) {
+    plan[3] = n;
+    plan[4] = t0;
+    plan[5] = total;
+  }
+  if (n > 0 && t0 >= before && t0 < before + mine) {
+    int at = before;
     for (int b = b0; b < b1; ++b) {
-      const int cnt = paged_seq(b, p).cnt;
-      const long long all = static_cast<long long>(cnt) * p.Hkv;
+      const int cnt = paged_seq(b, p).cnt, all = cnt * p.Hkv;
       if (t0 < at + all) {
-        const int off = static_cast<int>(t0 - at);
-        out[0] = b;
-        out[1] = off / cnt;
-        out[2] = off % cnt;
-        out[3] = static_cast<int>(t1 - t0);
+        plan[0] = b;
+        plan[1] = (t0 - at) / cnt;
+        plan[2] = (t0 - at) % cnt;
         break;
       }
       at += all;
     }
   }
   __syncthreads();
-  return t0;
 }
 
 __device__ __forceinline__ PagedWalk paged_walk(const PagedParams& p, const int* plan) {
@@ -227,13 +296,86 @@ __device__ __forceinline__ PagedWalk paged_walk(const PagedParams& p, const int*
   w.hkv = plan[1];
   w.k = plan[2];
   w.item = 0;
-  w.first = true;
-  if (w.rem > 0) w.s = paged_seq(w.b, p);
+  w.left = 0;
+  if (w.rem > 0) {
+    w.s = paged_seq(w.b, p);
+    w.enter();
+  }
   return w;
 }
 
+// Count an arrival at an item of n parts; true for the last one.  The word needs
+// no initialisation: whatever lies there without this call's nonce counts as
+// none, and the last arrival leaves 0, so a captured call can be replayed.
+__device__ __forceinline__ int paged_count_in(unsigned long long* word, unsigned long long nonce, int n) {
+  unsigned long long old = 0;  // as every call leaves it
+  for (;;) {  // ends: a failed swap means that another part counted itself in
+    const unsigned long long seen = (old >> 16) == nonce ? (old & 0xFFFFu) : 0ull;
+    const bool last = static_cast<int>(seen) + 1 == n;
+    const unsigned long long now = atomicCAS(word, old, last ? 0ull : (nonce << 16 | (seen + 1)));
+    if (now == old) return last;
+    old = now;
+  }
+}
+
+// The joined O and LSE of an item from `n` partials, in slots slot0, then
+// slot1, slot1 + 2, ...; 128 threads, thread = head dim (D = 64: the two halves
+// take alternate rows).  One pass with the running maximum, C partials of RB
+// rows read at a time: what it costs is the L2's latency, so as many reads as
+// the registers hold are under way at once.  Reads past L1: other SMs wrote them.
+template <int D, typename T>
+__device__ __forceinline__ void paged_join(const PagedParams& p, int b, int hkv, int slot0, int slot1,
+                                           int n) {
+  constexpr int HALVES = 128 / D;
+  constexpr int RB = 4, C = 8;
+  const int d = threadIdx.x % D, half = (threadIdx.x & 127) / D;
+  for (int r0 = half; r0 < p.rows; r0 += RB * HALVES) {
+    float mx[RB], den[RB], acc[RB];
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      mx[r] = -INFINITY;
+      den[r] = acc[r] = 0.f;
+    }
+    for (int q0 = 0; q0 < n; q0 += C) {
+      float ls[C][RB], o[C][RB];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const size_t slot = q0 + c == 0 ? slot0 : slot1 + 2 * (q0 + c - 1);
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+          const bool in = q0 + c < n && r0 + r * HALVES < p.rows;
+          const size_t at = slot * p.rows + r0 + r * HALVES;
+          ls[c][r] = in ? __ldcg(p.part_lse + at) : -INFINITY;
+          o[c][r] = in ? __ldcg(p.part_o + at * D + d) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+          const float m = fmaxf(mx[r], ls[c][r]);
+          const float old = m == -INFINITY ? 0.f : ex2(mx[r] - m), w = m == -INFINITY ? 0.f : ex2(ls[c][r] - m);
+          den[r] = fmaf(den[r], old, w);
+          acc[r] = fmaf(acc[r], old, w * o[c][r]);
+          mx[r] = m;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      const int row = r0 + r * HALVES;
+      if (row >= p.rows) break;
+      const int ql = row / p.g, h = hkv * p.g + row - ql * p.g;
+      reinterpret_cast<T*>(p.O)[((static_cast<size_t>(b) * p.Lq + ql) * p.H + h) * D + d] =
+          static_cast<T>(den[r] > 0.f ? acc[r] / den[r] : 0.f);
+      if (d == 0)
+        p.LSE[(static_cast<size_t>(b) * p.H + h) * p.Lq + ql] =
+            den[r] > 0.f ? (mx[r] + __log2f(den[r])) * 0.6931471805599453f : -INFINITY;
+    }
+  }
+}
+
 template <int D, bool BF16, int R>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
     fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ,
                            const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
@@ -252,13 +394,14 @@ __global__ void __launch_bounds__(192, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + Ly::MISC_OFF);
   AbortState* ab = reinterpret_cast<AbortState*>(gbase + Ly::MISC_OFF + 8);
   int* plan = reinterpret_cast<int*>(gbase + Ly::MISC_OFF + 16);
-  long long* sums = reinterpret_cast<long long*>(gbase + Ly::MISC_OFF + 32);
+  int* sums = reinterpret_cast<int*>(gbase + Ly::MISC_OFF + 48);
   unsigned int* err = device_error_word();
   const uint32_t warp = warp_id(), lane = lane_id();
 
+  const int len = (p.B <= 32 && static_cast<int>(lane) < p.B) ? p.lens[lane] : 0;
   pdl_launch_dependents();
   // Query rows past g * Lq, and P rows no thread writes, are zero.
-  for (uint32_t i = threadIdx.x; i < (Ly::QS * Ly::QT + 2 * Ly::PT) / 16u; i += Ly::NTHREADS)
+  for (uint32_t i = threadIdx.x; i < (Ly::QS * Ly::QT + Ly::PB * Ly::PT) / 16u; i += Ly::NTHREADS)
     reinterpret_cast<uint4*>(gbase + Ly::Q_OFF)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   if (threadIdx.x == 0) {
@@ -270,54 +413,79 @@ __global__ void __launch_bounds__(192, 1)
       mbar_init(bar(Ly::B_KVFULL + s), 1);
       mbar_init(bar(Ly::B_KVEMPTY + s), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < Ly::NB; ++i) {
       mbar_init(bar(Ly::B_SFULL + i), 1);
       mbar_init(bar(Ly::B_PFULL + i), 4);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar(Ly::B_PVDONE + i), 1);
       mbar_init(bar(Ly::B_OFULL + i), 1);
       mbar_init(bar(Ly::B_OEMPTY + i), 4);
     }
-    mbar_init(bar(Ly::B_XMAX), 4);
-    mbar_init(bar(Ly::B_XSUM), 4);
+    for (int i = 0; i < Ly::NG; ++i) mbar_init(bar(Ly::B_XMAX + i), 4);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(Ly::B_XSUM + i), Ly::SW);
+    for (int i = 0; i < Ly::NG; ++i) {
+      mbar_init(bar(Ly::B_JOIN + 2 * i), 4);
+      mbar_init(bar(Ly::B_JOIN + 2 * i + 1), 1);
+    }
     mbar_init(bar(Ly::B_DONE), 1);
     ab->flag = 0;
     fence_barrier_init();
   }
-  if (warp == 5) {
+  if (warp == Ly::SW + 1) {
     tmem_alloc(base + Ly::MISC_OFF, Ly::TMEM_COLS);
     tmem_relinquish();
   }
   tc_fence_before();
-  const long long t0 = paged_plan<Ly::NTHREADS>(p, blockIdx.x, gridDim.x, sums, plan);
+  paged_plan<Ly::NTHREADS>(p, blockIdx.x, gridDim.x, len, sums, plan);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 4) {
+  if (warp == Ly::SW) {
     // ------------------------------------------------------------ producer
-    // Ring order: K_0, then K_{i+1}, V_i per tile.  Lane j loads the j-th box
+    // Ring order: the first NG K tiles, then K_{i+NG}, V_i.  Lane j loads the j-th box
     // (a page, or 128 rows of one) of the tile.
-    const int box = min(p.page, 128), nbox = 128 / box;
+    const int box = min(p.page, 128), nbox = 128 / box, per_batch = 32 / nbox;
     uint32_t stage = 0, phase = 0, used = 0, qcnt = 0;
     bool ok = true;
     const uint64_t stream = policy_evict_first();
-    // Boxes that hold a key some query sees; the others are not loaded.
-    auto mine = [&](const PagedWalk& w) -> bool {
-      const int k0 = w.tile() * 128 + static_cast<int>(lane) * box;
-      return static_cast<int>(lane) < nbox && k0 < w.s.n && (k0 + box > w.s.wlo || k0 < p.sinks);
+    // Page ids of the next tiles, one box per lane: `cur` for the tiles from
+    // cur_tile on, `nxt` for the batch behind it (of the same item or the next).
+    PagedWalk ahead = paged_walk(p, plan);
+    int nxt = -1, nxt_n = 0, cur = -1, cur_at = 0, cur_n = 0;
+    auto fetch = [&]() {
+      nxt_n = 0;
+      if (ahead.rem <= 0) return;
+      nxt_n = min(per_batch, ahead.left);
+      if (ahead.k < ahead.s.ns) nxt_n = min(nxt_n, ahead.s.ns - ahead.k);  // up to the gap
+      const int at = (ahead.tile * 128 + static_cast<int>(lane) * box) / p.page;
+      nxt = (static_cast<int>(lane) < nxt_n * nbox && at < p.max_pages)
+                ? p.table[static_cast<size_t>(ahead.b) * p.max_pages + at]
+                : -1;
+      ahead.skip(p, nxt_n);
     };
-    auto page_of = [&](const PagedWalk& w) -> int {
-      const int k0 = w.tile() * 128 + static_cast<int>(lane) * box;
-      return mine(w) ? p.table[static_cast<size_t>(w.b) * p.max_pages + k0 / p.page] : -1;
+    // The page id of this lane's box of the next tile in order.
+    auto next_page = [&]() -> int {
+      if (cur_at == cur_n) {
+        cur = nxt;
+        cur_n = nxt_n;
+        cur_at = 0;
+        fetch();
+      }
+      return __shfl_sync(0xffffffffu, cur, (cur_at++ * nbox + static_cast<int>(lane)) & 31);
     };
     auto load = [&](const CUtensorMap* map, const PagedWalk& w, int pid) -> bool {
       if (!mbar_wait_warp(bar(Ly::B_KVEMPTY + stage), phase ^ 1u, ab, err, 1001)) return false;
-      const bool go = mine(w);
+      // Boxes that hold a key some query sees; the others are not loaded.
+      const int k0 = w.tile * 128 + static_cast<int>(lane) * box;
+      const bool go = static_cast<int>(lane) < nbox && k0 < w.s.n && (k0 + box > w.s.wlo || k0 < p.sinks);
       const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, go));
       if (lane == 0)
         mbar_arrive_expect_tx(bar(Ly::B_KVFULL + stage), boxes * box * static_cast<uint32_t>(D) * 2u);
       __syncwarp();
       if (go) {
-        const int row0 = (w.tile() * 128 + static_cast<int>(lane) * box) % p.page;
+        const int row0 = k0 & (p.page - 1);
+#pragma unroll
         for (int c = 0; c < Ly::KCH; ++c)
           tma_load_4d_hint(base + Ly::RING_OFF + stage * Ly::TILE + c * Ly::CHUNK + lane * box * 128u,
                            map, bar(Ly::B_KVFULL + stage), c * 64, w.hkv, row0, pid, stream);
@@ -342,20 +510,25 @@ __global__ void __launch_bounds__(192, 1)
       ++qcnt;
       return true;
     };
-    PagedWalk kw = paged_walk(p, plan), vw = kw;
+    PagedWalk kw = ahead, vw = ahead;
     if (kw.rem > 0) {
-      int pid_k = page_of(kw);
-      ok = load_q(kw) && load(&tmK, kw, pid_k);
+      fetch();
+      int pid[Ly::NG + 1];  // this lane's page of tiles i .. i + NG
+      auto load_k = [&](int x) -> bool {
+        if (kw.rem <= 0) return true;
+        pid[x] = next_page();
+        if (kw.first && !load_q(kw)) return false;
+        if (!load(&tmK, kw, pid[x])) return false;
+        kw.next(p);
+        return true;
+      };
+#pragma unroll
+      for (int x = 0; x < Ly::NG; ++x) ok = ok && load_k(x);
       while (ok && vw.rem > 0) {
-        const int pid_v = pid_k;
-        if (kw.rem > 1) {
-          kw.next(p);
-          pid_k = page_of(kw);
-          if (kw.first) ok = load_q(kw);
-          ok = ok && load(&tmK, kw, pid_k);
-        }
-        ok = ok && load(&tmV, vw, pid_v);
+        ok = load_k(Ly::NG) && load(&tmV, vw, pid[0]);
         vw.next(p);
+#pragma unroll
+        for (int x = 0; x < Ly::NG; ++x) pid[x] = pid[x + 1];
       }
       if (!ok && lane == 0) {
         // Unwinding: let copies in flight land.  The newest use of a stage
@@ -368,7 +541,7 @@ __global__ void __launch_bounds__(192, 1)
           mbar_wait_drain(bar(Ly::B_QFULL + c % Ly::QS), (c / Ly::QS) & 1);
       }
     }
-  } else if (warp == 5) {
+  } else if (warp == Ly::SW + 1) {
     // ------------------------------------------------------------ MMA issuer
     uint32_t stage = 0, phase = 0;
     bool ok = true;
@@ -400,9 +573,9 @@ __global__ void __launch_bounds__(192, 1)
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + Ly::TM_S + (i & 1) * N, kd + (((k >> 2) * Ly::CHUNK + (k & 3) * 32u) >> 4),
+          mma_ss(tmem + Ly::TM_S + (i % Ly::NB) * N, kd + (((k >> 2) * Ly::CHUNK + (k & 3) * 32u) >> 4),
                  qd + (((k >> 2) * Ly::QCH + (k & 3) * 32u) >> 4), IDESC_S, k > 0 ? 1u : 0u);
-        tc_commit(bar(Ly::B_SFULL + (i & 1)));
+        tc_commit(bar(Ly::B_SFULL + i % Ly::NB));
         tc_commit(bar(Ly::B_KVEMPTY + ks));
         if (sw.last()) tc_commit(bar(Ly::B_QEMPTY + qslot));
       }
@@ -410,12 +583,18 @@ __global__ void __launch_bounds__(192, 1)
       sw.next(p);
       return true;
     };
-    if (vw.rem > 0) ok = issue_s(0);
+    for (int x = 0; x < Ly::NG && sw.rem > 0; ++x)
+      if (!issue_s(x)) {
+        ok = false;
+        break;
+      }
+    int in_item = 0;  // tiles of vw's item before this one: a group's first has no O to add to
     for (int i = 0; ok && vw.rem > 0; ++i) {
-      const int buf = i & 1, ob = vw.item & 1;
-      // S(i+1) goes into the buffer tile i-1 left: its P is in shared memory
-      // and its scores were read before that P was handed over.
-      if (sw.rem > 0 && !issue_s(i + 1)) { ok = false; break; }
+      const int gr = i % Ly::NG, ob = vw.item & 1;
+      if (vw.first) in_item = 0;
+      // S(i+NG) goes into the buffer tile i-NG left, whose scores were read
+      // before its P was handed over.
+      if (sw.rem > 0 && !issue_s(i + Ly::NG)) { ok = false; break; }
       uint32_t vs;
       if (!take(vs, 1005)) { ok = false; break; }
       if (vw.first && vw.item >= 2 &&
@@ -423,55 +602,62 @@ __global__ void __launch_bounds__(192, 1)
         ok = false;
         break;
       }
-      if (!mbar_wait_warp(bar(Ly::B_PFULL + buf), (i >> 1) & 1, ab, err, 1007)) { ok = false; break; }
+      if (!mbar_wait_warp(bar(Ly::B_PFULL + i % Ly::NB), (i / Ly::NB) & 1, ab, err, 1007)) { ok = false; break; }
       tc_fence_after();
       const uint64_t vd = sdesc_sw128(base + Ly::RING_OFF + vs * Ly::TILE, Ly::CHUNK, 1024);
-      const uint64_t pd = sdesc_sw128(base + Ly::P_OFF + buf * Ly::PT, 16, 1024);
+      const uint64_t pd = sdesc_sw128(base + Ly::P_OFF + (i % Ly::PB) * Ly::PT, 16, 1024);
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          mma_ss(tmem + Ly::TM_O + ob * N, vd + ((2048u * k) >> 4),
+          mma_ss(tmem + Ly::TM_O + (ob * Ly::NG + gr) * N, vd + ((2048u * k) >> 4),
                  pd + (((k >> 2) * Ly::QCH + (k & 3) * 32u) >> 4), IDESC_PV,
-                 (!vw.first || k > 0) ? 1u : 0u);
-        tc_commit(bar(Ly::B_PVDONE + buf));
+                 (in_item >= Ly::NG || k > 0) ? 1u : 0u);
+        tc_commit(bar(Ly::B_PVDONE + (i & 1)));
         tc_commit(bar(Ly::B_KVEMPTY + vs));
         if (vw.last()) tc_commit(bar(Ly::B_OFULL + ob));
       }
       __syncwarp();
+      ++in_item;
       vw.next(p);
     }
     commit(Ly::B_DONE);
     mbar_wait_drain(bar(Ly::B_DONE), 0);
   } else {
     // ------------------------------------------------------------ softmax + epilogue
-    const int t = threadIdx.x;  // key of the tile; head dim of the epilogue
-    const uint32_t lane_off = (warp * 32u) << 16;
+    const int gr = warp >> 2, wq = warp & 3;  // group, warp of the group (its TMEM lanes)
+    const int t = threadIdx.x & 127;          // key of the tile; head dim of the epilogue
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const float sl2 = p.sl2;
-    float* wmax = reinterpret_cast<float*>(gbase + Ly::ST_OFF);  // [2][4][N]
-    float* mbuf = wmax + 8 * N + warp * N;                       // this warp's copy
-    float* aux = wmax + 12 * N;                                  // [4][N]
+    float* wmax = reinterpret_cast<float*>(gbase + Ly::ST_OFF) + gr * 16 * N;  // [2][4][N]
+    float* mbuf = wmax + 8 * N + wq * N;                                       // this warp's copy
+    float* al = wmax + 12 * N + wq * N;                                        // the same
+    float* sum_x = reinterpret_cast<float*>(gbase + Ly::SUM_OFF);  // [2][4 NG][N]
+    float* max_x = reinterpret_cast<float*>(gbase + Ly::MAX_OFF);  // [2][NG][N]
     const int row_l = lane & (CW - 1);                           // row of a chunk this lane keeps
-    float m[NCH], l[NCH];
-    uint32_t vpos = 0;  // position of the tile's V in the ring's sequence
-    uint32_t xsum = 0;
+    // Row sums: each thread its own keys' part per row, added up at the item's
+    // end; with more than 32 rows the registers do not reach and the lanes'
+    // parts are added up every tile (l[c]: row row_l of chunk c).
+    constexpr bool OWN_SUMS = R <= 32;
+    constexpr int NL = OWN_SUMS ? R : NCH;
+    float m[NCH], l[NL];
+    uint32_t joins = 0;
     bool ok = true;
     PagedWalk w = paged_walk(p, plan);
-    const int total = w.rem;
-    const int b0 = w.b, hkv0 = w.hkv, k0_first = w.k;
-    int first_open = 0, last_bh = -1, last_slot = 0;
-    int k_start = w.k;  // first tile of the current item in this part
-    for (int i = 0; ok && w.rem > 0; ++i) {
-      const int buf = i & 1;
-      vpos = w.rem > 1 ? 2u * i + 2u : 2u * i + 1u;
+    const int t0 = plan[4], total = plan[5], n_part = plan[3], G = gridDim.x;
+    int k_start = 0, in_item = 0;  // the item's first tile in this part; its tiles so far
+    for (int i = 0; ok && w.rem > 0; ++i, w.next(p)) {
       if (w.first) {
         k_start = w.k;
+        in_item = 0;
 #pragma unroll
-        for (int c = 0; c < NCH; ++c) {
-          m[c] = -INFINITY;
-          l[c] = 0.f;
-        }
+        for (int c = 0; c < NCH; ++c) m[c] = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < NL; ++r) l[r] = 0.f;
       }
-      if (!mbar_wait_warp(bar(Ly::B_SFULL + buf), (i >> 1) & 1, ab, err, 1008)) { ok = false; break; }
+      ++in_item;
+      if (i % Ly::NG == gr) {
+      const int buf = i % Ly::NB, pbuf = i % Ly::PB, gi = i / Ly::NG;  // gi: tiles of this group
+      if (!mbar_wait_warp(bar(Ly::B_SFULL + buf), (i / Ly::NB) & 1, ab, err, 1008)) { ok = false; break; }
       tc_fence_after();
       uint32_t sr[N];
       const uint32_t tS = tmem + lane_off + Ly::TM_S + buf * N;
@@ -484,7 +670,7 @@ __global__ void __launch_bounds__(192, 1)
 #pragma unroll
         for (int c = 0; c < N / 32; ++c) tmem_ld_wait32(sr + 32 * c);
       }
-      const int key0 = w.tile() * 128, key = key0 + t;
+      const int key0 = w.tile * 128, key = key0 + t;
       const int a0 = w.s.n - p.Lq;  // position of the first query
       const bool whole = key0 + 127 <= a0 && (p.window == 0 || key0 > w.s.n - 1 - p.window || key0 + 128 <= p.sinks);
       if (!whole) {
@@ -500,7 +686,7 @@ __global__ void __launch_bounds__(192, 1)
         }
       }
       if (p.scores != nullptr) {
-        float* dst = p.scores + (t0 + i) * static_cast<long long>(p.rows) * 128 + t;
+        float* dst = p.scores + static_cast<long long>(t0 + i) * p.rows * 128 + t;
 #pragma unroll
         for (int r = 0; r < R; ++r)
           if (r < p.rows) dst[r * 128] = __uint_as_float(sr[r]);
@@ -512,16 +698,16 @@ __global__ void __launch_bounds__(192, 1)
 #pragma unroll
         for (int r = 0; r < CW; ++r) x[r] = __uint_as_float(sr[c * CW + r]);
         const float v = paged_rows_reduce<CW, true>(x, lane);
-        if (lane < CW) wmax[(buf * 4 + warp) * N + c * CW + row_l] = v;
+        if (lane < CW) wmax[((gi & 1) * 4 + wq) * N + c * CW + row_l] = v;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(Ly::B_XMAX));
-      if (!mbar_wait_warp(bar(Ly::B_XMAX), i & 1, ab, err, 1009)) { ok = false; break; }
+      if (lane == 0) mbar_arrive(bar(Ly::B_XMAX + gr));
+      if (!mbar_wait_warp(bar(Ly::B_XMAX + gr), gi & 1, ab, err, 1009)) { ok = false; break; }
       bool grow = false;
       float alpha[NCH];
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
-        const float* wm = wmax + buf * 4 * N + c * CW + row_l;
+        const float* wm = wmax + (gi & 1) * 4 * N + c * CW + row_l;
         const float m_new = fmaxf(fmaxf(fmaxf(wm[0], wm[N]), fmaxf(wm[2 * N], wm[3 * N])), m[c]);
         alpha[c] = 1.f;
         if (m[c] == -INFINITY) {
@@ -533,21 +719,20 @@ __global__ void __launch_bounds__(192, 1)
         }
         if (lane < CW) {
           mbuf[c * CW + row_l] = m[c] == -INFINITY ? 0.f : m[c] * sl2;
-          aux[warp * N + c * CW + row_l] = alpha[c];
+          al[c * CW + row_l] = alpha[c];
         }
       }
       __syncwarp();
-      // The four warps see the same maxima, so they agree here.
+      // The group's four warps see the same maxima, so they agree here.
       if (__any_sync(0xffffffffu, grow)) {
-        // O^T holds the item's earlier tiles once PV(i-1) is done (the phase
-        // two tiles later needs this warp's P first).
-        if (!mbar_wait_warp(bar(Ly::B_PVDONE + (buf ^ 1)), ((i - 1) >> 1) & 1, ab, err, 1010)) {
+        // The group's O^T holds its earlier tiles of the item once PV(i-NG) is
+        // done (the next phase of that barrier needs this warp's P first).
+        if (!mbar_wait_warp(bar(Ly::B_PVDONE + ((i - Ly::NG) & 1)), ((i - Ly::NG) >> 1) & 1, ab, err, 1010)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t tO = tmem + lane_off + Ly::TM_O + (w.item & 1) * N;
-        const float* al = aux + warp * N;
+        const uint32_t tO = tmem + lane_off + Ly::TM_O + ((w.item & 1) * Ly::NG + gr) * N;
         constexpr int OC = N == 16 ? 16 : 32;
 #pragma unroll
         for (int c = 0; c < N / OC; ++c) {
@@ -568,10 +753,21 @@ __global__ void __launch_bounds__(192, 1)
             tmem_st32(tO + 32 * c, o);
         }
         tmem_st_wait();
+        if constexpr (OWN_SUMS) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) l[r] *= al[r];
+        }
       }
       // P = exp2(s c - m c), to shared memory in the 16-bit type (the MMA's
       // operand); the row sums take the unrounded values.
-      uint8_t* prow = gbase + Ly::P_OFF + buf * Ly::PT + (t >> 6) * Ly::QCH;
+      // (P's buffer: PV(i-PB) is done, as its S(i) was issued behind it; with two
+      // groups and two buffers it was issued before.)
+      if (Ly::PB == Ly::NG && i >= Ly::PB &&
+          !mbar_wait_warp(bar(Ly::B_PVDONE + (i & 1)), ((i - 2) >> 1) & 1, ab, err, 1016)) {
+        ok = false;
+        break;
+      }
+      uint8_t* prow = gbase + Ly::P_OFF + pbuf * Ly::PT + (t >> 6) * Ly::QCH;
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
         float x[CW];
@@ -581,10 +777,16 @@ __global__ void __launch_bounds__(192, 1)
           x[r] = ex2(fmaf(__uint_as_float(sr[rr]), sl2, -mbuf[rr]));
           *reinterpret_cast<T*>(prow + rr * 128 + (((t & 63) * 2) ^ ((rr & 7) << 4))) = static_cast<T>(x[r]);
         }
-        l[c] = l[c] * alpha[c] + paged_rows_reduce<CW, false>(x, lane);
+        if constexpr (OWN_SUMS) {
+#pragma unroll
+          for (int r = 0; r < CW; ++r) l[c * CW + r] += x[r];
+        } else {
+          l[c] = l[c] * alpha[c] + paged_rows_reduce<CW, false>(x, lane);
+        }
       }
       if (!whole) {
         // V rows of keys nobody sees: zero, whatever the page holds there.
+        const uint32_t vpos = min(n_part, i + 1 + Ly::NG) + i;  // V's place in the ring's order
         if (!mbar_wait_warp(bar(Ly::B_KVFULL + vpos % Ly::STAGES), (vpos / Ly::STAGES) & 1, ab, err, 1011)) {
           ok = false;
           break;
@@ -600,35 +802,58 @@ __global__ void __launch_bounds__(192, 1)
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(Ly::B_PFULL + buf));
+      if (lane == 0) mbar_arrive(bar(Ly::B_PFULL + buf));  // (a group may be two tiles ahead of the MMA)
+      }
 
       if (w.last()) {
-        // ---- the item's end in this part: O^T / l and LSE, or a partial
+        // ---- the item's end in this part: O^T / l and LSE, or a partial.  Both
+        // groups leave their row sums and maxima; the groups take turns at the
+        // rest, so the other goes on with the next item.  (It comes back to
+        // these areas two items later, after that item's exchange with this one.)
         const int ob = w.item & 1;
-        // Row sums of the four warps.
+        float* sx = sum_x + ob * 4 * Ly::NG * N;
+        float* mx = max_x + ob * Ly::NG * N;
 #pragma unroll
-        for (int c = 0; c < NCH; ++c)
-          if (lane < CW) aux[warp * N + c * CW + row_l] = l[c];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(Ly::B_XSUM));
-        if (!mbar_wait_warp(bar(Ly::B_XSUM), xsum & 1, ab, err, 1012)) { ok = false; break; }
-        ++xsum;
-        const bool starts = k_start == 0, ends = w.k + 1 == w.s.cnt;
-        const bool direct = starts && ends;
-        const int slot = 2 * blockIdx.x + (w.item > 0 ? 1 : 0);
-        if (w.item == 0 && !ends) first_open = 1;
-        if (starts && !ends) {
-          last_bh = w.b * p.Hkv + w.hkv;
-          last_slot = slot;
+        for (int c = 0; c < NCH; ++c) {
+          float v;
+          if constexpr (OWN_SUMS) {
+            float x[CW];
+#pragma unroll
+            for (int r = 0; r < CW; ++r) x[r] = l[c * CW + r];
+            v = paged_rows_reduce<CW, false>(x, lane);
+          } else {
+            v = l[c];
+          }
+          if (lane < CW) {
+            sx[warp * N + c * CW + row_l] = v;
+            if (wq == 0) mx[gr * N + c * CW + row_l] = m[c];
+          }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Ly::B_XSUM + ob));
+        if (Ly::NG == 2 && gr != ob) continue;
+        if (!mbar_wait_warp(bar(Ly::B_XSUM + ob), (w.item >> 1) & 1, ab, err, 1012)) { ok = false; break; }
+        const bool direct = k_start == 0 && w.k + 1 == w.s.cnt;
+        const int slot = 2 * blockIdx.x + (w.item > 0 ? 1 : 0);
+        // Factors of the groups' O^T rows: mbuf for group 0, al for group 1.
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
           const int rr = c * CW + row_l;
-          const float* ls = aux + rr;
-          const float sum = (ls[0] + ls[N]) + (ls[2 * N] + ls[3 * N]);
-          if (lane < CW) mbuf[rr] = sum > 0.f ? 1.f / sum : 0.f;
-          if (warp == 0 && lane < CW && rr < p.rows) {
-            const float lse2 = sum > 0.f ? m[c] * sl2 + __log2f(sum) : -INFINITY;
+          float top = mx[rr], f[Ly::NG], sum = 0.f;
+          if constexpr (Ly::NG == 2) top = fmaxf(top, mx[N + rr]);
+#pragma unroll
+          for (int x = 0; x < Ly::NG; ++x) {
+            const float* ls = sx + 4 * x * N + rr;
+            f[x] = mx[x * N + rr] == -INFINITY ? 0.f : ex2((mx[x * N + rr] - top) * sl2);
+            sum += f[x] * ((ls[0] + ls[N]) + (ls[2 * N] + ls[3 * N]));
+          }
+          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+          if (lane < CW) {
+            mbuf[rr] = f[0] * inv;
+            if constexpr (Ly::NG == 2) al[rr] = f[1] * inv;
+          }
+          if (wq == 0 && lane < CW && rr < p.rows) {
+            const float lse2 = sum > 0.f ? top * sl2 + __log2f(sum) : -INFINITY;
             if (direct)
               p.LSE[(static_cast<size_t>(w.b) * p.H + w.hkv * p.g + rr % p.g) * p.Lq + rr / p.g] =
                   lse2 * 0.6931471805599453f;
@@ -639,27 +864,28 @@ __global__ void __launch_bounds__(192, 1)
         __syncwarp();
         if (!mbar_wait_warp(bar(Ly::B_OFULL + ob), (w.item >> 1) & 1, ab, err, 1013)) { ok = false; break; }
         tc_fence_after();
+        // A group that had no tile of the item left nothing in its O.
+        const bool has[2] = {in_item >= 2 || i % Ly::NG == 0, in_item >= 2 || i % Ly::NG == 1};
         if (t < D) {
-          const uint32_t tO = tmem + lane_off + Ly::TM_O + ob * N;
+          const uint32_t tO = tmem + lane_off + Ly::TM_O + ob * Ly::NG * N;
           T* dst = reinterpret_cast<T*>(p.O) + (static_cast<size_t>(w.b) * p.Lq * p.H + w.hkv * p.g) * D + t;
           float* part = p.part_o + static_cast<size_t>(slot) * p.rows * D + t;
-          constexpr int OC = N == 16 ? 16 : 32;
+          constexpr int OC = 16;
           int hh = 0;
 #pragma unroll
           for (int c = 0; c < N / OC; ++c) {
-            uint32_t o[OC];
-            if constexpr (OC == 16) {
-              tmem_ld16(tO, o);
-              tmem_ld_wait16(o);
-            } else {
-              tmem_ld32(tO + 32 * c, o);
-              tmem_ld_wait32(o);
-            }
+            uint32_t o[Ly::NG][OC];
+#pragma unroll
+            for (int x = 0; x < Ly::NG; ++x) tmem_ld16(tO + x * N + OC * c, o[x]);
+#pragma unroll
+            for (int x = 0; x < Ly::NG; ++x) tmem_ld_wait16(o[x]);
 #pragma unroll
             for (int r = 0; r < OC; ++r) {
               const int rr = c * OC + r;
               if (rr < R && rr < p.rows) {
-                const float v = __uint_as_float(o[r]) * mbuf[rr];
+                float v = has[0] ? __uint_as_float(o[0][r]) * mbuf[rr] : 0.f;
+                if constexpr (Ly::NG == 2)
+                  if (has[1]) v = fmaf(__uint_as_float(o[1][r]), al[rr], v);
                 if (direct)
                   dst[static_cast<size_t>(hh) * D] = static_cast<T>(v);
                 else
@@ -675,87 +901,55 @@ __global__ void __launch_bounds__(192, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(Ly::B_OEMPTY + ob));
+        if (!direct) {
+          // ---- a partial: count it in; the CTA that comes last joins the item
+          const int start = t0 + i - w.k;  // the item's first tile
+          const int c0 = paged_part_of(total, G, start);
+          const int c1 = paged_part_of(total, G, start + w.s.cnt - 1);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(Ly::B_JOIN + 2 * gr));
+          if (!mbar_wait_warp(bar(Ly::B_JOIN + 2 * gr), joins & 1, ab, err, 1014)) { ok = false; break; }
+          int* flag = plan + 6 + gr;
+          if (t == 0) {
+            __threadfence();  // the group's partial, before the count
+            *flag = paged_count_in(p.count + c0, p.nonce, c1 - c0 + 1);
+            __threadfence();  // the count, before the others' partials
+            mbar_arrive(bar(Ly::B_JOIN + 2 * gr + 1));
+          }
+          if (!mbar_wait_warp(bar(Ly::B_JOIN + 2 * gr + 1), joins & 1, ab, err, 1015)) { ok = false; break; }
+          ++joins;
+          if (*flag) {
+            const int slot0 = 2 * c0 + (start > paged_part(total, G, c0) ? 1 : 0);
+            paged_join<D, T>(p, w.b, w.hkv, slot0, 2 * (c0 + 1), c1 - c0 + 1);
+          }
+        }
       }
-      w.next(p);
     }
-    if (t == 0) {
+    // Empty sequences: O = 0, LSE = -inf.
+    for (int b = blockIdx.x; gr == 0 && b < p.B; b += G) {
+      if (p.lens[b] > 0) continue;
+      T* dst = reinterpret_cast<T*>(p.O) + static_cast<size_t>(b) * p.Lq * p.H * D;
+      for (int x = t; x < p.Lq * p.H * D; x += 128) dst[x] = static_cast<T>(0.f);
+      for (int x = t; x < p.Lq * p.H; x += 128)
+        p.LSE[static_cast<size_t>(b) * p.Lq * p.H + x] = -INFINITY;
+    }
+    if (threadIdx.x == 0 && p.scores != nullptr) {
       PagedMeta mt;
       mt.t0 = t0;
-      mt.n = ok ? total : 0;
-      mt.b = b0;
-      mt.hkv = hkv0;
-      mt.k = k0_first;
-      mt.first_open = first_open;
-      mt.last_bh = ok ? last_bh : -1;
-      mt.last_slot = last_slot;
+      mt.n = ok ? plan[3] : 0;
+      mt.b = plan[0];
+      mt.hkv = plan[1];
+      mt.k = plan[2];
       p.meta[blockIdx.x] = mt;
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == Ly::SW + 1) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, Ly::TMEM_COLS);
-  }
-}
-
-// Join the partials of the items that the parts' borders cut: block c joins
-// the item that starts in part c and goes on in the next ones.  It also writes
-// O = 0, LSE = -inf of the empty sequences c, c + G, ....
-template <int D, bool BF16>
-__global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p, int G) {
-  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  pdl_launch_dependents();
-  pdl_wait();
-  const int c = blockIdx.x, lane = lane_id();
-  for (int b = c; b < p.B; b += G) {
-    if (p.lens[b] > 0 && p.cap > 0) continue;
-    T* dst = reinterpret_cast<T*>(p.O) + static_cast<size_t>(b) * p.Lq * p.H * D;
-    for (int i = threadIdx.x; i < p.Lq * p.H * D; i += blockDim.x) dst[i] = static_cast<T>(0.f);
-    for (int i = threadIdx.x; i < p.Lq * p.H; i += blockDim.x)
-      p.LSE[static_cast<size_t>(b) * p.Lq * p.H + i] = -INFINITY;
-  }
-  const PagedMeta mt = p.meta[c];
-  if (mt.n == 0 || mt.last_bh < 0) return;
-  __shared__ int last_part;
-  if (threadIdx.x == 0) {
-    // The parts the item goes through: c, then the first items of the next
-    // non-empty parts up to the one it ends in.
-    int e = c + 1;
-    while (e < G && (p.meta[e].n == 0 || p.meta[e].first_open)) ++e;
-    last_part = e < G ? e : G - 1;
-  }
-  __syncthreads();
-  const int e = last_part;
-  const int b = mt.last_bh / p.Hkv, hkv = mt.last_bh - b * p.Hkv;
-  constexpr int PER = D / 32;
-  for (int row = warp_id(); row < p.rows; row += 8) {
-    float mx = p.part_lse[static_cast<size_t>(mt.last_slot) * p.rows + row];
-    for (int q = c + 1; q <= e; ++q)
-      if (p.meta[q].n) mx = fmaxf(mx, p.part_lse[static_cast<size_t>(2 * q) * p.rows + row]);
-    float den = 0.f, acc[PER];
-#pragma unroll
-    for (int u = 0; u < PER; ++u) acc[u] = 0.f;
-    if (mx != -INFINITY) {
-      for (int q = c; q <= e; ++q) {
-        if (q > c && p.meta[q].n == 0) continue;
-        const size_t at = static_cast<size_t>(q == c ? mt.last_slot : 2 * q) * p.rows + row;
-        const float wgt = ex2(p.part_lse[at] - mx);
-        den += wgt;
-#pragma unroll
-        for (int u = 0; u < PER; ++u) acc[u] = fmaf(wgt, p.part_o[at * D + lane + 32 * u], acc[u]);
-      }
-    }
-    const float inv = den > 0.f ? 1.f / den : 0.f;
-    const int ql = row / p.g, h = hkv * p.g + row - ql * p.g;
-    T* dst = reinterpret_cast<T*>(p.O) + ((static_cast<size_t>(b) * p.Lq + ql) * p.H + h) * D;
-#pragma unroll
-    for (int u = 0; u < PER; ++u) dst[lane + 32 * u] = static_cast<T>(acc[u] * inv);
-    if (lane == 0)
-      p.LSE[(static_cast<size_t>(b) * p.H + h) * p.Lq + ql] =
-          den > 0.f ? (mx + __log2f(den)) * 0.6931471805599453f : -INFINITY;
   }
 }
 
@@ -780,9 +974,9 @@ __global__ void __launch_bounds__(128)
       __syncthreads();
     }
     if (i % Y != y) continue;
-    const int key = w.tile() * 128 + t;
+    const int key = w.tile * 128 + t;
     if (key >= w.s.n) continue;
-    const float* src = p.scores + (mt.t0 + i) * static_cast<long long>(p.rows) * 128 + t;
+    const float* src = p.scores + static_cast<long long>(mt.t0 + i) * p.rows * 128 + t;
     float sum = 0.f;
     for (int r = 0; r < p.rows; ++r) sum += ex2(fmaf(src[r * 128], p.sl2, -lse2[r]));
     float* dst = weights + (static_cast<long long>(w.b) * p.Hkv + w.hkv) * wstride + key;
