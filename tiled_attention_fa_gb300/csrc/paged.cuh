@@ -31,8 +31,9 @@
 //     are joined at the item's end: a tile's chain from scores to P takes 1500
 //     cycles, as long as its K and V take to arrive at D = 64.
 // Warps 0-7 (0-3 for 128 rows): softmax (thread = key of the tile), epilogue
-// (thread = head dim); the next two warps: TMA producer; TMEM allocation and
-// MMA issue.
+// (thread = head dim); then a warp each for the TMA loads, the S^T products
+// (and TMEM) and the O^T products: issuing a product holds its warp while it
+// runs, and one warp for both took 1900 cycles a tile with its waits.
 // Row maxima are reduced over the 32 keys of a warp by a halving exchange
 // (lane r ends with row r), then over the four warps through shared memory;
 // a row's max moves only when it grew by more than 2^8 in exp2 units, as in
@@ -91,9 +92,6 @@ __device__ __forceinline__ PagedSeq paged_seq_of(int len, const PagedParams& p) 
   s.cnt = s.n > 0 ? s.ns + ((s.n + 127) >> 7) - s.lo : 0;
   return s;
 }
-__device__ __forceinline__ PagedSeq paged_seq(int b, const PagedParams& p) {
-  return paged_seq_of(p.lens[b], p);
-}
 
 // Walk over the tiles of one CTA's part; a step costs a few instructions, an
 // item's start reads the length.
@@ -104,6 +102,7 @@ struct PagedWalk {
   int rem;        // tiles left in the part, this one included
   int item;       // items begun before this one in the part
   bool first;     // first tile of its item in this part
+  const int* lens;  // [B]; a copy in shared memory when B <= 32
   PagedSeq s;
 
   __device__ __forceinline__ bool last() const { return left == 1; }
@@ -129,7 +128,7 @@ struct PagedWalk {
             rem = 0;
             return;
           }
-          s = paged_seq(b, p);
+          s = paged_seq_of(lens[b], p);
         } while (s.cnt == 0);
       }
       enter();
@@ -176,11 +175,11 @@ struct PagedLayout {
   static constexpr uint32_t BAR_OFF = MAX_OFF + 2u * NG * N * 4u;
   static constexpr int B_QFULL = 0, B_QEMPTY = QS, B_KVFULL = 2 * QS, B_KVEMPTY = B_KVFULL + STAGES,
                        B_SFULL = B_KVEMPTY + STAGES, B_PFULL = B_SFULL + NB, B_PVDONE = B_PFULL + NB,
-                       B_OFULL = B_PVDONE + 2, B_OEMPTY = B_OFULL + 2, B_XMAX = B_OEMPTY + 2,
+                       B_OFULL = B_PVDONE + NB, B_OEMPTY = B_OFULL + 2, B_XMAX = B_OEMPTY + 2,
                        B_XSUM = B_XMAX + NG, B_JOIN = B_XSUM + 2, B_DONE = B_JOIN + 2 * NG,
-                       NBAR = B_DONE + 1;
+                       NBAR = B_DONE + 2;
   static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;  // tmem slot, abort flag, plan
-  static constexpr uint32_t USED = MISC_OFF + 128;
+  static constexpr uint32_t USED = MISC_OFF + 256;
   // At D = 64 the PV product still takes 128 rows of V^T; rows 64-127 come
   // from the 16 KB behind the tile and their results are never read.  Behind
   // the last ring stage that much must still be shared memory of this CTA.
@@ -188,8 +187,15 @@ struct PagedLayout {
   static constexpr uint32_t SMEM_ALLOC = SMEM_USED + 1024;
   static constexpr uint32_t TM_S = 0, TM_O = NB * N;  // O[item parity][group]
   static constexpr uint32_t TMEM_COLS = (NB + 2 * NG) * N;
-  static constexpr int SW = 4 * NG;  // softmax warps; then the producer's and the issuer's
-  static constexpr int NTHREADS = 32 * SW + 64;
+  static constexpr int SW = 4 * NG;  // softmax warps; then the producer, S and O^T warps
+  static constexpr int NTHREADS = 32 * SW + 96;
+  // arrivals a barrier takes a phase
+  __device__ static constexpr int arrivals(int i) {
+    return (i >= B_PFULL && i < B_PVDONE) || (i >= B_OEMPTY && i < B_XSUM) ? 4
+           : i >= B_XSUM && i < B_JOIN                                      ? SW
+           : i >= B_JOIN && i < B_DONE && ((i - B_JOIN) & 1) == 0           ? 4
+                                                                            : 1;
+  }
   static_assert(SMEM_ALLOC <= 232448, "shared memory");
   static_assert(TMEM_COLS <= 512 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM");
   static_assert(BAR_OFF % 8 == 0 && ST_OFF % 16 == 0, "alignment");
@@ -252,7 +258,7 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, int c, int G, i
   const int per = (p.B + NT - 1) / NT;
   const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
   int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += paged_seq(b, p).cnt * p.Hkv;
+  for (int b = b0; b < b1; ++b) mine += paged_seq_of(p.lens[b], p).cnt * p.Hkv;
   int incl = mine;
 #pragma unroll
   for (int h = 1; h < 32; h <<= 1) {
@@ -276,7 +282,7 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, int c, int G, i
   if (n > 0 && t0 >= before && t0 < before + mine) {
     int at = before;
     for (int b = b0; b < b1; ++b) {
-      const int cnt = paged_seq(b, p).cnt, all = cnt * p.Hkv;
+      const int cnt = paged_seq_of(p.lens[b], p).cnt, all = cnt * p.Hkv;
       if (t0 < at + all) {
         plan[0] = b;
         plan[1] = (t0 - at) / cnt;
@@ -289,8 +295,9 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, int c, int G, i
   __syncthreads();
 }
 
-__device__ __forceinline__ PagedWalk paged_walk(const PagedParams& p, const int* plan) {
+__device__ __forceinline__ PagedWalk paged_walk(const PagedParams& p, const int* plan, const int* lens) {
   PagedWalk w;
+  w.lens = lens;
   w.rem = plan[3];
   w.b = plan[0];
   w.hkv = plan[1];
@@ -298,7 +305,7 @@ __device__ __forceinline__ PagedWalk paged_walk(const PagedParams& p, const int*
   w.item = 0;
   w.left = 0;
   if (w.rem > 0) {
-    w.s = paged_seq(w.b, p);
+    w.s = paged_seq_of(lens[w.b], p);
     w.enter();
   }
   return w;
@@ -366,7 +373,7 @@ __device__ __forceinline__ void paged_join(const PagedParams& p, int b, int hkv,
       if (row >= p.rows) break;
       const int ql = row / p.g, h = hkv * p.g + row - ql * p.g;
       reinterpret_cast<T*>(p.O)[((static_cast<size_t>(b) * p.Lq + ql) * p.H + h) * D + d] =
-          static_cast<T>(den[r] > 0.f ? acc[r] / den[r] : 0.f);
+          static_cast<T>(den[r] > 0.f ? __fdividef(acc[r], den[r]) : 0.f);
       if (d == 0)
         p.LSE[(static_cast<size_t>(b) * p.H + h) * p.Lq + ql] =
             den[r] > 0.f ? (mx[r] + __log2f(den[r])) * 0.6931471805599453f : -INFINITY;
@@ -394,7 +401,9 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + Ly::MISC_OFF);
   AbortState* ab = reinterpret_cast<AbortState*>(gbase + Ly::MISC_OFF + 8);
   int* plan = reinterpret_cast<int*>(gbase + Ly::MISC_OFF + 16);
-  int* sums = reinterpret_cast<int*>(gbase + Ly::MISC_OFF + 48);
+  int* sums = reinterpret_cast<int*>(gbase + Ly::MISC_OFF + 48);      // NTHREADS / 32
+  int* lens_s = reinterpret_cast<int*>(gbase + Ly::MISC_OFF + 128);   // 32
+  const int* lens = p.B <= 32 ? lens_s : p.lens;
   unsigned int* err = device_error_word();
   const uint32_t warp = warp_id(), lane = lane_id();
 
@@ -404,34 +413,10 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
   for (uint32_t i = threadIdx.x; i < (Ly::QS * Ly::QT + Ly::PB * Ly::PT) / 16u; i += Ly::NTHREADS)
     reinterpret_cast<uint4*>(gbase + Ly::Q_OFF)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < Ly::QS; ++s) {
-      mbar_init(bar(Ly::B_QFULL + s), 1);
-      mbar_init(bar(Ly::B_QEMPTY + s), 1);
-    }
-    for (int s = 0; s < Ly::STAGES; ++s) {
-      mbar_init(bar(Ly::B_KVFULL + s), 1);
-      mbar_init(bar(Ly::B_KVEMPTY + s), 1);
-    }
-    for (int i = 0; i < Ly::NB; ++i) {
-      mbar_init(bar(Ly::B_SFULL + i), 1);
-      mbar_init(bar(Ly::B_PFULL + i), 4);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(Ly::B_PVDONE + i), 1);
-      mbar_init(bar(Ly::B_OFULL + i), 1);
-      mbar_init(bar(Ly::B_OEMPTY + i), 4);
-    }
-    for (int i = 0; i < Ly::NG; ++i) mbar_init(bar(Ly::B_XMAX + i), 4);
-    for (int i = 0; i < 2; ++i) mbar_init(bar(Ly::B_XSUM + i), Ly::SW);
-    for (int i = 0; i < Ly::NG; ++i) {
-      mbar_init(bar(Ly::B_JOIN + 2 * i), 4);
-      mbar_init(bar(Ly::B_JOIN + 2 * i + 1), 1);
-    }
-    mbar_init(bar(Ly::B_DONE), 1);
-    ab->flag = 0;
-    fence_barrier_init();
-  }
+  for (int i = threadIdx.x; i < Ly::NBAR; i += Ly::NTHREADS) mbar_init(bar(i), Ly::arrivals(i));
+  if (warp == 0) lens_s[lane] = len;
+  if (threadIdx.x == 0) ab->flag = 0;
+  fence_barrier_init();
   if (warp == Ly::SW + 1) {
     tmem_alloc(base + Ly::MISC_OFF, Ly::TMEM_COLS);
     tmem_relinquish();
@@ -451,7 +436,7 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
     const uint64_t stream = policy_evict_first();
     // Page ids of the next tiles, one box per lane: `cur` for the tiles from
     // cur_tile on, `nxt` for the batch behind it (of the same item or the next).
-    PagedWalk ahead = paged_walk(p, plan);
+    PagedWalk ahead = paged_walk(p, plan, lens);
     int nxt = -1, nxt_n = 0, cur = -1, cur_at = 0, cur_n = 0;
     auto fetch = [&]() {
       nxt_n = 0;
@@ -542,86 +527,83 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
       }
     }
   } else if (warp == Ly::SW + 1) {
-    // ------------------------------------------------------------ MMA issuer
-    uint32_t stage = 0, phase = 0;
+    // ------------------------------------------------------------ S^T = K Q^T
+    // Ring place of K_j: j, or NG + 2 (j - NG) behind the first NG; of V_i:
+    // the K tiles loaded before it, min(n, i + 1 + NG), plus i.
+    PagedWalk w = paged_walk(p, plan, lens);
     bool ok = true;
-    auto commit = [&](int b) {
-      if (elect_one()) tc_commit(bar(b));
-      __syncwarp();
-    };
-    auto take = [&](uint32_t& slot, unsigned int site) -> bool {
-      slot = stage;
-      if (!mbar_wait_warp(bar(Ly::B_KVFULL + stage), phase, ab, err, site)) return false;
-      if (++stage == Ly::STAGES) {
-        stage = 0;
-        phase ^= 1u;
-      }
-      tc_fence_after();
-      return true;
-    };
-    PagedWalk sw = paged_walk(p, plan), vw = sw;
-    // S^T of tile i (the walk sw's).
-    auto issue_s = [&](int i) -> bool {
-      const uint32_t qslot = sw.item % Ly::QS;
-      if (sw.first) {
-        if (!mbar_wait_warp(bar(Ly::B_QFULL + qslot), (sw.item / Ly::QS) & 1, ab, err, 1003)) return false;
-      }
-      uint32_t ks;
-      if (!take(ks, 1004)) return false;
-      const uint64_t kd = sdesc_sw128(base + Ly::RING_OFF + ks * Ly::TILE, 16, 1024);
+    for (int i = 0; ok && w.rem > 0; w.skip(p, w.left)) {
+      const uint32_t qslot = w.item % Ly::QS;
+      if (!mbar_wait_warp(bar(Ly::B_QFULL + qslot), (w.item / Ly::QS) & 1, ab, err, 1003)) { ok = false; break; }
       const uint64_t qd = sdesc_sw128(base + Ly::Q_OFF + qslot * Ly::QT, 16, 1024);
-      if (elect_one()) {
+      for (int x = 0; x < w.left; ++x, ++i) {
+        const uint32_t pos = i < Ly::NG ? i : 2 * i - Ly::NG, ks = pos % Ly::STAGES;
+        const int buf = i % Ly::NB;
+        // The buffer's last tile is through: its scores are read, and its P is
+        // too, so that the softmax may write P again once this S is there.
+        if (i >= Ly::NB &&
+            !mbar_wait_warp(bar(Ly::B_PVDONE + buf), (i / Ly::NB - 1) & 1, ab, err, 1017)) {
+          ok = false;
+          break;
+        }
+        if (!mbar_wait_warp(bar(Ly::B_KVFULL + ks), (pos / Ly::STAGES) & 1, ab, err, 1004)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t kd = sdesc_sw128(base + Ly::RING_OFF + ks * Ly::TILE, 16, 1024);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + Ly::TM_S + (i % Ly::NB) * N, kd + (((k >> 2) * Ly::CHUNK + (k & 3) * 32u) >> 4),
-                 qd + (((k >> 2) * Ly::QCH + (k & 3) * 32u) >> 4), IDESC_S, k > 0 ? 1u : 0u);
-        tc_commit(bar(Ly::B_SFULL + i % Ly::NB));
-        tc_commit(bar(Ly::B_KVEMPTY + ks));
-        if (sw.last()) tc_commit(bar(Ly::B_QEMPTY + qslot));
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(tmem + Ly::TM_S + buf * N, kd + (((k >> 2) * Ly::CHUNK + (k & 3) * 32u) >> 4),
+                   qd + (((k >> 2) * Ly::QCH + (k & 3) * 32u) >> 4), IDESC_S, k > 0 ? 1u : 0u);
+          tc_commit(bar(Ly::B_SFULL + buf));
+          tc_commit(bar(Ly::B_KVEMPTY + ks));
+          if (x + 1 == w.left) tc_commit(bar(Ly::B_QEMPTY + qslot));
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      sw.next(p);
-      return true;
-    };
-    for (int x = 0; x < Ly::NG && sw.rem > 0; ++x)
-      if (!issue_s(x)) {
-        ok = false;
-        break;
-      }
-    int in_item = 0;  // tiles of vw's item before this one: a group's first has no O to add to
-    for (int i = 0; ok && vw.rem > 0; ++i) {
-      const int gr = i % Ly::NG, ob = vw.item & 1;
-      if (vw.first) in_item = 0;
-      // S(i+NG) goes into the buffer tile i-NG left, whose scores were read
-      // before its P was handed over.
-      if (sw.rem > 0 && !issue_s(i + Ly::NG)) { ok = false; break; }
-      uint32_t vs;
-      if (!take(vs, 1005)) { ok = false; break; }
-      if (vw.first && vw.item >= 2 &&
-          !mbar_wait_warp(bar(Ly::B_OEMPTY + ob), ((vw.item >> 1) - 1) & 1, ab, err, 1006)) {
-        ok = false;
-        break;
-      }
-      if (!mbar_wait_warp(bar(Ly::B_PFULL + i % Ly::NB), (i / Ly::NB) & 1, ab, err, 1007)) { ok = false; break; }
-      tc_fence_after();
-      const uint64_t vd = sdesc_sw128(base + Ly::RING_OFF + vs * Ly::TILE, Ly::CHUNK, 1024);
-      const uint64_t pd = sdesc_sw128(base + Ly::P_OFF + (i % Ly::PB) * Ly::PT, 16, 1024);
-      if (elect_one()) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ss(tmem + Ly::TM_O + (ob * Ly::NG + gr) * N, vd + ((2048u * k) >> 4),
-                 pd + (((k >> 2) * Ly::QCH + (k & 3) * 32u) >> 4), IDESC_PV,
-                 (in_item >= Ly::NG || k > 0) ? 1u : 0u);
-        tc_commit(bar(Ly::B_PVDONE + (i & 1)));
-        tc_commit(bar(Ly::B_KVEMPTY + vs));
-        if (vw.last()) tc_commit(bar(Ly::B_OFULL + ob));
-      }
-      __syncwarp();
-      ++in_item;
-      vw.next(p);
     }
-    commit(Ly::B_DONE);
+    if (elect_one()) tc_commit(bar(Ly::B_DONE));
+    __syncwarp();
     mbar_wait_drain(bar(Ly::B_DONE), 0);
+  } else if (warp == Ly::SW + 2) {
+    // ------------------------------------------------------------ O^T += V^T P^T
+    PagedWalk w = paged_walk(p, plan, lens);
+    const int n_part = w.rem;
+    bool ok = true;
+    for (int i = 0; ok && w.rem > 0; w.skip(p, w.left)) {
+      const int ob = w.item & 1;
+      if (w.item >= 2 &&
+          !mbar_wait_warp(bar(Ly::B_OEMPTY + ob), ((w.item >> 1) - 1) & 1, ab, err, 1006)) {
+        ok = false;
+        break;
+      }
+      for (int x = 0; x < w.left; ++x, ++i) {
+        const uint32_t pos = min(n_part, i + 1 + Ly::NG) + i, vs = pos % Ly::STAGES;
+        const int buf = i % Ly::NB;
+        if (!mbar_wait_warp(bar(Ly::B_KVFULL + vs), (pos / Ly::STAGES) & 1, ab, err, 1005) ||
+            !mbar_wait_warp(bar(Ly::B_PFULL + buf), (i / Ly::NB) & 1, ab, err, 1007)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t vd = sdesc_sw128(base + Ly::RING_OFF + vs * Ly::TILE, Ly::CHUNK, 1024);
+        const uint64_t pd = sdesc_sw128(base + Ly::P_OFF + (i % Ly::PB) * Ly::PT, 16, 1024);
+        if (elect_one()) {
+          // (a group's first tile of the item has no O to add to)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_ss(tmem + Ly::TM_O + (ob * Ly::NG + i % Ly::NG) * N, vd + ((2048u * k) >> 4),
+                   pd + (((k >> 2) * Ly::QCH + (k & 3) * 32u) >> 4), IDESC_PV,
+                   (x >= Ly::NG || k > 0) ? 1u : 0u);
+          tc_commit(bar(Ly::B_PVDONE + buf));
+          tc_commit(bar(Ly::B_KVEMPTY + vs));
+          if (x + 1 == w.left) tc_commit(bar(Ly::B_OFULL + ob));
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) tc_commit(bar(Ly::B_DONE + 1));
+    __syncwarp();
+    mbar_wait_drain(bar(Ly::B_DONE + 1), 0);
   } else {
     // ------------------------------------------------------------ softmax + epilogue
     const int gr = warp >> 2, wq = warp & 3;  // group, warp of the group (its TMEM lanes)
@@ -642,7 +624,7 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
     float m[NCH], l[NL];
     uint32_t joins = 0;
     bool ok = true;
-    PagedWalk w = paged_walk(p, plan);
+    PagedWalk w = paged_walk(p, plan, lens);
     const int t0 = plan[4], total = plan[5], n_part = plan[3], G = gridDim.x;
     int k_start = 0, in_item = 0;  // the item's first tile in this part; its tiles so far
     for (int i = 0; ok && w.rem > 0; ++i, w.next(p)) {
@@ -727,7 +709,7 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
       if (__any_sync(0xffffffffu, grow)) {
         // The group's O^T holds its earlier tiles of the item once PV(i-NG) is
         // done (the next phase of that barrier needs this warp's P first).
-        if (!mbar_wait_warp(bar(Ly::B_PVDONE + ((i - Ly::NG) & 1)), ((i - Ly::NG) >> 1) & 1, ab, err, 1010)) {
+        if (!mbar_wait_warp(bar(Ly::B_PVDONE + (i - Ly::NG) % Ly::NB), ((i - Ly::NG) / Ly::NB) & 1, ab, err, 1010)) {
           ok = false;
           break;
         }
@@ -760,10 +742,10 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
       }
       // P = exp2(s c - m c), to shared memory in the 16-bit type (the MMA's
       // operand); the row sums take the unrounded values.
-      // (P's buffer: PV(i-PB) is done, as its S(i) was issued behind it; with two
-      // groups and two buffers it was issued before.)
-      if (Ly::PB == Ly::NG && i >= Ly::PB &&
-          !mbar_wait_warp(bar(Ly::B_PVDONE + (i & 1)), ((i - 2) >> 1) & 1, ab, err, 1016)) {
+      // (P's buffer: PV(i-NB) was done before S(i) was issued; with fewer P than
+      // S buffers the later PV has to be waited for.)
+      if (Ly::PB < Ly::NB && i >= Ly::PB &&
+          !mbar_wait_warp(bar(Ly::B_PVDONE + (i - Ly::PB) % Ly::NB), ((i - Ly::PB) / Ly::NB) & 1, ab, err, 1016)) {
         ok = false;
         break;
       }
@@ -912,8 +894,9 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
           int* flag = plan + 6 + gr;
           if (t == 0) {
             __threadfence();  // the group's partial, before the count
-            *flag = paged_count_in(p.count + c0, p.nonce, c1 - c0 + 1);
-            __threadfence();  // the count, before the others' partials
+            const int last = paged_count_in(p.count + c0, p.nonce, c1 - c0 + 1);
+            if (last) __threadfence();  // the count, before the others' partials
+            *flag = last;
             mbar_arrive(bar(Ly::B_JOIN + 2 * gr + 1));
           }
           if (!mbar_wait_warp(bar(Ly::B_JOIN + 2 * gr + 1), joins & 1, ab, err, 1015)) { ok = false; break; }
@@ -962,7 +945,7 @@ __global__ void __launch_bounds__(128)
   const PagedMeta mt = p.meta[blockIdx.x];
   __shared__ float lse2[128];
   const int plan[4] = {mt.b, mt.hkv, mt.k, mt.n};
-  PagedWalk w = paged_walk(p, plan);
+  PagedWalk w = paged_walk(p, plan, p.lens);
   const int Y = gridDim.y, y = blockIdx.y, t = threadIdx.x;
   for (int i = 0; w.rem > 0; ++i, w.next(p)) {
     if (w.first) {
