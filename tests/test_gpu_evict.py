@@ -86,7 +86,8 @@ def test_ties_zeros_and_odd_values(cuda_lib):
 
 
 def test_longer_than_shared_memory(cuda_lib):
-    check(*setup(1, 1, 64, "fp16", 64, [60000], 500, 3), 500, 4, 100)
+    """More keys than eight CTAs hold in shared memory."""
+    check(*setup(1, 1, 64, "fp16", 256, [420000], 500, 3), 500, 4, 100)
 
 
 def test_lengths_are_clamped_and_bad_pages_skipped(cuda_lib):
@@ -188,3 +189,12 @@ def test_refusals(cuda_lib):
     with pytest.raises(ValueError):
         fa.paged_evict(k, v, t, n, wd[:, :, :20].contiguous(), d, 32)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("n,B,Hkv", [(4097, 1, 1), (9000, 2, 2), (33000, 1, 1), (20000, 40, 8)])
+def test_clusters_of_every_size(cuda_lib, n, B, Hkv):
+    """One CTA to eight per pair, shares that end in the middle of a warp's, ties across shares."""
+    k, v, table, dst, lens, w = setup(B, Hkv, 64, "bf16", 256, [n - 37 * b for b in range(B)], 300, n)
+    w[0, 0] = (w[0, 0] * 4).round()
+    w[-1, -1] = torch.randint(0, 2, w.shape[2:], generator=torch.Generator().manual_seed(1)).float()
+    check(k, v, table, dst, lens, w, 300, 4, 30)

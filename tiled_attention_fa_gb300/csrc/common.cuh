@@ -106,10 +106,12 @@ inline bool make_group_map(CUtensorMap* map, const void* Q, int B, int Lq, int H
 // Launch with the programmatic-dependency attribute: the kernel may be placed
 // while its predecessor still runs and waits for it with griddepcontrol.wait.
 template <typename... A, typename... P>
-inline bool launch_after(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {
+inline bool launch_after_smem(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                              const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -117,6 +119,10 @@ inline bool launch_after(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...) == cudaSuccess;
+}
+template <typename... A, typename... P>
+inline bool launch_after(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t s, const A&... args) {
+  return launch_after_smem(kern, grid, block, 0, s, args...);
 }
 
 inline int sm_count() {

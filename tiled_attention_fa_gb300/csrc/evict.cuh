@@ -4,15 +4,20 @@
 // `recent`, and of those between the `need` = keep - sinks - recent heaviest,
 // ties to the lower index; then move the survivors, in their order, into other
 // pages.  Two kernels:
-//   fa_evict_select_kernel  one CTA per (sequence, head).  The weights become
-//     32-bit keys that order like the floats; a radix select over 11 + 11 + 10
-//     bits (histogram, then a suffix scan for the bin that holds the need-th
-//     largest) finds the threshold T and how many keys equal to T are taken;
-//     then each warp counts and writes its contiguous share, so survivors come
-//     out in ascending order with no sort.  Whole numbers only: exact.
+//   fa_evict_select_kernel  one cluster of 1 to 8 CTAs per (sequence, head), each
+//     holding a contiguous share of the keys in shared memory.  The weights
+//     become 32-bit keys that order like the floats; a radix select over
+//     11 + 11 + 10 bits (each CTA's histogram, added up a slice per CTA through
+//     the cluster's shared memory, then a scan for the bin that holds the
+//     need-th largest) finds the threshold T and how many keys equal to T are
+//     taken; then each warp counts and writes its contiguous share, so survivors
+//     come out in ascending order with no sort.  Whole numbers only: exact.
+//     Bound by latency: ten cluster barriers and the atomics of a few hot bins.
 //   fa_evict_move_kernel    bound by the read and write of the survivors' K
 //     and V: 16 bytes per thread and access, several rows in flight.
 #pragma once
+
+#include <cooperative_groups.h>
 
 #include <cstdint>
 
@@ -34,7 +39,7 @@ struct EvictParams {
   int B, Hkv, units;      // units = D / 8 per row and head
   int page, max_pages, dst_pages, num_pages;
   int keep, sinks, recent;
-  int smem_keys;          // keys that fit in shared memory
+  int smem_keys;          // keys of a CTA that fit in shared memory
 };
 
 // Unsigned order of the floats: NaN above everything, -0 equal to 0.
@@ -44,83 +49,154 @@ __device__ __forceinline__ uint32_t evict_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kEvictThreads = 1024, kEvictBins = 2048;
+constexpr int kEvictBins = 2048, kEvictCluster = 8;
+constexpr int evict_threads(int cs) { return cs == 1 ? 1024 : 512; }
 
-__global__ void __launch_bounds__(kEvictThreads) fa_evict_select_kernel(const EvictParams p) {
-  constexpr int NT = kEvictThreads, NW = NT / 32;
+// Exclusive sum of v over the block's threads; the block's total in `total`.
+template <int NT>
+__device__ __forceinline__ uint32_t evict_scan(uint32_t v, uint32_t* warps, uint32_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t incl = v;
+#pragma unroll
+  for (int h = 1; h < 32; h <<= 1) {
+    const uint32_t o = __shfl_up_sync(0xffffffffu, incl, h);
+    if (lane >= h) incl += o;
+  }
+  __syncthreads();  // (warps may still be read from the last scan)
+  if (lane == 31) warps[warp] = incl;
+  __syncthreads();
+  uint32_t before = incl - v;
+  total = 0;
+#pragma unroll
+  for (int x = 0; x < NT / 32; ++x) {
+    const uint32_t c = warps[x];
+    if (x < warp) before += c;
+    total += c;
+  }
+  return before;
+}
+
+template <int CS>
+__global__ void __launch_bounds__(evict_threads(CS)) fa_evict_select_kernel(const EvictParams p) {
+  namespace cg = cooperative_groups;
+  constexpr int NT = evict_threads(CS), NW = NT / 32;
   extern __shared__ uint32_t keys[];  // [smem_keys]
   __shared__ uint32_t hist[kEvictBins];
-  __shared__ uint32_t wsum[NW], wsum2[NW];
-  __shared__ uint32_t found[3];  // bin, count above it, count in it
+  __shared__ uint32_t warps[NW];
+  __shared__ uint32_t slice[kEvictCluster];  // totals of the ranks' slices of bins
+  __shared__ uint32_t found[2];              // bin, keys above it
+  __shared__ uint32_t counts[kEvictCluster][2];  // sure, tied keys of each rank
+  const int rank = CS == 1 ? 0 : static_cast<int>(cg::this_cluster().block_rank());
+  auto sync = [&]() {
+    if constexpr (CS == 1)
+      __syncthreads();
+    else
+      cg::this_cluster().sync();
+  };
+  auto of_rank = [&](uint32_t* x, int r) -> uint32_t* {
+    if constexpr (CS == 1)
+      return x;
+    else
+      return cg::this_cluster().map_shared_rank(x, r);
+  };
   pdl_launch_dependents();
-  const int bh = blockIdx.x, b = bh / p.Hkv;
+  const int bh = blockIdx.x / CS, b = bh / p.Hkv;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int n = static_cast<int>(
       min(static_cast<long long>(max(p.lens[b], 0)), static_cast<long long>(p.max_pages) * p.page));
   int* kept = p.kept + static_cast<long long>(bh) * p.keep;
-  if (t == 0 && bh - b * p.Hkv == 0) p.new_lens[b] = min(n, p.keep);
-  if (n <= p.keep) {
-    for (int i = t; i < p.keep; i += NT) kept[i] = i < n ? i : -1;
+  if (rank == 0 && t == 0 && bh - b * p.Hkv == 0) p.new_lens[b] = min(n, p.keep);
+  if (n <= p.keep) {  // (the whole cluster)
+    for (int i = rank * NT + t; i < p.keep; i += CS * NT) kept[i] = i < n ? i : -1;
     return;
   }
   const float* w = p.weights + bh * p.wstride;
-  const int lo = p.sinks, hi = n - p.recent;  // the contested keys (more of them than `need`)
-  const bool fits = n <= p.smem_keys;
-  auto key_at = [&](int j) -> uint32_t { return fits ? keys[j] : evict_key(w[j]); };
-  if (fits)
-    for (int j = t; j < n; j += NT) keys[j] = evict_key(w[j]);
+  // This rank's keys [s0, s1), and the contested ones of them [lo, hi).
+  const int share = ((n + CS - 1) / CS + 31) / 32 * 32;
+  const int s0 = min(n, rank * share), s1 = min(n, s0 + share);
+  const int lo = max(s0, p.sinks), hi = min(s1, n - p.recent);
+  const bool fits = share <= p.smem_keys;
+  auto key_at = [&](int j) -> uint32_t { return fits ? keys[j - s0] : evict_key(w[j]); };
+  if (fits) {
+    int j = s0 + t;
+    for (; j + 3 * NT < s1; j += 4 * NT) {  // four reads under way
+      const float a = w[j], b4 = w[j + NT], c = w[j + 2 * NT], d = w[j + 3 * NT];
+      keys[j - s0] = evict_key(a);
+      keys[j - s0 + NT] = evict_key(b4);
+      keys[j - s0 + 2 * NT] = evict_key(c);
+      keys[j - s0 + 3 * NT] = evict_key(d);
+    }
+    for (; j < s1; j += NT) keys[j - s0] = evict_key(w[j]);
+  }
   uint32_t need = p.keep - p.sinks - p.recent;
   uint32_t prefix = 0, mask = 0;  // bits fixed so far
   const uint32_t want = need;
+  constexpr int per_rank = kEvictBins / CS;  // bins of a slice; rank r sums bins from the top
   if (want > 0) {
     constexpr int shifts[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
-#pragma unroll
+#pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       for (int i = t; i < kEvictBins; i += NT) hist[i] = 0;
       __syncthreads();
       const uint32_t bm = (1u << bits[pass]) - 1u;
+      const int sh = shifts[pass];
       for (int j = lo + t; j < hi; j += NT) {
         const uint32_t k = key_at(j);
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shifts[pass]) & bm], 1u);
+        if ((k & mask) == prefix) atomicAdd(&hist[(k >> sh) & bm], 1u);
       }
-      __syncthreads();
-      // Thread t owns bins top - 2t, top - 2t - 1 (from the heaviest down):
-      // the bin in which the running count reaches `need`.
-      const int b1 = kEvictBins - 1 - 2 * t, b0 = b1 - 1;
-      const uint32_t c1 = hist[b1], c0 = hist[b0];
-      uint32_t incl = c1 + c0;
+      sync();
+      // Rank r owns the bins top - r * per_rank downwards; thread t owns `each`
+      // consecutive ones of them, summed over the ranks' histograms.
+      constexpr int each = per_rank > NT ? per_rank / NT : 1;
+      const int first = kEvictBins - 1 - rank * per_rank - t * each;
+      uint32_t c[each], mine = 0;
 #pragma unroll
-      for (int h = 1; h < 32; h <<= 1) {
-        const uint32_t o = __shfl_up_sync(0xffffffffu, incl, h);
-        if (lane >= h) incl += o;
+      for (int y = 0; y < each; ++y) c[y] = 0;
+      if (t * each < per_rank) {
+#pragma unroll
+        for (int r = 0; r < CS; ++r)
+#pragma unroll
+          for (int y = 0; y < each; ++y) c[y] += of_rank(hist, r)[first - y];
+#pragma unroll
+        for (int y = 0; y < each; ++y) mine += c[y];
       }
-      if (lane == 31) wsum[warp] = incl;
-      __syncthreads();
-      uint32_t before = incl - c1 - c0;
-      for (int x = 0; x < warp; ++x) before += wsum[x];
-      if (before < need && before + c1 >= need) {
-        found[0] = b1;
-        found[1] = before;
-      } else if (before + c1 < need && before + c1 + c0 >= need) {
-        found[0] = b0;
-        found[1] = before + c1;
+      uint32_t total;
+      uint32_t before = evict_scan<NT>(mine, warps, total);
+      if (CS > 1) {
+        if (t < CS) of_rank(slice, t)[rank] = total;
+        sync();
       }
-      __syncthreads();
-      prefix |= found[0] << shifts[pass];
-      mask |= bm << shifts[pass];
+      // The slice, then the bin, in which the running count reaches `need`.
+      for (int r = 0; r < rank; ++r) before += slice[r];
+      if (t * each < per_rank && before < need && before + mine >= need) {
+        int at = first;
+#pragma unroll
+        for (int y = 0; y + 1 < each; ++y)
+          if (at == first - y && before + c[y] < need) {
+            before += c[y];
+            --at;
+          }
+        for (int r = 0; r < CS; ++r) {
+          uint32_t* f = of_rank(found, r);
+          f[0] = at;
+          f[1] = before;
+        }
+      }
+      sync();
+      prefix |= found[0] << sh;
+      mask |= bm << sh;
       need -= found[1];
-      __syncthreads();
     }
   } else {
     __syncthreads();
   }
   // Now prefix is the need-th largest key's value, and `need` of the keys
   // equal to it are taken (the first ones); want == 0 takes none.
-  const int per = (n + NW * 32 - 1) / (NW * 32) * 32;
-  const int w0 = min(n, warp * per), w1 = min(n, w0 + per);
+  const int per = (s1 - s0 + NW * 32 - 1) / (NW * 32) * 32;
+  const int w0 = min(s1, s0 + warp * per), w1 = min(s1, w0 + per);
   // 2: always taken, 1: equal to the threshold, 0: not taken
   auto cls = [&](int j) -> int {
-    if (j < lo || j >= hi) return 2;
+    if (j < p.sinks || j >= n - p.recent) return 2;
     if (want == 0) return 0;
     const uint32_t k = key_at(j);
     return k > prefix ? 2 : (k == prefix ? 1 : 0);
@@ -131,15 +207,23 @@ __global__ void __launch_bounds__(kEvictThreads) fa_evict_select_kernel(const Ev
     sure += __popc(__ballot_sync(0xffffffffu, c == 2));
     tied += __popc(__ballot_sync(0xffffffffu, c == 1));
   }
-  if (lane == 0) {
-    wsum[warp] = sure;
-    wsum2[warp] = tied;
+  // Survivors and tied keys before this warp's: in the ranks before, in the
+  // warps before (one scan for both: 16 bits would not do, so two).
+  uint32_t all_sure, all_tied;
+  uint32_t at = evict_scan<NT>(lane == 0 ? sure : 0u, warps, all_sure);
+  uint32_t ties = evict_scan<NT>(lane == 0 ? tied : 0u, warps, all_tied);
+  at = __shfl_sync(0xffffffffu, at, 0);
+  ties = __shfl_sync(0xffffffffu, ties, 0);
+  if (CS > 1) {
+    if (t < CS) {
+      of_rank(&counts[0][0], t)[2 * rank] = all_sure;
+      of_rank(&counts[0][0], t)[2 * rank + 1] = all_tied;
+    }
+    sync();  // (the last access to another rank's shared memory is before it)
   }
-  __syncthreads();
-  uint32_t at = 0, ties = 0;  // survivors, tied keys of the warps before
-  for (int x = 0; x < warp; ++x) {
-    at += wsum[x];
-    ties += wsum2[x];
+  for (int r = 0; r < rank; ++r) {
+    at += counts[r][0];
+    ties += counts[r][1];
   }
   at += min(ties, need);
   for (int j0 = w0; j0 < w1; j0 += 32) {

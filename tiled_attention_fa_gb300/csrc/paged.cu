@@ -27,9 +27,8 @@ WsPlan ws_plan(int B, int Lq, long long cap, int H, int Hkv, int D, bool weights
   const size_t rows = static_cast<size_t>(H / Hkv) * Lq;
   WsPlan w;
   if (sms < 1) sms = 1;
-  size_t at = align256(sizeof(PagedMeta) * sms);
-  w.count = at;
-  at += align256(sizeof(unsigned long long) * sms);
+  w.count = 0;
+  size_t at = align256(sizeof(unsigned long long) * sms);
   w.part_o = at;
   at += align256(2 * static_cast<size_t>(sms) * rows * D * sizeof(float));
   w.part_lse = at;
@@ -83,12 +82,10 @@ fa_status launch_decode(const PagedDecodeArgs& a, PagedParams& p, int G, cudaStr
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::SMEM_ALLOC) !=
       cudaSuccess)
     return FA_ERR_CUDA;
-  kern<<<G, Ly::NTHREADS, Ly::SMEM_ALLOC, s>>>(tq, tk, tv, p);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (!launch_after_smem(kern, dim3(G), dim3(Ly::NTHREADS), Ly::SMEM_ALLOC, s, tq, tk, tv, p))
+    return FA_ERR_CUDA;
   if (a.weights == nullptr) return FA_OK;
-  // 16 blocks per part: the adds of one key need no order, and each block has
-  // one tile's reads in flight.
-  return launch_after(fa_paged_weights_kernel, dim3(G, 16), dim3(128), s, p, a.weights,
+  return launch_after(fa_paged_weights_kernel, dim3((p.max_tiles + 7) / 8, a.B * a.Hkv), dim3(256), s, p, a.weights,
                       static_cast<long long>(a.weights_stride))
              ? FA_OK
              : FA_ERR_CUDA;
@@ -122,7 +119,6 @@ fa_status run_paged_decode(const PagedDecodeArgs& a, cudaStream_t s) {
   p.lens = a.lens;
   p.O = a.O;
   p.LSE = a.LSE;
-  p.meta = reinterpret_cast<PagedMeta*>(ws);
   p.count = reinterpret_cast<unsigned long long*>(ws + w.count);
   p.nonce = call_nonce();
   p.part_o = reinterpret_cast<float*>(ws + w.part_o);
@@ -137,12 +133,14 @@ fa_status run_paged_decode(const PagedDecodeArgs& a, cudaStream_t s) {
   p.page = a.page;
   p.max_pages = a.max_pages;
   p.cap = static_cast<int>(cap);
+  p.max_tiles = static_cast<int>((cap + 127) / 128);
   p.window = a.window < p.cap ? a.window : 0;  // wider than the cache: every key
   p.sinks = p.window ? (a.sinks < p.cap ? a.sinks : p.cap) : 0;
   p.sl2 = 1.4426950408889634f / sqrtf(static_cast<float>(a.D));
   // One CTA per SM, fewer when even full sequences have fewer tiles.
   const long long most = static_cast<long long>(a.B) * a.Hkv * ((cap + 127) / 128);
   if (most >= (1ll << 31) || sms >= 65536) return FA_ERR_UNSUPPORTED;
+  if (a.weights != nullptr && static_cast<long long>(a.B) * a.Hkv > 65535) return FA_ERR_UNSUPPORTED;
   const int G = most < sms ? static_cast<int>(most) : sms;
   const bool bf16 = a.dtype == FA_BF16;
   if (a.D == 64) return bf16 ? pick_rows<64, true>(a, p, G, s) : pick_rows<64, false>(a, p, G, s);

@@ -52,26 +52,19 @@
 
 namespace fa {
 
-// What a CTA of the decode kernel leaves for the weights kernel: its part.
-struct PagedMeta {
-  int t0, n;      // first tile of the part in the list of all tiles, and how many
-  int b, hkv, k;  // first item and the first tile visited of it
-  int pad[3];
-};
-
 struct PagedParams {
   const int* table;  // [B, max_pages]
   const int* lens;   // [B]
   void* O;           // [B, Lq, H, D]
   float* LSE;        // [B, H, Lq] natural log
-  PagedMeta* meta;   // [G], with scores
   unsigned long long* count;  // [G] arrivals at the item that starts in part c and goes on:
   unsigned long long nonce;   // nonce << 16 | arrivals, 0 again when all have come
   float* part_o;     // [2 G, rows, D]
   float* part_lse;   // [2 G, rows], log2 units
-  float* scores;     // [tiles, rows, 128] raw scores for the weights, or NULL
+  float* scores;     // [B * Hkv, max_tiles, rows, 128] raw scores for the weights, or NULL
   int B, Lq, H, Hkv, g, rows;
   int page, max_pages, cap;  // cap = max_pages * page
+  int max_tiles;             // ceil(cap / 128)
   int window, sinks;         // window 0: none (then sinks 0)
   float sl2;                 // log2(e) / sqrt(D)
 };
@@ -407,14 +400,11 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
   unsigned int* err = device_error_word();
   const uint32_t warp = warp_id(), lane = lane_id();
 
-  const int len = (p.B <= 32 && static_cast<int>(lane) < p.B) ? p.lens[lane] : 0;
-  pdl_launch_dependents();
   // Query rows past g * Lq, and P rows no thread writes, are zero.
   for (uint32_t i = threadIdx.x; i < (Ly::QS * Ly::QT + Ly::PB * Ly::PT) / 16u; i += Ly::NTHREADS)
     reinterpret_cast<uint4*>(gbase + Ly::Q_OFF)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   for (int i = threadIdx.x; i < Ly::NBAR; i += Ly::NTHREADS) mbar_init(bar(i), Ly::arrivals(i));
-  if (warp == 0) lens_s[lane] = len;
   if (threadIdx.x == 0) ab->flag = 0;
   fence_barrier_init();
   if (warp == Ly::SW + 1) {
@@ -422,6 +412,12 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
     tmem_relinquish();
   }
   tc_fence_before();
+  // Everything above overlaps the end of the kernel before; nothing of global
+  // memory was touched.
+  pdl_launch_dependents();
+  pdl_wait();
+  const int len = (p.B <= 32 && static_cast<int>(lane) < p.B) ? p.lens[lane] : 0;
+  if (warp == 0) lens_s[lane] = len;
   paged_plan<Ly::NTHREADS>(p, blockIdx.x, gridDim.x, len, sums, plan);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -668,7 +664,8 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
         }
       }
       if (p.scores != nullptr) {
-        float* dst = p.scores + static_cast<long long>(t0 + i) * p.rows * 128 + t;
+        float* dst = p.scores + ((static_cast<size_t>(w.b) * p.Hkv + w.hkv) * p.max_tiles + w.k) *
+                                    p.rows * 128 + t;
 #pragma unroll
         for (int r = 0; r < R; ++r)
           if (r < p.rows) dst[r * 128] = __uint_as_float(sr[r]);
@@ -916,15 +913,6 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
       for (int x = t; x < p.Lq * p.H; x += 128)
         p.LSE[static_cast<size_t>(b) * p.Lq * p.H + x] = -INFINITY;
     }
-    if (threadIdx.x == 0 && p.scores != nullptr) {
-      PagedMeta mt;
-      mt.t0 = t0;
-      mt.n = ok ? plan[3] : 0;
-      mt.b = plan[0];
-      mt.hkv = plan[1];
-      mt.k = plan[2];
-      p.meta[blockIdx.x] = mt;
-    }
   }
 
   tc_fence_before();
@@ -937,33 +925,34 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
 }
 
 // Add every visible key's attention weight, sum over the item's rows of
-// exp(s - LSE), from the raw scores the decode kernel left.  Block (c, y)
-// takes every gridDim.y-th tile of part c; each key belongs to one thread.
-__global__ void __launch_bounds__(128)
+// exp(s - LSE), from the raw scores the decode kernel left.  Block (x, bh):
+// tiles 8x .. 8x + 7 of the item's list; each key belongs to one thread.
+__global__ void __launch_bounds__(256)
     fa_paged_weights_kernel(const PagedParams p, float* __restrict__ weights, long long wstride) {
   pdl_wait();
-  const PagedMeta mt = p.meta[blockIdx.x];
   __shared__ float lse2[128];
-  const int plan[4] = {mt.b, mt.hkv, mt.k, mt.n};
-  PagedWalk w = paged_walk(p, plan, p.lens);
-  const int Y = gridDim.y, y = blockIdx.y, t = threadIdx.x;
-  for (int i = 0; w.rem > 0; ++i, w.next(p)) {
-    if (w.first) {
-      __syncthreads();
-      if (t < p.rows) {
-        const float v = p.LSE[(static_cast<size_t>(w.b) * p.H + w.hkv * p.g + t % p.g) * p.Lq + t / p.g];
-        lse2[t] = v == -INFINITY ? 0.f : v * 1.4426950408889634f;  // (then every score is -inf)
-      }
-      __syncthreads();
-    }
-    if (i % Y != y) continue;
-    const int key = w.tile * 128 + t;
-    if (key >= w.s.n) continue;
-    const float* src = p.scores + static_cast<long long>(mt.t0 + i) * p.rows * 128 + t;
+  const int bh = blockIdx.y, b = bh / p.Hkv, hkv = bh - b * p.Hkv;
+  const PagedSeq s = paged_seq_of(p.lens[b], p);
+  const int k0 = blockIdx.x * 8;
+  if (k0 >= s.cnt) return;
+  const int t = threadIdx.x & 127;
+  if (threadIdx.x < p.rows) {
+    const float v = p.LSE[(static_cast<size_t>(b) * p.H + hkv * p.g + t % p.g) * p.Lq + t / p.g];
+    lse2[t] = v == -INFINITY ? 0.f : v * 1.4426950408889634f;  // (then every score is -inf)
+  }
+  __syncthreads();
+  float* dst = weights + static_cast<long long>(bh) * wstride + t;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int k = k0 + 2 * x + (threadIdx.x >> 7);
+    if (k >= s.cnt) break;
+    const int key0 = (k < s.ns ? k : s.lo + k - s.ns) * 128;
+    if (key0 + t >= s.n) break;
+    const float* src = p.scores + (static_cast<size_t>(bh) * p.max_tiles + k) * p.rows * 128 + t;
     float sum = 0.f;
+#pragma unroll 4
     for (int r = 0; r < p.rows; ++r) sum += ex2(fmaf(src[r * 128], p.sl2, -lse2[r]));
-    float* dst = weights + (static_cast<long long>(w.b) * p.Hkv + w.hkv) * wstride + key;
-    *dst += sum;
+    dst[key0] += sum;
   }
 }
 
@@ -977,6 +966,7 @@ __global__ void __launch_bounds__(256)
                           float* __restrict__ weights, long long wstride,
                           const float* __restrict__ new_w, int B, int L, int Hkv, int units,
                           int page, int max_pages, int num_pages) {
+  pdl_launch_dependents();
   const int per = Hkv * units;  // 16-byte units of a token (units = D / 8 per head)
   const long long all = static_cast<long long>(B) * L * per;
   for (long long i = blockIdx.x * 256ll + threadIdx.x; i < all; i += gridDim.x * 256ll) {
