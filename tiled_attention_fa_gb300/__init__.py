@@ -25,18 +25,20 @@ from .api import (  # noqa: F401
     decode_workspace_size,
     fwd,
     fwd_fp8,
-    key_weights,
-    key_weights_workspace_size,
-    paged_decode,
-    paged_decode_workspace_size,
-    paged_evict,
-    paged_write,
     alloc_window_workspace,
     window_attention_backward,
     window_bwd,
     window_fwd,
     window_workspace_size,
     workspace_size,
+)
+from .cache import (  # noqa: F401
+    key_weights,
+    key_weights_workspace_size,
+    paged_decode,
+    paged_decode_workspace_size,
+    paged_evict,
+    paged_write,
 )
 
 __all__ = ["fwd", "bwd_preprocess", "bwd", "attention_backward", "bwd_main", "bwd_postprocess", "workspace_size",

@@ -11,6 +11,8 @@ one batch overlapping the kernels of its neighbours.
 
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import _lib
@@ -45,14 +47,20 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _on_current_device(*tensors) -> None:
-    """Refuse tensors that lie elsewhere than on the current device, whose
-    stream the kernels go to."""
-    here = torch._C._cuda_getDevice()
-    for t in tensors:
-        if t is not None and t.get_device() != here:
-            raise ValueError(f"a tensor lies on cuda:{t.get_device()}, the current device is "
-                             f"cuda:{here}")
+def _device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _want(t, name: str, shape, dtype, device: int) -> None:
+    """``_need``, and on the current device, whose stream the kernels go to."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda
+                and t.get_device() == device):
+            return
+    except AttributeError:
+        pass
+    _need(t, name, shape, dtype)
+    raise ValueError(f"{name} lies on cuda:{t.get_device()}, the current device is cuda:{device}")
 
 
 def _stream(stream) -> int:
@@ -98,17 +106,19 @@ def window_fwd(q, k, v, window: int, sinks: int = 0, out=None, lse=None, stream=
     last Lq positions): query i, at position a = i + Lk - Lq, sees key j iff
     j <= a and (j > a - window or j < sinks)."""
     B, L, H, D = q.shape
-    Lk, Hkv = k.shape[1], k.shape[2]
-    _need(q, "q")
-    _need(k, "k", (B, Lk, Hkv, D), q.dtype)
-    _need(v, "v", (B, Lk, Hkv, D), q.dtype)
+    _, Lk, Hkv, _ = k.shape
+    dt, dev = q.dtype, _device()
+    _want(q, "q", (B, L, H, D), dt, dev)
+    _want(k, "k", (B, Lk, Hkv, D), dt, dev)
+    _want(v, "v", (B, Lk, Hkv, D), dt, dev)
     if out is None:
         out = torch.empty_like(q)
+    else:
+        _want(out, "out", (B, L, H, D), dt, dev)
     if lse is None:
-        lse = torch.empty(B, H, L, device=q.device, dtype=torch.float32)
-    _need(out, "out", q.shape, q.dtype)
-    _need(lse, "lse", (B, H, L), torch.float32)
-    _on_current_device(q, k, v, out, lse)
+        lse = q.new_empty((B, H, L), dtype=torch.float32)
+    else:
+        _want(lse, "lse", (B, H, L), torch.float32, dev)
     st = _lib.load().fa_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                    lse.data_ptr(), B, L, Lk, H, Hkv, D, window, sinks,
                                    _dtype_code(q), _stream(stream))
@@ -225,179 +235,6 @@ def decode_merge(workspace, out, lse, Lk: int, Hkv: int, stream=None):
     _lib.check("fa_decode_merge", st)
 
 
-def _pools(k_cache, v_cache, dtype):
-    """(num_pages, page, Hkv, D) of two pools whose pages may lie apart but are
-    contiguous in themselves (halves of one tensor, for instance)."""
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-        if t.dim() != 4 or t.shape != k_cache.shape:
-            raise ValueError(f"{name} must be [pages, page, Hkv, D], both pools alike")
-        _, page, hkv, d = t.shape
-        if t.stride()[1:] != (hkv * d, d, 1):
-            raise ValueError(f"the pages of {name} must be contiguous")
-    return k_cache.shape
-
-
-def _page_stride(t) -> int:
-    """Elements between two pages (of a pool of one page: the page itself)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2] * t.shape[3]
-
-
-def _row_stride(weights, name, B, Hkv, cap) -> int:
-    """Elements between the rows of key weights [B, Hkv, >= cap] fp32."""
-    _need(weights, name, dtype=torch.float32)
-    if weights.dim() != 3 or weights.shape[:2] != (B, Hkv) or weights.shape[2] < cap:
-        raise ValueError(f"{name} has shape {tuple(weights.shape)}, expected ({B}, {Hkv}, >= {cap})")
-    return weights.shape[2]
-
-
-def paged_write(k, v, k_cache, v_cache, block_table, start, counts=None, weights=None,
-                new_weights=None, stream=None) -> None:
-    """Write new keys and values k, v [B, L, Hkv, D] into the pages of
-    k_cache, v_cache [pages, page, Hkv, D]: token j of sequence b goes to
-    position start[b] + j, in page block_table[b, position // page].
-    block_table [B, P], start [B] and counts [B] (tokens of each sequence that
-    count, all L when None) are int32.  ``weights`` [B, Hkv, >= P * page] fp32
-    gets ``new_weights`` [B, Hkv, L] (or 0) at the positions written."""
-    num_pages, page, Hkv, D = _pools(k_cache, v_cache, k.dtype)
-    B, L = k.shape[:2]
-    _need(k, "k", (B, L, Hkv, D))
-    _need(v, "v", (B, L, Hkv, D), k.dtype)
-    P = block_table.shape[-1]
-    _need(block_table, "block_table", (B, P), torch.int32)
-    _need(start, "start", (B,), torch.int32)
-    if counts is not None:
-        _need(counts, "counts", (B,), torch.int32)
-    wstride = 0
-    if weights is not None:
-        wstride = _row_stride(weights, "weights", B, Hkv, P * page)
-    if new_weights is not None:
-        _need(new_weights, "new_weights", (B, Hkv, L), torch.float32)
-    _on_current_device(k, v, k_cache, v_cache, block_table, start, counts, weights, new_weights)
-    st = _lib.load().fa_paged_write(
-        k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _page_stride(k_cache),
-        _page_stride(v_cache), block_table.data_ptr(), start.data_ptr(), _ptr(counts), _ptr(weights),
-        wstride, _ptr(new_weights), B, L, Hkv, D, page, P, num_pages, _dtype_code(k), _stream(stream))
-    _lib.check("fa_paged_write", st)
-
-
-def paged_decode_workspace_size(B: int, Lq: int, H: int, Hkv: int, D: int, page: int, max_pages: int,
-                                weights: bool = False) -> int:
-    """Bytes of the workspace ``paged_decode`` needs on the current device."""
-    return int(_lib.load().fa_paged_decode_workspace_size(B, Lq, H, Hkv, D, page, max_pages,
-                                                          int(weights)))
-
-
-def paged_decode(q, k_cache, v_cache, block_table, lens, window: int = 0, sinks: int = 0,
-                 weights=None, out=None, lse=None, workspace=None, stream=None):
-    """O, LSE of the last Lq tokens of every sequence, q [B, Lq, H, D], over
-    its keys and values in the pages of k_cache, v_cache [pages, page, Hkv, D].
-    block_table [B, P] and lens [B] are int32; lens counts all keys, the new
-    tokens' own included: query i sits at position a = lens[b] - Lq + i and
-    sees key j iff j <= a and (window == 0 or j > a - window or j < sinks).  A
-    query that sees nothing gives O = 0, LSE = -inf.  (H / Hkv) * Lq <= 128.
-    ``weights`` [B, Hkv, >= P * page] fp32 is added to in place: each key's
-    attention weight over the queries and the group's heads.  ``workspace`` (a
-    CUDA byte tensor of at least ``paged_decode_workspace_size`` bytes) is
-    allocated when not given."""
-    num_pages, page, Hkv, D = _pools(k_cache, v_cache, q.dtype)
-    B, Lq, H, _ = q.shape
-    _need(q, "q", (B, Lq, H, D))
-    P = block_table.shape[-1]
-    _need(block_table, "block_table", (B, P), torch.int32)
-    _need(lens, "lens", (B,), torch.int32)
-    out, lse = _decode_outputs(q, B, Lq, H, out, lse)
-    wstride = 0
-    if weights is not None:
-        wstride = _row_stride(weights, "weights", B, Hkv, P * page)
-    _on_current_device(q, k_cache, v_cache, block_table, lens, weights, out, lse, workspace)
-    if workspace is None:
-        n = paged_decode_workspace_size(B, Lq, H, Hkv, D, page, P, weights is not None)
-        workspace = torch.empty(max(n, 16), device=q.device, dtype=torch.uint8)
-    st = _lib.load().fa_paged_decode(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _page_stride(k_cache),
-        _page_stride(v_cache), block_table.data_ptr(), lens.data_ptr(), out.data_ptr(),
-        lse.data_ptr(), _ptr(weights), wstride, workspace.data_ptr(), _nbytes(workspace), B, Lq, H,
-        Hkv, D, page, P, num_pages, window, sinks, _dtype_code(q), _stream(stream))
-    _lib.check("fa_paged_decode", st)
-    return out, lse
-
-
-def paged_evict(k_cache, v_cache, block_table, lens, weights, dst_table, keep: int, sinks: int = 0,
-                recent: int = 0, kept=None, new_lens=None, new_weights=None, stream=None):
-    """Cut every sequence's paged keys and values down to ``keep`` per K/V
-    head: its first ``sinks``, its last ``recent`` and the heaviest others by
-    ``weights`` [B, Hkv, >= P * page] fp32 (ties to the lower position).  The
-    survivors move, in their order, into the pages of dst_table [B, P2] int32
-    (P2 * page >= keep), which no sequence of the call may read from; the old
-    pages stay as they are.
-    Returns kept [B, Hkv, keep] int32 (old positions, -1 behind the last),
-    new_lens [B] int32 = min(lens, keep) and new_weights [B, Hkv, P2 * page]
-    (zero behind the survivors)."""
-    num_pages, page, Hkv, D = _pools(k_cache, v_cache, k_cache.dtype)
-    B, P = block_table.shape
-    P2 = dst_table.shape[-1]
-    _need(block_table, "block_table", (B, P), torch.int32)
-    _need(lens, "lens", (B,), torch.int32)
-    _need(dst_table, "dst_table", (B, P2), torch.int32)
-    wstride = _row_stride(weights, "weights", B, Hkv, P * page)
-    if keep < 1:
-        raise ValueError("keep must be at least 1")
-    dev = k_cache.device
-    if kept is None:
-        kept = torch.empty(B, Hkv, keep, device=dev, dtype=torch.int32)
-    if new_lens is None:
-        new_lens = torch.empty(B, device=dev, dtype=torch.int32)
-    if new_weights is None:
-        new_weights = torch.empty(B, Hkv, P2 * page, device=dev, dtype=torch.float32)
-    _need(kept, "kept", (B, Hkv, keep), torch.int32)
-    _need(new_lens, "new_lens", (B,), torch.int32)
-    _need(new_weights, "new_weights", (B, Hkv, P2 * page), torch.float32)
-    _on_current_device(k_cache, v_cache, block_table, lens, weights, dst_table, kept, new_lens,
-                       new_weights)
-    st = _lib.load().fa_paged_evict(
-        k_cache.data_ptr(), v_cache.data_ptr(), _page_stride(k_cache), _page_stride(v_cache),
-        block_table.data_ptr(), lens.data_ptr(), weights.data_ptr(), wstride, dst_table.data_ptr(),
-        keep, sinks, recent, kept.data_ptr(), new_lens.data_ptr(), new_weights.data_ptr(), B, Hkv, D,
-        page, P, P2, num_pages, _dtype_code(k_cache), _stream(stream))
-    _lib.check("fa_paged_evict", st)
-    return kept, new_lens, new_weights
-
-
-def key_weights_workspace_size() -> int:
-    """Bytes of the workspace ``key_weights`` needs on the current device."""
-    return int(_lib.load().fa_key_weights_workspace_size())
-
-
-def key_weights(q, k, lse, causal: bool = False, window: int = 0, sinks: int = 0, out=None,
-                workspace=None, stream=None):
-    """The attention each key has received: W [B, Hkv, Lk] fp32, the sum over
-    the group's heads and the queries of exp(q . k / sqrt(D) - LSE), where
-    ``lse`` [B, H, Lq] is what ``fwd`` or (window > 0, causal) ``window_fwd``
-    gave for q [B, Lq, H, D] and k [B, Lk, Hkv, D] under the same mask.
-    ``workspace`` (a CUDA byte tensor of at least
-    ``key_weights_workspace_size`` bytes) is allocated when not given."""
-    B, L, H, D = q.shape
-    Lk, Hkv = k.shape[1], k.shape[2]
-    _need(q, "q")
-    _need(k, "k", (B, Lk, Hkv, D), q.dtype)
-    _need(lse, "lse", (B, H, L), torch.float32)
-    if out is None:
-        out = torch.empty(B, Hkv, Lk, device=q.device, dtype=torch.float32)
-    _need(out, "out", (B, Hkv, Lk), torch.float32)
-    _on_current_device(q, k, lse, out, workspace)
-    if workspace is None:
-        workspace = torch.empty(key_weights_workspace_size(), device=q.device, dtype=torch.uint8)
-    st = _lib.load().fa_key_weights(q.data_ptr(), k.data_ptr(), lse.data_ptr(), out.data_ptr(),
-                                    workspace.data_ptr(), _nbytes(workspace), B, L, Lk, H, Hkv, D,
-                                    int(bool(causal)), window, sinks, _dtype_code(q), _stream(stream))
-    _lib.check("fa_key_weights", st)
-    return out
-
-
 def workspace_size(B: int, L: int, H: int, D: int) -> int:
     """Bytes of the fp32 dQ accumulator the backward needs."""
     return int(_lib.load().fa_bwd_workspace_size(B, L, H, D))
@@ -465,6 +302,7 @@ def bwd(q, k, v, o, do, lse, delta, causal: bool = False, dq=None, dk=None, dv=N
     return dq, dk, dv
 
 
+@functools.lru_cache(maxsize=1024)
 def window_workspace_size(B: int, Lq: int, Lk: int, H: int, Hkv: int, D: int, window: int,
                           sinks: int = 0) -> int:
     """Bytes of the workspace ``window_bwd`` needs: the fp32 dQ accumulator and
@@ -485,23 +323,30 @@ def window_bwd(q, k, v, do, lse, delta, window: int, sinks: int = 0, dq=None, dk
     ``accum_zeroed`` (fa_bwd_preprocess zeroed its accumulator) the call zeroes
     that part first."""
     B, L, H, D = q.shape
-    Lk, Hkv = k.shape[1], k.shape[2]
-    _need(q, "q")
-    for name, t, shp in (("k", k, (B, Lk, Hkv, D)), ("v", v, (B, Lk, Hkv, D)), ("do", do, q.shape)):
-        _need(t, name, shp, q.dtype)
-    _need(lse, "lse", (B, H, L), torch.float32)
-    _need(delta, "delta", (B, H, L), torch.float32)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    _need(dq, "dq", q.shape, q.dtype)
-    _need(dk, "dk", k.shape, q.dtype)
-    _need(dv, "dv", v.shape, q.dtype)
+    _, Lk, Hkv, _ = k.shape
+    dt, dev, kv = q.dtype, _device(), (B, Lk, Hkv, D)
+    _want(q, "q", (B, L, H, D), dt, dev)
+    _want(k, "k", kv, dt, dev)
+    _want(v, "v", kv, dt, dev)
+    _want(do, "do", (B, L, H, D), dt, dev)
+    _want(lse, "lse", (B, H, L), torch.float32, dev)
+    _want(delta, "delta", (B, H, L), torch.float32, dev)
+    if dq is None:
+        dq = torch.empty_like(q)
+    else:
+        _want(dq, "dq", (B, L, H, D), dt, dev)
+    if dk is None:
+        dk = torch.empty_like(k)
+    else:
+        _want(dk, "dk", kv, dt, dev)
+    if dv is None:
+        dv = torch.empty_like(v)
+    else:
+        _want(dv, "dv", kv, dt, dev)
     if dq_accum is None:
         dq_accum = alloc_window_workspace(B, L, Lk, H, Hkv, D, window, sinks, q.device)
         accum_zeroed = False
-    _need(dq_accum, "dq_accum", dtype=torch.float32)
-    _on_current_device(q, k, v, do, lse, delta, dq, dk, dv, dq_accum)
+    _want(dq_accum, "dq_accum", dq_accum.shape, torch.float32, dev)
     st = _lib.load().fa_window_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), do.data_ptr(),
                                    lse.data_ptr(), delta.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                                    dv.data_ptr(), dq_accum.data_ptr(), dq_accum.numel() * 4,
