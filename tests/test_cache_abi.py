@@ -101,3 +101,19 @@ def test_paged_evict(lib):
         assert call(**kw) == INVALID, kw
     assert call(D=32) == UNSUPPORTED and call(page=48, kst=1 << 20, vst=1 << 20) == UNSUPPORTED
     assert call(B=1 << 15, Hkv=2) == UNSUPPORTED
+
+
+def test_tensors_on_the_host_are_refused(lib):
+    """The calls on torch tensors check their arguments before they touch the device."""
+    import torch
+
+    import tiled_attention_fa_gb300 as fa
+    q, kv = torch.zeros(1, 2, 4, 64, dtype=torch.float16), torch.zeros(3, 16, 2, 64, dtype=torch.float16)
+    i = torch.zeros(1, 3, dtype=torch.int32)
+    for call in (lambda: fa.window_fwd(q, q, q, 4), lambda: fa.window_attention_backward(q, q, q, q, q, q, 4),
+                 lambda: fa.window_bwd(q, q, q, q, q, q, 4), lambda: fa.paged_decode(q, kv, kv, i, i),
+                 lambda: fa.paged_write(q, q, kv, kv, i, i), lambda: fa.key_weights(q, q, q),
+                 lambda: fa.paged_evict(kv, kv, i, i, q, i, 4), lambda: fa.paged_decode(None, kv, kv, i, i),
+                 lambda: fa.key_weights([1.0], q, q)):
+        with pytest.raises(TypeError):
+            call()

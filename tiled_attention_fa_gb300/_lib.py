@@ -20,6 +20,7 @@ FA_NOALLOC_SCRATCH_BYTES = 64 << 20
 FA_F16, FA_BF16 = 0, 1
 
 _lib = None
+_binding = None
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
@@ -90,6 +91,21 @@ def load():
         fn.restype = res
     _lib = lib
     return lib
+
+
+def binding():
+    """The C++ part of the binding (``_binding.so``, built with the library)."""
+    global _binding
+    if _binding is None:
+        load()
+        import torch  # noqa: F401  (its libraries must be loaded first)
+        try:
+            from . import _binding as mod
+        except ImportError as e:
+            raise RuntimeError("the binding is missing or was built for another torch: build it with "
+                               "`python -m tiled_attention_fa_gb300.build`") from e
+        _binding = mod
+    return _binding
 
 
 def check(fn: str, status: int) -> None:

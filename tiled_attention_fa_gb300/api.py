@@ -11,8 +11,6 @@ one batch overlapping the kernels of its neighbours.
 
 from __future__ import annotations
 
-import functools
-
 import torch
 
 from . import _lib
@@ -41,26 +39,6 @@ def _need(t: torch.Tensor, name: str, shape=None, dtype=None):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _device() -> int:
-    return torch._C._cuda_getDevice()
-
-
-def _want(t, name: str, shape, dtype, device: int) -> None:
-    """``_need``, and on the current device, whose stream the kernels go to."""
-    try:
-        if (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda
-                and t.get_device() == device):
-            return
-    except AttributeError:
-        pass
-    _need(t, name, shape, dtype)
-    raise ValueError(f"{name} lies on cuda:{t.get_device()}, the current device is cuda:{device}")
 
 
 def _stream(stream) -> int:
@@ -105,25 +83,10 @@ def window_fwd(q, k, v, window: int, sinks: int = 0, out=None, lse=None, stream=
     q [B, Lq, H, D]; k, v [B, Lk, Hkv, D] with Lq <= Lk (the queries are the
     last Lq positions): query i, at position a = i + Lk - Lq, sees key j iff
     j <= a and (j > a - window or j < sinks)."""
-    B, L, H, D = q.shape
-    _, Lk, Hkv, _ = k.shape
-    dt, dev = q.dtype, _device()
-    _want(q, "q", (B, L, H, D), dt, dev)
-    _want(k, "k", (B, Lk, Hkv, D), dt, dev)
-    _want(v, "v", (B, Lk, Hkv, D), dt, dev)
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _want(out, "out", (B, L, H, D), dt, dev)
-    if lse is None:
-        lse = q.new_empty((B, H, L), dtype=torch.float32)
-    else:
-        _want(lse, "lse", (B, H, L), torch.float32, dev)
-    st = _lib.load().fa_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                   lse.data_ptr(), B, L, Lk, H, Hkv, D, window, sinks,
-                                   _dtype_code(q), _stream(stream))
-    _lib.check("fa_window_fwd", st)
-    return out, lse
+    r = _lib.binding().window_fwd(q, k, v, window, sinks, out, lse, stream)
+    if r.__class__ is int:
+        _lib.check("fa_window_fwd", r)
+    return r
 
 
 def decode_workspace_size(B: int, Lq: int, Lk: int, H: int, Hkv: int, D: int) -> int:
@@ -302,7 +265,6 @@ def bwd(q, k, v, o, do, lse, delta, causal: bool = False, dq=None, dk=None, dv=N
     return dq, dk, dv
 
 
-@functools.lru_cache(maxsize=1024)
 def window_workspace_size(B: int, Lq: int, Lk: int, H: int, Hkv: int, D: int, window: int,
                           sinks: int = 0) -> int:
     """Bytes of the workspace ``window_bwd`` needs: the fp32 dQ accumulator and
@@ -322,50 +284,21 @@ def window_bwd(q, k, v, do, lse, delta, window: int, sinks: int = 0, dq=None, dk
     the fp32 workspace of ``window_workspace_size`` bytes; unless
     ``accum_zeroed`` (fa_bwd_preprocess zeroed its accumulator) the call zeroes
     that part first."""
-    B, L, H, D = q.shape
-    _, Lk, Hkv, _ = k.shape
-    dt, dev, kv = q.dtype, _device(), (B, Lk, Hkv, D)
-    _want(q, "q", (B, L, H, D), dt, dev)
-    _want(k, "k", kv, dt, dev)
-    _want(v, "v", kv, dt, dev)
-    _want(do, "do", (B, L, H, D), dt, dev)
-    _want(lse, "lse", (B, H, L), torch.float32, dev)
-    _want(delta, "delta", (B, H, L), torch.float32, dev)
-    if dq is None:
-        dq = torch.empty_like(q)
-    else:
-        _want(dq, "dq", (B, L, H, D), dt, dev)
-    if dk is None:
-        dk = torch.empty_like(k)
-    else:
-        _want(dk, "dk", kv, dt, dev)
-    if dv is None:
-        dv = torch.empty_like(v)
-    else:
-        _want(dv, "dv", kv, dt, dev)
-    if dq_accum is None:
-        dq_accum = alloc_window_workspace(B, L, Lk, H, Hkv, D, window, sinks, q.device)
-        accum_zeroed = False
-    _want(dq_accum, "dq_accum", dq_accum.shape, torch.float32, dev)
-    st = _lib.load().fa_window_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), do.data_ptr(),
-                                   lse.data_ptr(), delta.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-                                   dv.data_ptr(), dq_accum.data_ptr(), dq_accum.numel() * 4,
-                                   0 if accum_zeroed else 1, B, L, Lk, H, Hkv, D, window, sinks, _dtype_code(q),
-                                   _stream(stream))
-    _lib.check("fa_window_bwd", st)
-    return dq, dk, dv
+    r = _lib.binding().window_bwd(q, k, v, None, lse, do, delta, window, sinks, dq, dk, dv, dq_accum,
+                                  accum_zeroed, stream)
+    if r.__class__ is int:
+        _lib.check("fa_window_bwd", r)
+    return r[:3]
 
 
 def window_attention_backward(q, k, v, o, lse, do, window: int, sinks: int = 0, dq_accum=None,
                               stream=None):
     """``attention_backward`` for ``window_fwd``: preprocess + backward in one call."""
-    B, L, H, D = q.shape
-    if dq_accum is None:
-        dq_accum = alloc_window_workspace(B, L, k.shape[1], H, k.shape[2], D, window, sinks, q.device)
-    delta = bwd_preprocess(o, do, dq_accum=dq_accum, stream=stream)
-    dq, dk, dv = window_bwd(q, k, v, do, lse, delta, window, sinks, dq_accum=dq_accum,
-                            accum_zeroed=True, stream=stream)
-    return dq, dk, dv, delta
+    r = _lib.binding().window_bwd(q, k, v, o, lse, do, None, window, sinks, None, None, None, dq_accum,
+                                  True, stream)
+    if r.__class__ is int:
+        _lib.check("fa_window_bwd", r)
+    return r
 
 
 def bwd_main(q, k, v, do, lse, delta, dq_accum, causal: bool = False, dk=None, dv=None,

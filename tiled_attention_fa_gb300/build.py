@@ -5,6 +5,8 @@
 Each .cu unit compiles in parallel to an object file under ``_build/``; the
 objects then link into ``libfa_gb300.so`` with the CUDA runtime linked
 statically, so loading the library needs no GPU and no libcuda at load time.
+``_binding.so``, the part of the Python binding that works on torch tensors in
+C++, compiles alongside against the installed torch and links to the library.
 """
 
 from __future__ import annotations
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +25,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB_NAME = "libfa_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 UNITS = ["api.cu", "fwd.cu", "bwd.cu", "decode.cu", "paged.cu", "weights.cu", "evict.cu"]
+BINDING_PATH = os.path.join(HERE, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -48,11 +52,43 @@ def _compile(unit: str, verbose_ptxas: bool) -> tuple:
     return unit, obj, r.returncode, r.stdout + r.stderr
 
 
+def _compile_binding() -> tuple:
+    """binding.cpp against the installed torch (headers only are needed here)."""
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(BUILD, "binding.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = [os.environ.get("CXX", "g++"), "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj, "-O2",
+           "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", inc, "-I",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-I", cuda, "-I",
+           sysconfig.get_paths()["include"]]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    return "binding.cpp", obj, r.returncode, r.stdout + r.stderr
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING_PATH + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L" + HERE, "-l:" + LIB_NAME,
+           "-Wl,-rpath,$ORIGIN", "-L" + lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("link of the binding failed:\n" + r.stdout + r.stderr)
+    os.replace(tmp, BINDING_PATH)
+
+
 def build(verbose_ptxas: bool = False, quiet: bool = False) -> str:
     """Compile every unit and link the shared library; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(UNITS)) as ex:
+    with ThreadPoolExecutor(max_workers=len(UNITS) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(lambda u: _compile(u, verbose_ptxas), UNITS))
+        binding = binding.result()
+    if binding[2] != 0:
+        raise RuntimeError("the binding failed to compile:\n" + binding[3])
     failed = [r for r in results if r[2] != 0]
     for unit, _, rc, out in results:
         if (rc != 0 or verbose_ptxas) and out.strip():
@@ -60,12 +96,13 @@ def build(verbose_ptxas: bool = False, quiet: bool = False) -> str:
     if failed:
         raise RuntimeError("nvcc failed for " + ", ".join(r[0] for r in failed))
     tmp = LIB_PATH + ".tmp"
-    cmd = [nvcc(), "-shared", "-o", tmp] + [r[1] for r in results] + ARCH + \
+    cmd = [nvcc(), "-shared", "-Xlinker", "-soname=" + LIB_NAME, "-o", tmp] + [r[1] for r in results] + ARCH + \
         ["-Xcompiler", "-fPIC", "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
     os.replace(tmp, LIB_PATH)
+    _link_binding(binding[1])
     if not quiet:
         print("built", LIB_PATH)
     return LIB_PATH
