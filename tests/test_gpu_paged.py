@@ -197,13 +197,12 @@ def test_prompt_then_steps(cuda_lib):
     vc = kc.clone()
     table = torch.randperm(B * P, generator=g).view(B, P).to(torch.int32).cuda()
     start = torch.zeros(B, dtype=torch.int32, device="cuda")
-    whole, _ = fa.window_fwd(q, k, v, window, sinks)
-    o, _ = fa.window_fwd(q[:, :L].contiguous(), k[:, :L].contiguous(), v[:, :L].contiguous(), window, sinks)
-    assert torch.equal(o, whole[:, :L])
+    prompt, _ = fa.window_fwd(q[:, :L].contiguous(), k[:, :L].contiguous(), v[:, :L].contiguous(), window, sinks)
     fa.paged_write(k[:, :L].contiguous(), v[:, :L].contiguous(), kc, vc, table, start)
     lens = start + L
     mask = ref.seen(np.arange(n), n, window, sinks)
     O, _, bound = ref.forward(to64(q), to64(k), to64(v), mask, "bf16")
+    within(to64(prompt), O[:, :L], bound[:, :L], "O of the prompt")
     for t in range(L, n):
         one = [x[:, t: t + 1].contiguous() for x in (q, k, v)]
         fa.paged_write(one[1], one[2], kc, vc, table, lens)

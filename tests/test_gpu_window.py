@@ -77,7 +77,8 @@ def test_window_many_tiles(cuda_lib, D, dtype):
 
 
 def test_a_wide_window_is_the_causal_call(cuda_lib):
-    q, k, v, _ = make_qkv_kv(2, 600, 900, 4, 2, 128, "bf16", 3)
+    """Bit for bit where both run the same schedule (more Q tiles than SMs)."""
+    q, k, v, _ = make_qkv_kv(2, 600, 900, 32, 2, 128, "bf16", 3)
     qd, kd, vd = q.cuda(), k.cuda(), v.cuda()
     o1, l1 = fa.fwd(qd, kd, vd, causal=True)
     o2, l2 = fa.window_fwd(qd, kd, vd, 900)
@@ -174,3 +175,15 @@ def test_refusals(cuda_lib):
     assert e.value.status == _lib.FA_ERR_SCRATCH_TOO_SMALL
     with pytest.raises(TypeError):
         fa.window_fwd(q.cpu(), k, v, 4)
+
+
+@pytest.mark.parametrize("B,H,Lq,Lk,D,window,sinks", [(1, 1, 128, 128, 64, 40, 0), (1, 2, 129, 129, 128, 129, 0),
+                                                      (1, 4, 100, 2000, 128, 1500, 200), (2, 8, 300, 1300, 64, 500, 4)])
+def test_one_tile_per_cta(cuda_lib, B, H, Lq, Lk, D, window, sinks):
+    """Few Q tiles: the two warpgroups share one tile's steps (an odd and an even number of them, one
+    alone, and rows that see nothing of one warpgroup's steps)."""
+    (q, k, v, do), o, lse, _ = both(B, Lq, Lk, H, H, D, "bf16", window, sinks, seed=Lq + D, train=False)
+    mask = ref.seen(np.arange(Lk - Lq, Lk), Lk, window, sinks)
+    O, lse_r, bound = ref.forward(q, k, v, mask, "bf16")
+    within(o, O, bound, "O")
+    within(lse, lse_r, np.full(lse_r.shape, ref.FP32), "LSE")

@@ -36,6 +36,11 @@
 // skips the one window tile that only the first needs.  A row may see nothing
 // of its first tiles (its window starts further right), so the running max can
 // be -inf there: exponents are then taken against 0, giving P = 0.
+// A problem of fewer Q tiles than SMs gives each tile a CTA of its own, and both
+// warpgroups then take that one tile: warpgroup t the steps j with j % 2 = t,
+// each with a maximum, sum and O of its own, joined by warpgroup 0 at the end
+// (O_0 and O_1 lie in the same TMEM lanes).  A single tile's chain S, softmax, PV
+// would take 3,100 cycles a step with nothing to overlap it.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -80,9 +85,10 @@ struct FwdLayout {
   // barrier slots
   static constexpr int B_QFULL = 0, B_QEMPTY = 1, B_KVFULL = 2, B_KVEMPTY = 2 + STAGES,
                        B_SFULL = 2 + 2 * STAGES, B_PFULL = B_SFULL + 2, B_OFULL = B_PFULL + 4,
-                       B_OEMPTY = B_OFULL + 2, B_DONE = B_OEMPTY + 2, NBAR = B_DONE + 1;
+                       B_OEMPTY = B_OFULL + 2, B_DONE = B_OEMPTY + 2, B_MATE = B_DONE + 1, NBAR = B_MATE + 1;
   static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
-  static constexpr uint32_t SMEM_USED = MISC_OFF + 16;
+  static constexpr uint32_t MATE_OFF = MISC_OFF + 16;  // [2][128] fp32, shared-step items
+  static constexpr uint32_t SMEM_USED = MATE_OFF + 1024;
   static constexpr uint32_t SMEM_ALLOC = SMEM_USED + 1024;  // slack for 1024-byte alignment
   static constexpr uint32_t TM_S0 = 0, TM_S1 = 128, TM_O0 = 256, TM_O1 = 256 + D;
   // At D = 64 (16-bit inputs) the Q tiles also live in TMEM (32 columns of
@@ -97,6 +103,10 @@ struct FwdLayout {
   static constexpr int NTHREADS = 320;
 };
 
+// Mask and division of the work: the dense forward, the window with pairs of Q
+// tiles as items, or the window with single Q tiles as items (few of them).
+constexpr int kDense = 0, kWindow = 1, kWindowSplit = 2;
+
 struct FwdItem {
   int b, h, hkv, q0;
   int n[2];  // KV tiles visited by Q tile 0 / 1 (0 = tile lies past L)
@@ -105,7 +115,7 @@ struct FwdItem {
   int ns, lo, hole;
 };
 
-template <bool WIN>
+template <int WIN>
 __device__ __forceinline__ FwdItem fwd_decode(int item, const FwdParams& p) {
   FwdItem it;
   int bh, qp;
@@ -127,6 +137,7 @@ __device__ __forceinline__ FwdItem fwd_decode(int item, const FwdParams& p) {
   it.hkv = it.h / (p.H / p.Hkv);
   it.q0 = qp * 256;
   if constexpr (WIN) {
+    if (WIN == kWindowSplit) it.q0 = qp * 128;
     const int n_sink = (p.sinks + 127) / 128;
     const int a0 = it.q0 + p.past;  // position of the pair's first row
     const int lo1 = max(a0 + 128 - p.window + 1, 0) / 128;
@@ -135,6 +146,14 @@ __device__ __forceinline__ FwdItem fwd_decode(int item, const FwdParams& p) {
     // Rows past Lq lie past Lk too; a tile with any row inside has a last
     // visible tile of at least its own window's first.
     it.n[0] = it.ns + min((a0 + 127) / 128 + 1, p.n_kv) - it.lo;
+    if constexpr (WIN == kWindowSplit) {
+      // Ends of the warpgroups' steps: behind their last one.
+      const int n = it.n[0];
+      it.n[0] = (n & 1) ? n : n - 1;
+      it.n[1] = (n & 1) ? n - 1 : n;
+      it.hole = -1;
+      return it;
+    }
     it.n[1] = it.q0 + 128 < p.Lq ? it.ns + min((a0 + 255) / 128 + 1, p.n_kv) - it.lo : 0;
     it.hole = (it.n[1] > 0 && lo1 > it.lo && n_sink <= it.lo) ? it.ns : -1;
   } else {
@@ -173,20 +192,22 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
 
 // Does Q tile t visit step j of the item / is it its first step, and which
 // K/V tile is it.
-template <bool WIN>
+template <int WIN>
 __device__ __forceinline__ bool fwd_visits(const FwdItem& it, int t, int j) {
+  if (WIN == kWindowSplit) return j < it.n[t] && (j & 1) == t;
   return j < it.n[t] && (!WIN || t == 0 || j != it.hole);
 }
-template <bool WIN>
+template <int WIN>
 __device__ __forceinline__ bool fwd_first(const FwdItem& it, int t, int j) {
+  if (WIN == kWindowSplit) return j == t;
   return j == ((WIN && t == 1 && it.hole == 0) ? 1 : 0);
 }
-template <bool WIN>
+template <int WIN>
 __device__ __forceinline__ int fwd_kv_tile(const FwdItem& it, int j) {
   return !WIN || j < it.ns ? j : it.lo + j - it.ns;
 }
 
-template <int D, bool BF16, bool FP8 = false, bool WIN = false>
+template <int D, bool BF16, bool FP8 = false, int WIN = kDense>
 __global__ void __launch_bounds__(320, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
@@ -224,6 +245,7 @@ __global__ void __launch_bounds__(320, 1)
       mbar_init(bar(Ly::B_OEMPTY + t), 4);
     }
     mbar_init(bar(Ly::B_DONE), 1);
+    mbar_init(bar(Ly::B_MATE), 4);
     ab->flag = 0;
     fence_barrier_init();
   }
@@ -258,8 +280,9 @@ __global__ void __launch_bounds__(320, 1)
           ok = false;
           break;
         }
-        mbar_arrive_expect_tx(bar(Ly::B_QFULL), 2 * Ly::TILE);
-        for (int t = 0; t < 2; ++t)
+        constexpr int q_tiles = WIN == kWindowSplit ? 1 : 2;
+        mbar_arrive_expect_tx(bar(Ly::B_QFULL), q_tiles * Ly::TILE);
+        for (int t = 0; t < q_tiles; ++t)
           for (int c = 0; c < Ly::KCH; ++c)
             tma_load_4d(base + Ly::Q_OFF + t * Ly::TILE + c * Ly::CHUNK, &tmQ, bar(Ly::B_QFULL),
                         c * (128 / Ly::EB), it.h, it.q0 + 128 * t, it.b);
@@ -317,7 +340,8 @@ __global__ void __launch_bounds__(320, 1)
       // (>> 4) to the start-address field, which stays below 2^14.
       // K of pair `ps` is its second tile, V its first.
       auto issue_s = [&](int t, uint32_t ps) {
-        const uint64_t qd = sdesc_sw128(base + Ly::Q_OFF + t * Ly::TILE, 16, 1024);
+        const int qt = WIN == kWindowSplit ? 0 : t;  // the Q tile
+        const uint64_t qd = sdesc_sw128(base + Ly::Q_OFF + qt * Ly::TILE, 16, 1024);
         const uint64_t kd =
             sdesc_sw128(base + Ly::RING_OFF + (2 * ps + 1) * Ly::TILE, 16, 1024);
         if (elect_one()) {
@@ -327,7 +351,7 @@ __global__ void __launch_bounds__(320, 1)
             if constexpr (FP8)
               mma_ss_f8(tS(t), qd + off, kd + off, IDESC_S, k > 0 ? 1u : 0u);
             else if constexpr (Ly::Q_TMEM)
-              mma_ts(tS(t), tmem + (t ? Ly::TM_Q1 : Ly::TM_Q0) + 8u * k, kd + off, IDESC_S,
+              mma_ts(tS(t), tmem + (qt ? Ly::TM_Q1 : Ly::TM_Q0) + 8u * k, kd + off, IDESC_S,
                      k > 0 ? 1u : 0u);
             else
               mma_ss(tS(t), qd + off, kd + off, IDESC_S, k > 0 ? 1u : 0u);
@@ -376,6 +400,7 @@ __global__ void __launch_bounds__(320, 1)
           if (elect_one()) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
+              if (WIN == kWindowSplit && t == 1) break;
               const uint64_t qd = sdesc_sw128(base + Ly::Q_OFF + t * Ly::TILE, 16, 1024);
 #pragma unroll
               for (int k = 0; k < Ly::KS_S; ++k)
@@ -401,6 +426,11 @@ __global__ void __launch_bounds__(320, 1)
         for (int j = 0; ok && j < nmax; ++j) {
           // Pair j+1 holds V_j and K_{j+1}.
           if (!take(ps, 203)) { ok = false; break; }
+          if (WIN == kWindowSplit && j + 1 < nmax) {
+            // The other warpgroup's next step, ahead of this one's P.
+            issue_s((j + 1) & 1, ps);
+            commit(Ly::B_SFULL + ((j + 1) & 1));
+          }
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             uint32_t& p_cnt = t ? p_cnt1 : p_cnt0;
@@ -431,7 +461,7 @@ __global__ void __launch_bounds__(320, 1)
                 ++o_uses;
               }
             }
-            if (fwd_visits<WIN>(it, t, j + 1)) {
+            if (fwd_visits<WIN>(it, t, j + 1) && WIN != kWindowSplit) {
               issue_s(t, ps);
               commit(Ly::B_SFULL + t);
             }
@@ -455,7 +485,7 @@ __global__ void __launch_bounds__(320, 1)
     const uint32_t tS = tmem + lane_off + (t ? Ly::TM_S1 : Ly::TM_S0);
     const uint32_t tO = tmem + lane_off + (t ? Ly::TM_O1 : Ly::TM_O0);
     const float sl2 = p.sl2;
-    uint32_t s_cnt = 0, o_cnt = 0;
+    uint32_t s_cnt = 0, o_cnt = 0, mates = 0;
     bool ok = true;
     for (int round = 0; ok && round * static_cast<int>(gridDim.x) < p.n_items; ++round) {
         const int item = fwd_item_of(round);
@@ -463,7 +493,7 @@ __global__ void __launch_bounds__(320, 1)
       const FwdItem it = fwd_decode<WIN>(item, p);
       const int n = it.n[t];
       if (n == 0) continue;
-      const int tile_lo = it.q0 + 128 * t;
+      const int tile_lo = it.q0 + (WIN == kWindowSplit ? 0 : 128 * t);
       const int q = tile_lo + r;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
@@ -612,10 +642,37 @@ __global__ void __launch_bounds__(320, 1)
         l = l * alpha + rs;
       }
       if (!ok) break;
+      float* mate = reinterpret_cast<float*>(gbase + Ly::MATE_OFF);  // [2][128] m, l
+      if (WIN == kWindowSplit && t == 1) {
+        // Warpgroup 0 finishes the tile (and releases both O).
+        mate[r] = m;
+        mate[128 + r] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Ly::B_MATE));
+        continue;
+      }
       // ---- epilogue: O / l, LSE
       if (!mbar_wait_warp(bar(Ly::B_OFULL + t), o_cnt & 1, ab, err, 302)) { ok = false; break; }
       ++o_cnt;
       tc_fence_after();
+      const bool join = WIN == kWindowSplit && it.n[1] > 0;
+      float f0 = 1.f, f1 = 0.f;  // factors of O_0 and O_1
+      if (join) {
+        if (!mbar_wait_warp(bar(Ly::B_MATE), mates & 1, ab, err, 303) ||
+            !mbar_wait_warp(bar(Ly::B_OFULL + 1), mates & 1, ab, err, 304)) {
+          ok = false;
+          break;
+        }
+        ++mates;
+        tc_fence_after();
+        const float m1 = mate[r], l1 = mate[128 + r], top = fmaxf(m, m1);
+        // (a row may see nothing of one warpgroup's steps, or be past Lq and see
+        // nothing at all)
+        f0 = m == -INFINITY ? 0.f : ex2((m - top) * sl2);
+        f1 = m1 == -INFINITY ? 0.f : ex2((m1 - top) * sl2);
+        l = l * f0 + l1 * f1;
+        m = top;
+      }
       const float inv = l > 0.f ? p.o_scale / l : 0.f;
       T* orow = reinterpret_cast<T*>(p.O) + ((static_cast<size_t>(it.b) * p.Lq + q) * p.H + it.h) * D;
 #pragma unroll
@@ -623,6 +680,14 @@ __global__ void __launch_bounds__(320, 1)
         uint32_t o[32];
         tmem_ld32(tO + 32 * cc, o);
         tmem_ld_wait32(o);
+        if (WIN == kWindowSplit && join) {
+          uint32_t o1[32];
+          tmem_ld32(tO + (Ly::TM_O1 - Ly::TM_O0) + 32 * cc, o1);
+          tmem_ld_wait32(o1);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            o[i] = __float_as_uint(fmaf(__uint_as_float(o[i]), f0, __uint_as_float(o1[i]) * f1));
+        }
         uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -640,6 +705,7 @@ __global__ void __launch_bounds__(320, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(Ly::B_OEMPTY + t));
+      if (WIN == kWindowSplit && join && lane == 0) mbar_arrive(bar(Ly::B_OEMPTY + 1));
     }
   }
 
