@@ -514,13 +514,33 @@ __global__ void __launch_bounds__(320, 1)
         const bool need_mask = (k0 + 128 > p.Lk) || (p.causal && k0 + 127 > tile_lo + p.past);
         if constexpr (WIN) {
           // Tiles that straddle the diagonal, the window's start or the last
-          // sink key; hidden: key >= lim, or sinks <= key < wlo.
-          const int a = q + p.past;
+          // sink key.  A row sees keys [lo, hi) of the tile, and where a tile
+          // holds both sinks and the window's start not those between; one
+          // loop for each bound that cuts some row of the warp (most tiles have
+          // one: 2 instructions a score instead of 4 for the whole condition).
           if (need_mask || (k0 + p.window <= tile_lo + 127 + p.past && k0 + 128 > p.sinks)) {
-            const int lim = min(a + 1, p.Lk) - k0, wlo = a - p.window + 1 - k0, snk = p.sinks - k0;
+            const int a = q + p.past, snk = p.sinks - k0;
+            int hi = min(a + 1, p.Lk) - k0, lo = a - p.window + 1 - k0, gap = 0;
+            if (snk > 0) {
+              if (lo >= 128) hi = min(hi, snk);
+              else if (lo > snk) gap = lo;
+              lo = 0;
+            }
+            if (__any_sync(0xffffffffu, hi < 128)) {
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c >= lim || (c < wlo && c >= snk)) sr[c] = __float_as_uint(-INFINITY);
+              for (int c = 0; c < 128; ++c)
+                if (c >= hi) sr[c] = __float_as_uint(-INFINITY);
+            }
+            if (__any_sync(0xffffffffu, lo > 0)) {
+#pragma unroll
+              for (int c = 0; c < 128; ++c)
+                if (c < lo) sr[c] = __float_as_uint(-INFINITY);
+            }
+            if (__any_sync(0xffffffffu, gap > 0)) {
+#pragma unroll
+              for (int c = 0; c < 128; ++c)
+                if (c >= snk && c < gap) sr[c] = __float_as_uint(-INFINITY);
+            }
           }
         } else if (need_mask) {
           const int lim = p.causal ? min(q + p.past + 1, p.Lk) : p.Lk;  // keys [0, lim) visible
