@@ -130,6 +130,7 @@ fa_status run_paged_decode(const PagedDecodeArgs& a, cudaStream_t s) {
   p.Hkv = a.Hkv;
   p.g = a.H / a.Hkv;
   p.rows = p.g * a.Lq;
+  p.ginv = 65536 / p.g + 1;
   p.page = a.page;
   p.max_pages = a.max_pages;
   p.cap = static_cast<int>(cap);

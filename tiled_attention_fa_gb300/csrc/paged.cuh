@@ -63,6 +63,7 @@ struct PagedParams {
   float* part_lse;   // [2 G, rows], log2 units
   float* scores;     // [B * Hkv, max_tiles, rows, 128] raw scores for the weights, or NULL
   int B, Lq, H, Hkv, g, rows;
+  int ginv;                  // 65536 / g + 1: row / g = row * ginv >> 16 for the rows there are (128 at most)
   int page, max_pages, cap;  // cap = max_pages * page
   int max_tiles;             // ceil(cap / 128)
   int window, sinks;         // window 0: none (then sinks 0)
@@ -307,8 +308,9 @@ __device__ __forceinline__ PagedWalk paged_walk(const PagedParams& p, const int*
 // Count an arrival at an item of n parts; true for the last one.  The word needs
 // no initialisation: whatever lies there without this call's nonce counts as
 // none, and the last arrival leaves 0, so a captured call can be replayed.
-__device__ __forceinline__ int paged_count_in(unsigned long long* word, unsigned long long nonce, int n) {
-  unsigned long long old = 0;  // as every call leaves it
+// `old`: the word as it was read a while ago, so that the first swap mostly fits.
+__device__ __forceinline__ int paged_count_in(unsigned long long* word, unsigned long long nonce, int n,
+                                              unsigned long long old) {
   for (;;) {  // ends: a failed swap means that another part counted itself in
     const unsigned long long seen = (old >> 16) == nonce ? (old & 0xFFFFu) : 0ull;
     const bool last = static_cast<int>(seen) + 1 == n;
@@ -319,57 +321,76 @@ __device__ __forceinline__ int paged_count_in(unsigned long long* word, unsigned
 }
 
 // The joined O and LSE of an item from `n` partials, in slots slot0, then
-// slot1, slot1 + 2, ...; 128 threads, thread = head dim (D = 64: the two halves
-// take alternate rows).  One pass with the running maximum, C partials of RB
-// rows read at a time: what it costs is the L2's latency, so as many reads as
-// the registers hold are under way at once.  Reads past L1: other SMs wrote them.
-template <int D, typename T>
+// slot1, slot1 + 2, ...; 128 threads, four head dims of U rows each.  One pass
+// with the running maximum over C partials at a time.  What it costs is the
+// latency of the L2 beside a full memory bus (about 2000 cycles), so a round's
+// U * C reads go out together: past the last row or partial they repeat the last
+// one with no weight instead of standing under a condition, and the warp meets
+// before the first is used, or the compiler spreads them between their uses (16
+// rows of 3 partials: 17,500 cycles with conditions and a float per read, 7400
+// without the meeting, 3500 so).
+// Reads past L1: other SMs wrote them.
+template <int D, typename T, int R>
 __device__ __forceinline__ void paged_join(const PagedParams& p, int b, int hkv, int slot0, int slot1,
                                            int n) {
-  constexpr int HALVES = 128 / D;
-  constexpr int RB = 4, C = 8;
-  const int d = threadIdx.x % D, half = (threadIdx.x & 127) / D;
-  for (int r0 = half; r0 < p.rows; r0 += RB * HALVES) {
-    float mx[RB], den[RB], acc[RB];
+  constexpr int U = R * (D / 4) >= 512 ? 4 : R * (D / 4) >= 256 ? 2 : 1, C = 16 / U;
+  constexpr int PER_ROW = D / 4, ROWS = 128 / PER_ROW;  // threads of a row, rows of a step
+  const int d = (threadIdx.x % PER_ROW) * 4, rt = (threadIdx.x & 127) / PER_ROW;
+#pragma unroll 1
+  for (int r0 = rt; r0 - rt < p.rows; r0 += U * ROWS) {  // as often for every lane
+    float mx[U], den[U];
+    float4 acc[U];
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      mx[r] = -INFINITY;
-      den[r] = acc[r] = 0.f;
+    for (int u = 0; u < U; ++u) {
+      mx[u] = -INFINITY;
+      den[u] = 0.f;
+      acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
+#pragma unroll 1
     for (int q0 = 0; q0 < n; q0 += C) {
-      float ls[C][RB], o[C][RB];
+      float ls[C][U];
+      float4 o[C][U];
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const size_t slot = q0 + c == 0 ? slot0 : slot1 + 2 * (q0 + c - 1);
+        const int q = min(q0 + c, n - 1);
+        const size_t slot = q == 0 ? slot0 : slot1 + 2 * (q - 1);
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-          const bool in = q0 + c < n && r0 + r * HALVES < p.rows;
-          const size_t at = slot * p.rows + r0 + r * HALVES;
-          ls[c][r] = in ? __ldcg(p.part_lse + at) : -INFINITY;
-          o[c][r] = in ? __ldcg(p.part_o + at * D + d) : 0.f;
+        for (int u = 0; u < U; ++u) {
+          const size_t at = slot * p.rows + min(r0 + u * ROWS, p.rows - 1);
+          ls[c][u] = __ldcg(p.part_lse + at);
+          o[c][u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + d));
         }
       }
+      __syncwarp();  // all reads out before the first is used
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-          const float m = fmaxf(mx[r], ls[c][r]);
-          const float old = m == -INFINITY ? 0.f : ex2(mx[r] - m), w = m == -INFINITY ? 0.f : ex2(ls[c][r] - m);
-          den[r] = fmaf(den[r], old, w);
-          acc[r] = fmaf(acc[r], old, w * o[c][r]);
-          mx[r] = m;
+        for (int u = 0; u < U; ++u) {
+          const bool in = q0 + c < n;
+          const float l = in ? ls[c][u] : -INFINITY;
+          const float m = fmaxf(mx[u], l);
+          const float old = m == -INFINITY ? 0.f : ex2(mx[u] - m), w = m == -INFINITY ? 0.f : ex2(l - m);
+          den[u] = fmaf(den[u], old, w);
+          acc[u].x = fmaf(acc[u].x, old, in ? w * o[c][u].x : 0.f);
+          acc[u].y = fmaf(acc[u].y, old, in ? w * o[c][u].y : 0.f);
+          acc[u].z = fmaf(acc[u].z, old, in ? w * o[c][u].z : 0.f);
+          acc[u].w = fmaf(acc[u].w, old, in ? w * o[c][u].w : 0.f);
+          mx[u] = m;
         }
     }
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      const int row = r0 + r * HALVES;
-      if (row >= p.rows) break;
-      const int ql = row / p.g, h = hkv * p.g + row - ql * p.g;
-      reinterpret_cast<T*>(p.O)[((static_cast<size_t>(b) * p.Lq + ql) * p.H + h) * D + d] =
-          static_cast<T>(den[r] > 0.f ? __fdividef(acc[r], den[r]) : 0.f);
-      if (d == 0)
-        p.LSE[(static_cast<size_t>(b) * p.H + h) * p.Lq + ql] =
-            den[r] > 0.f ? (mx[r] + __log2f(den[r])) * 0.6931471805599453f : -INFINITY;
+    for (int u = 0; u < U; ++u) {
+      const int row = r0 + u * ROWS;
+      if (row < p.rows) {
+        const int ql = row * p.ginv >> 16, h = hkv * p.g + row - ql * p.g;
+        const float inv = den[u] > 0.f ? __fdividef(1.f, den[u]) : 0.f;
+        *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.O) +
+                                  ((static_cast<size_t>(b) * p.Lq + ql) * p.H + h) * D + d) =
+            make_uint2(pack2<T>(acc[u].x * inv, acc[u].y * inv), pack2<T>(acc[u].z * inv, acc[u].w * inv));
+        if (d == 0)
+          p.LSE[(static_cast<size_t>(b) * p.H + h) * p.Lq + ql] =
+              den[u] > 0.f ? (mx[u] + __log2f(den[u])) * 0.6931471805599453f : -INFINITY;
+      }
     }
   }
 }
@@ -833,8 +854,9 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
           }
           if (wq == 0 && lane < CW && rr < p.rows) {
             const float lse2 = sum > 0.f ? top * sl2 + __log2f(sum) : -INFINITY;
+            const int ql = rr * p.ginv >> 16;
             if (direct)
-              p.LSE[(static_cast<size_t>(w.b) * p.H + w.hkv * p.g + rr % p.g) * p.Lq + rr / p.g] =
+              p.LSE[(static_cast<size_t>(w.b) * p.H + w.hkv * p.g + rr - ql * p.g) * p.Lq + ql] =
                   lse2 * 0.6931471805599453f;
             else
               p.part_lse[static_cast<size_t>(slot) * p.rows + rr] = lse2;
@@ -858,22 +880,28 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
             for (int x = 0; x < Ly::NG; ++x) tmem_ld16(tO + x * N + OC * c, o[x]);
 #pragma unroll
             for (int x = 0; x < Ly::NG; ++x) tmem_ld_wait16(o[x]);
+            float v[OC];
 #pragma unroll
             for (int r = 0; r < OC; ++r) {
               const int rr = c * OC + r;
-              if (rr < R && rr < p.rows) {
-                float v = has[0] ? __uint_as_float(o[0][r]) * mbuf[rr] : 0.f;
-                if constexpr (Ly::NG == 2)
-                  if (has[1]) v = fmaf(__uint_as_float(o[1][r]), al[rr], v);
-                if (direct)
-                  dst[static_cast<size_t>(hh) * D] = static_cast<T>(v);
-                else
-                  part[rr * D] = v;
-                if (++hh == p.g) {  // next query
-                  hh = 0;
-                  dst += static_cast<size_t>(p.H) * D;
+              if (rr >= R) break;
+              v[r] = has[0] ? __uint_as_float(o[0][r]) * mbuf[rr] : 0.f;
+              if constexpr (Ly::NG == 2) v[r] = has[1] ? fmaf(__uint_as_float(o[1][r]), al[rr], v[r]) : v[r];
+            }
+            if (!direct) {
+#pragma unroll
+              for (int r = 0; r < OC; ++r)
+                if (c * OC + r < R && c * OC + r < p.rows) part[(c * OC + r) * D] = v[r];
+            } else {
+#pragma unroll
+              for (int r = 0; r < OC; ++r)
+                if (c * OC + r < R && c * OC + r < p.rows) {
+                  dst[static_cast<size_t>(hh) * D] = static_cast<T>(v[r]);
+                  if (++hh == p.g) {  // next query
+                    hh = 0;
+                    dst += static_cast<size_t>(p.H) * D;
+                  }
                 }
-              }
             }
           }
         }
@@ -885,13 +913,15 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
           const int start = t0 + i - w.k;  // the item's first tile
           const int c0 = paged_part_of(total, G, start);
           const int c1 = paged_part_of(total, G, start + w.s.cnt - 1);
+          unsigned long long* word = p.count + c0;
+          const unsigned long long word_was = t == 0 ? __ldcg(word) : 0ull;
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(Ly::B_JOIN + 2 * gr));
           if (!mbar_wait_warp(bar(Ly::B_JOIN + 2 * gr), joins & 1, ab, err, 1014)) { ok = false; break; }
           int* flag = plan + 6 + gr;
           if (t == 0) {
             __threadfence();  // the group's partial, before the count
-            const int last = paged_count_in(p.count + c0, p.nonce, c1 - c0 + 1);
+            const int last = paged_count_in(word, p.nonce, c1 - c0 + 1, word_was);
             if (last) __threadfence();  // the count, before the others' partials
             *flag = last;
             mbar_arrive(bar(Ly::B_JOIN + 2 * gr + 1));
@@ -900,7 +930,7 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
           ++joins;
           if (*flag) {
             const int slot0 = 2 * c0 + (start > paged_part(total, G, c0) ? 1 : 0);
-            paged_join<D, T>(p, w.b, w.hkv, slot0, 2 * (c0 + 1), c1 - c0 + 1);
+            paged_join<D, T, R>(p, w.b, w.hkv, slot0, 2 * (c0 + 1), c1 - c0 + 1);
           }
         }
       }
