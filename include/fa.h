@@ -39,7 +39,7 @@ typedef enum {
                                 nothing was launched */
   FA_ERR_CUDA = 3,           /* a CUDA runtime call or kernel launch failed */
   FA_ERR_DEVICE_TIMEOUT = 4, /* a kernel gave up a bounded wait (see fa_check_device_error) */
-  FA_ERR_SCRATCH_TOO_SMALL = 5 /* fa_bwd_noalloc's fixed scratch or fa_decode's workspace is
+  FA_ERR_SCRATCH_TOO_SMALL = 5 /* fa_bwd_noalloc's fixed scratch or a call's workspace is
                                   smaller than the problem needs; nothing was launched */
 } fa_status;
 
@@ -179,7 +179,11 @@ fa_status fa_paged_write(const void* K, const void* V, void* K_pool, void* V_poo
  * `workspace`: fa_paged_decode_workspace_size bytes, asked with the device
  * that runs the call current (FA_ERR_SCRATCH_TOO_SMALL when smaller); its
  * contents need no initialisation; calls (and replayed graphs) that overlap
- * on the GPU must not share one.
+ * on the GPU must not share one.  (After a device error in a replayed graph,
+ * zero its workspace or capture it again before the next replay: the counts of
+ * the parts that did finish are still in it.)  FA_ERR_UNSUPPORTED also for
+ * 2^31 or more tiles of 128 keys (B * Hkv * ceil(max_pages * page / 128)), and
+ * with `weights` for B * Hkv > 65535.
  */
 size_t fa_paged_decode_workspace_size(int B, int Lq, int H, int Hkv, int D, int page, int max_pages,
                                       int weights);

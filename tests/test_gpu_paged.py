@@ -299,3 +299,30 @@ def test_refusals(cuda_lib):
     assert e.value.status == _lib.FA_ERR_UNSUPPORTED
     torch.cuda.synchronize()
     fa.check_device_error()
+
+
+def test_what_a_call_allocates_belongs_to_its_stream():
+    """With a stream argument, outputs and workspace come from that stream's memory: the current
+    stream's next allocation cannot get them while the kernels run."""
+    B, H, Hkv, D, page = 2, 8, 2, 128, 64
+    k, v, table, lens = cache(B, Hkv, D, "bf16", page, [200, 300], 5)
+    table, lens = table.cuda(), lens.cuda()
+    q = torch.randn(B, 1, H, D).bfloat16().cuda()
+    x = torch.randn(B, 256, H, D).bfloat16().cuda()
+    y = torch.randn(B, 256, Hkv, D).bfloat16().cuda()
+    w = torch.rand(B, Hkv, table.shape[1] * page).cuda()
+    dst = torch.tensor([[11], [12]], dtype=torch.int32).cuda()
+    pools = [torch.zeros(13, page, Hkv, D, dtype=torch.bfloat16).cuda() for _ in range(2)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = list(fa.paged_decode(q, k, v, table, lens, stream=side))
+    o, lse = fa.window_fwd(x, y, y, 100, 4, stream=side)
+    outs += [o, lse, fa.key_weights(x, y, lse, True, 100, 4, stream=side)]
+    outs += fa.window_attention_backward(x, y, y, o, lse, o, 100, 4, stream=side)[:3]
+    outs += fa.paged_evict(*pools, table % 11, lens, w, dst, 32, stream=side)
+    torch.cuda.synchronize()
+    fa.check_device_error()
+    for t in outs:
+        owner = [s["stream"] for s in torch.cuda.memory_snapshot()
+                 if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]]
+        assert owner == [side.cuda_stream]

@@ -187,3 +187,16 @@ def test_one_tile_per_cta(cuda_lib, B, H, Lq, Lk, D, window, sinks):
     O, lse_r, bound = ref.forward(q, k, v, mask, "bf16")
     within(o, O, bound, "O")
     within(lse, lse_r, np.full(lse_r.shape, ref.FP32), "LSE")
+
+
+def test_a_refused_backward_leaves_everything_alone():
+    """No part of a refused call runs, the step that sums O dO among them."""
+    x = torch.randn(1, 200, 2, 64, device="cuda").half()
+    lse = torch.zeros(1, 2, 200, device="cuda")
+    delta, dq, ws = torch.full_like(lse, 7.0), torch.full_like(x, 7.0), torch.full((1 << 20,), 7, dtype=torch.uint8, device="cuda")
+    for window, sinks, w in ((0, 0, ws), (64, -1, ws), (64, 0, ws[:1024])):
+        with pytest.raises(_lib.FAError):
+            _lib.check("fa_window_bwd", _lib.binding().window_bwd(
+                x, x, x, x, lse, x, delta, window, sinks, dq, None, None, w, False, None))
+    torch.cuda.synchronize()
+    assert (delta == 7).all() and (dq == 7).all() and (ws == 7).all()

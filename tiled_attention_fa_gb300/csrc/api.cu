@@ -425,7 +425,7 @@ const char* fa_status_string(fa_status s) {
     case FA_ERR_DEVICE_TIMEOUT: return "a kernel gave up a bounded wait";
     case FA_ERR_SCRATCH_TOO_SMALL:
       return "scratch too small: the problem needs more than fa_bwd_noalloc's fixed array or "
-             "the fa_decode workspace given";
+             "the workspace given";
   }
   return "unknown status";
 }

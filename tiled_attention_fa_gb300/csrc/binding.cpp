@@ -12,6 +12,7 @@
 
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <climits>
@@ -90,19 +91,39 @@ int number(PyObject* o, const char* name) {
   return static_cast<int>(v);
 }
 
-// A stream object, a raw handle, or None for the current stream.
-void* stream_of(PyObject* o, int dev) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
-  PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
-  if (h == nullptr) {
-    PyErr_Clear();
-    Py_INCREF(o);
-    h = o;
+// The stream of a call: a stream object, a raw handle, or None for the current
+// stream.  While it lives, what the call allocates belongs to that stream, so
+// that its memory is not given to another's work before the kernels are done.
+class Stream {
+ public:
+  Stream(PyObject* o, int dev) {
+    const auto d = static_cast<c10::DeviceIndex>(dev);
+    if (o == Py_None) {
+      handle_ = c10::cuda::getCurrentCUDAStream(d).stream();
+      return;
+    }
+    PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
+    if (h == nullptr) {
+      PyErr_Clear();
+      Py_INCREF(o);
+      h = o;
+    }
+    handle_ = PyLong_AsVoidPtr(h);
+    Py_DECREF(h);
+    if (handle_ == nullptr && PyErr_Occurred()) throw python_error();
+    guard_.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle_), d));
   }
-  void* p = PyLong_AsVoidPtr(h);
-  Py_DECREF(h);
-  if (p == nullptr && PyErr_Occurred()) throw python_error();
-  return p;
+  operator void*() const { return handle_; }
+
+ private:
+  void* handle_ = nullptr;
+  c10::cuda::OptionalCUDAStreamGuard guard_;
+};
+
+bool truth(PyObject* o) {
+  const int r = PyObject_IsTrue(o);
+  if (r < 0) throw python_error();
+  return r == 1;
 }
 
 int dtype_code(const Tensor& t) {
@@ -202,12 +223,13 @@ PyObject* window_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   want(k, "k", kv, dt, dev);
   const Tensor& v = wanted(a[2], "v", kv, dt, dev);
   const int window = number(a[3], "window"), sinks = number(a[4], "sinks");
+  const Stream stream(a[7], dev);
   const Tensor out = output(a[5], "out", q.sizes(), dt, dev, q);
   const Tensor lse = output(a[6], "lse", ls, kF32, dev, q);
   const fa_status st =
       fa_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr<float>(),
                     small(s.a), small(s.b), small(c.b), small(s.c), small(c.c), small(s.d), window,
-                    sinks, code, stream_of(a[7], dev));
+                    sinks, code, stream);
   return st == FA_OK ? tuple_of({out, lse}) : status(st);
   END_HANDLE_TH_ERRORS
 }
@@ -232,21 +254,20 @@ PyObject* window_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int window = number(a[7], "window"), sinks = number(a[8], "sinks");
   const int B = small(s.a), L = small(s.b), Lk = small(c.b), H = small(s.c), Hkv = small(c.c),
             D = small(s.d);
-  const bool prep = a[3] != Py_None;
+  const bool prep = a[3] != Py_None, zeroed = a[12] != Py_None && truth(a[13]);
+  const Stream stream(a[14], dev);
   if (prep) wanted(a[3], "o", q.sizes(), dt, dev);
   const Tensor delta = output(a[6], "delta", ls, kF32, dev, q);
   if (!prep && a[6] == Py_None) fail(PyExc_TypeError, "delta must be a CUDA tensor");
   const Tensor dq = output(a[9], "dq", q.sizes(), dt, dev, q);
   const Tensor dk = output(a[10], "dk", kv, dt, dev, q);
   const Tensor dv = output(a[11], "dv", kv, dt, dev, q);
-  const Tensor ws = workspace(a[12], fa_window_bwd_workspace_size(B, L, Lk, H, Hkv, D, window, sinks), dev, q);
+  const size_t need = fa_window_bwd_workspace_size(B, L, Lk, H, Hkv, D, window, sinks);  // 0: refused below
+  const Tensor ws = workspace(a[12], need, dev, q);
   const size_t bytes = ws.numel() * ws.element_size();
-  const bool zeroed = a[12] != Py_None && PyObject_IsTrue(a[13]) == 1;
-  void* stream = stream_of(a[14], dev);
+  if (bytes < need) return status(FA_ERR_SCRATCH_TOO_SMALL);
   fa_status st = FA_OK;
-  if (prep) {
-    // Before anything runs: the accumulator that the preprocess zeroes must fit.
-    if (bytes < fa_bwd_workspace_size(B, L, H, D)) return status(FA_ERR_SCRATCH_TOO_SMALL);
+  if (prep && need != 0) {
     st = fa_bwd_preprocess(THPVariable_Unpack(a[3]).data_ptr(), grad.data_ptr(),
                            delta.data_ptr<float>(), static_cast<float*>(ws.data_ptr()), B, L, H, D,
                            code, stream);
@@ -286,7 +307,7 @@ PyObject* paged_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return status(fa_paged_write(k.data_ptr(), v.data_ptr(), p.k.data_ptr(), p.v.data_ptr(), p.kst,
                                p.vst, ints(table), ints(start), counts, w, wst, nw, small(s.a),
                                small(s.b), small(p.hkv), small(p.d), small(p.page), small(P),
-                               small(p.pages), code, stream_of(a[9], dev)));
+                               small(p.pages), code, Stream(a[9], dev)));
   END_HANDLE_TH_ERRORS
 }
 
@@ -311,6 +332,7 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   float* w = a[7] == Py_None ? nullptr : weights_of(a[7], s.a, p.hkv, P * p.page, dev, wst);
   const int B = small(s.a), Lq = small(s.b), H = small(s.c), Hkv = small(p.hkv), D = small(p.d),
             page = small(p.page);
+  const Stream stream(a[11], dev);
   const Tensor out = output(a[8], "out", qs, dt, dev, q);
   const Tensor lse = output(a[9], "lse", ls, kF32, dev, q);
   const Tensor ws = workspace(
@@ -318,7 +340,7 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const fa_status st = fa_paged_decode(
       q.data_ptr(), p.k.data_ptr(), p.v.data_ptr(), p.kst, p.vst, ints(table), ints(lens),
       out.data_ptr(), lse.data_ptr<float>(), w, wst, ws.data_ptr(), ws.numel() * ws.element_size(), B,
-      Lq, H, Hkv, D, page, small(P), small(p.pages), window, sinks, code, stream_of(a[11], dev));
+      Lq, H, Hkv, D, page, small(P), small(p.pages), window, sinks, code, stream);
   return st == FA_OK ? tuple_of({out, lse}) : status(st);
   END_HANDLE_TH_ERRORS
 }
@@ -343,6 +365,7 @@ PyObject* paged_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int keep = number(a[6], "keep"), sinks = number(a[7], "sinks"), recent = number(a[8], "recent");
   if (keep < 1) fail(PyExc_ValueError, "keep must be at least 1");
   const int64_t ks[3] = {B, p.hkv, keep}, ns[3] = {B, p.hkv, P2 * p.page};
+  const Stream stream(a[12], dev);
   const Tensor kept = output(a[9], "kept", ks, kI32, dev, k);
   const Tensor new_lens = output(a[10], "new_lens", bs, kI32, dev, k);
   const Tensor new_w = output(a[11], "new_weights", ns, kF32, dev, k);
@@ -350,7 +373,7 @@ PyObject* paged_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
       p.k.data_ptr(), p.v.data_ptr(), p.kst, p.vst, ints(table), ints(lens), w, wst, ints(dst), keep,
       sinks, recent, kept.data_ptr<int>(), new_lens.data_ptr<int>(), new_w.data_ptr<float>(), small(B),
       small(p.hkv), small(p.d), small(p.page), small(P), small(P2), small(p.pages), code,
-      stream_of(a[12], dev));
+      stream);
   return st == FA_OK ? tuple_of({kept, new_lens, new_w}) : status(st);
   END_HANDLE_TH_ERRORS
 }
@@ -368,15 +391,15 @@ PyObject* key_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
   want(q, "q", q.sizes(), dt, dev);
   want(k, "k", kv, dt, dev);
   const Tensor& lse = wanted(a[2], "lse", ls, kF32, dev);
-  const int causal = PyObject_IsTrue(a[3]);
-  if (causal < 0) throw python_error();
+  const int causal = truth(a[3]) ? 1 : 0;
   const int window = number(a[4], "window"), sinks = number(a[5], "sinks");
+  const Stream stream(a[8], dev);
   const Tensor out = output(a[6], "out", os, kF32, dev, q);
   const Tensor ws = workspace(a[7], fa_key_weights_workspace_size(), dev, q);
   const fa_status st = fa_key_weights(
       q.data_ptr(), k.data_ptr(), lse.data_ptr<float>(), out.data_ptr<float>(), ws.data_ptr(),
       ws.numel() * ws.element_size(), small(s.a), small(s.b), small(c.b), small(s.c), small(c.c),
-      small(s.d), causal, window, sinks, code, stream_of(a[8], dev));
+      small(s.d), causal, window, sinks, code, stream);
   return st == FA_OK ? THPVariable_Wrap(out) : status(st);
   END_HANDLE_TH_ERRORS
 }

@@ -3,7 +3,6 @@
 #include <atomic>
 #include <chrono>
 #include <cmath>
-#include <random>
 #include <type_traits>
 
 #include "common.cuh"
@@ -45,9 +44,9 @@ WsPlan ws_plan(int B, int Lq, long long cap, int H, int Hkv, int D, bool weights
 // initialisation (48 bits, not 0).
 unsigned long long call_nonce() {
   static std::atomic<unsigned long long> next{[] {
-    const unsigned long long t =
-        std::chrono::steady_clock::now().time_since_epoch().count() ^
-        (static_cast<unsigned long long>(std::random_device{}()) << 20);
+    const unsigned long long t = std::chrono::steady_clock::now().time_since_epoch().count() ^
+                                 std::chrono::system_clock::now().time_since_epoch().count() << 7 ^
+                                 reinterpret_cast<uintptr_t>(&t) << 20;  // where this process's stack lies
     return t * 0x9E3779B97F4A7C15ull;
   }()};
   const unsigned long long n = next.fetch_add(1) & 0xFFFFFFFFFFFFull;
