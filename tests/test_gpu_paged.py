@@ -326,3 +326,23 @@ def test_what_a_call_allocates_belongs_to_its_stream():
         owner = [s["stream"] for s in torch.cuda.memory_snapshot()
                  if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]]
         assert owner == [side.cuda_stream]
+
+
+@pytest.mark.parametrize("B,Lq,page,lo,hi", [(14, 1, 64, 8000, 16384), (32, 1, 64, 100, 700), (8, 8, 32, 300, 6000),
+                                             (8, 32, 32, 300, 6000)])
+def test_many_runs_under_load_give_the_same_bits(B, Lq, page, lo, hi):
+    """Loads that land late or out of order change nothing.  (Zeroing the unseen rows of an item's
+    last V tile once reached the tile that had the stage before, in four runs of ten at the first
+    of these shapes.)"""
+    P = -(-hi // page)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    k, v = (torch.randn(B * P, page, 8, 128, device="cuda", generator=g).bfloat16() for _ in range(2))
+    q = torch.randn(B, Lq, 32, 128, device="cuda", generator=g).bfloat16()
+    for _ in range(5):
+        table = torch.randperm(B * P, device="cuda", generator=g).int().view(B, P)
+        lens = torch.randint(lo, hi + 1, (B,), device="cuda", generator=g).int()
+        outs = torch.stack([fa.paged_decode(q, k, v, table, lens)[0] for _ in range(40)])
+        torch.cuda.synchronize()
+        fa.check_device_error()
+        differ = [i for i, o in enumerate(outs) if not torch.equal(o, outs[0])]
+        assert not differ

@@ -596,8 +596,12 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
       for (int x = 0; x < w.left; ++x, ++i) {
         const uint32_t pos = min(n_part, i + 1 + Ly::NG) + i, vs = pos % Ly::STAGES;
         const int buf = i % Ly::NB;
-        if (!mbar_wait_warp(bar(Ly::B_KVFULL + vs), (pos / Ly::STAGES) & 1, ab, err, 1005) ||
-            !mbar_wait_warp(bar(Ly::B_PFULL + buf), (i / Ly::NB) & 1, ab, err, 1007)) {
+        // P first: then K_i and all before it have landed, one of which may
+        // have had V_i's stage before it.  (A wait for a phase's parity passes
+        // as well while the phase before it is still open, so whoever waits for
+        // a stage must know that its last fill has landed.)
+        if (!mbar_wait_warp(bar(Ly::B_PFULL + buf), (i / Ly::NB) & 1, ab, err, 1007) ||
+            !mbar_wait_warp(bar(Ly::B_KVFULL + vs), (pos / Ly::STAGES) & 1, ab, err, 1005)) {
           ok = false;
           break;
         }
@@ -785,7 +789,18 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
         }
       }
       if (!whole) {
-        // V rows of keys nobody sees: zero, whatever the page holds there.
+        // V rows of keys nobody sees: zero, whatever the page holds there.  The
+        // stage's last fill must have landed before its next one is waited for:
+        // it was a K up to K_i (S_i is here), or at the latest V_{i - STAGES/2},
+        // which PV_{i-NB}, done before S_i, does not cover when STAGES/2 < NB.
+        // (PV_{i-LAST+NB} needs this tile's P, so that barrier is at most one
+        // phase on.)
+        constexpr int LAST = Ly::STAGES / 2;
+        if (LAST < Ly::NB && i >= LAST &&
+            !mbar_wait_warp(bar(Ly::B_PVDONE + (i - LAST) % Ly::NB), ((i - LAST) / Ly::NB) & 1, ab, err, 1018)) {
+          ok = false;
+          break;
+        }
         const uint32_t vpos = min(n_part, i + 1 + Ly::NG) + i;  // V's place in the ring's order
         if (!mbar_wait_warp(bar(Ly::B_KVFULL + vpos % Ly::STAGES), (vpos / Ly::STAGES) & 1, ab, err, 1011)) {
           ok = false;
