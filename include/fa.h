@@ -167,10 +167,11 @@ fa_status fa_paged_write(const void* K, const void* V, void* K_pool, void* V_poo
  * paged keys and values (already written).  lens [B] counts all keys, the new
  * ones included: query i of sequence b has position a = lens[b] - Lq + i and
  * sees key j iff j <= a and (window == 0, or j > a - window, or j < sinks).
- * A query that sees nothing (a negative position, an empty sequence) gives
- * O = 0, LSE = -inf.  Keys that no query of the call sees are never used,
- * whatever their slots hold; pages wholly behind the length or before the
- * window are not read and may be absent from the table.
+ * A length beyond the table (max_pages * page) counts as the table's, one
+ * below 0 as 0.  A query that sees nothing (a negative position, an empty
+ * sequence) gives O = 0, LSE = -inf.  Keys that no query of the call sees are
+ * never used, whatever their slots hold; pages wholly behind the length or
+ * before the window are not read and may be absent from the table.
  * Q, O [B, Lq, H, D]; LSE [B, H, Lq]; (H / Hkv) * Lq <= 128
  * (FA_ERR_UNSUPPORTED otherwise).  With `weights` the call adds to each
  * visible key's weight sum over the group's heads and the queries of

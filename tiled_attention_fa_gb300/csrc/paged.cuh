@@ -432,6 +432,11 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
     tmem_alloc(base + Ly::MISC_OFF, Ly::TMEM_COLS);
     tmem_relinquish();
   }
+  if (warp == Ly::SW && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
   tc_fence_before();
   // Everything above overlaps the end of the kernel before; nothing of global
   // memory was touched.
@@ -447,7 +452,8 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
     // ------------------------------------------------------------ producer
     // Ring order: the first NG K tiles, then K_{i+NG}, V_i.  Lane j loads the j-th box
     // (a page, or 128 rows of one) of the tile.
-    const int box = min(p.page, 128), nbox = 128 / box, per_batch = 32 / nbox;
+    const int page_log = 31 - __clz(p.page);  // (a page is a power of two)
+    const int box = min(p.page, 128), nbox = 128 >> min(page_log, 7), per_batch = 32 >> (7 - min(page_log, 7));
     uint32_t stage = 0, phase = 0, used = 0, qcnt = 0;
     bool ok = true;
     const uint64_t stream = policy_evict_first();
@@ -460,7 +466,7 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
       if (ahead.rem <= 0) return;
       nxt_n = min(per_batch, ahead.left);
       if (ahead.k < ahead.s.ns) nxt_n = min(nxt_n, ahead.s.ns - ahead.k);  // up to the gap
-      const int at = (ahead.tile * 128 + static_cast<int>(lane) * box) / p.page;
+      const int at = (ahead.tile * 128 + static_cast<int>(lane) * box) >> page_log;
       nxt = (static_cast<int>(lane) < nxt_n * nbox && at < p.max_pages)
                 ? p.table[static_cast<size_t>(ahead.b) * p.max_pages + at]
                 : -1;
