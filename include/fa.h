@@ -301,8 +301,10 @@ fa_status fa_bwd_kv(const void* Q, const void* K, const void* V, const void* O, 
  * zero.  The backward's workspace holds fa_window_bwd_workspace_size bytes
  * (FA_ERR_SCRATCH_TOO_SMALL when smaller): first the fp32 dQ accumulator of
  * fa_bwd_workspace_size(B, Lq, H, D) bytes, which must hold zeros on entry
- * (fa_bwd_preprocess sets them) unless zero_accum, then the parts of the sink
- * keys' dK and dV, which need no initialisation.
+ * (fa_bwd_preprocess sets them) unless zero_accum, then fp32 parts of dK and
+ * dV, which need no initialisation.  Ask for the size with the device that runs
+ * the call current: how the work is cut depends on its SMs.  dK and dV do not
+ * depend on timing; dQ is summed by fp32 atomics, as in fa_bwd.
  */
 fa_status fa_window_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE, int B,
                         int Lq, int Lk, int H, int Hkv, int D, int window, int sinks, int dtype,

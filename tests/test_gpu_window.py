@@ -200,3 +200,22 @@ def test_a_refused_backward_leaves_everything_alone():
                 x, x, x, x, lse, x, delta, window, sinks, dq, None, None, w, False, None))
     torch.cuda.synchronize()
     assert (delta == 7).all() and (dq == 7).all() and (ws == 7).all()
+
+
+@pytest.mark.parametrize("B,Lq,Lk,H,Hkv,D,dtype,window,sinks", [
+    (1, 735, 735, 16, 2, 128, "bf16", 723, 4),      # eight heads a unit's share each, no far units
+    (1, 900, 1100, 12, 2, 64, "fp16", 200, 130),    # six heads, two sink tiles with far units, a past
+    (2, 640, 640, 8, 1, 128, "fp16", 100, 1),
+    (1, 130, 1500, 8, 1, 64, "bf16", 300, 700),     # tiles that no query sees
+])
+def test_few_units_are_cut_by_heads(cuda_lib, B, Lq, Lk, H, Hkv, D, dtype, window, sinks):
+    """dK and dV of a K/V head added up from several units' query heads."""
+    (q, k, v, do), _, _, grads = both(B, Lq, Lk, H, Hkv, D, dtype, window, sinks, seed=H)
+    own = B * Hkv * -(-Lk // 128) * 2 * 128 * D * 4
+    size = fa.window_workspace_size(B, Lq, Lk, H, Hkv, D, window, sinks)
+    assert size >= _lib.load().fa_bwd_workspace_size(B, Lq, H, D) + 2 * own  # (so it is cut)
+    mask = ref.seen(np.arange(Lk - Lq, Lk), Lk, window, sinks)
+    for name, g, r, e in zip(("dQ", "dK", "dV"), grads, *ref.backward(q, k, v, do, mask, dtype)):
+        within(g, r, e, name)
+    unseen = ~mask.any(axis=0)
+    assert not grads[1][:, unseen].any() and not grads[2][:, unseen].any()

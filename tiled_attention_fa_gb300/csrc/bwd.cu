@@ -1,4 +1,5 @@
 // Host launchers of the backward kernels (preprocess, main pass, dQ post-process).
+#include <cmath>
 #include <mutex>
 #include <type_traits>
 
@@ -69,14 +70,46 @@ void plan_window(BwdParams& p, int B, int window, int sinks) {
   }
   p.n_rest = (most + p.chunk - 1) / p.chunk;
   p.n_items = B * p.Hkv * (p.n_kv + p.n_sink * p.n_rest);
+  // Few units of many heads leave SMs idle: cut them by query heads.  Costs in
+  // steps of a 128 x 128 tile: a unit's start and end take about 3, its fp32
+  // parts 1 more and their sum a launch and a share of the traffic.  Whole and
+  // cut, with the dQ post-process: B1 H32/4 L735 D128 window 723 126 and 48 us,
+  // B2 H16/2 L1000 D64 window 300 81 and 32, B1 H8/1 L4000 D128 window 1000 179
+  // and 63.
+  p.hs = 1;
+  const int g = p.H / p.Hkv, sms = sm_count();
+  const double steps = static_cast<double>(g) * (p.chunk < p.n_q ? p.chunk : p.n_q);
+  const double units = static_cast<double>(p.n_items);
+  double best = std::ceil(units / (sms < 1 ? 1 : sms)) * (steps + 3);
+  for (int hs = 2; hs <= g && sms > 0 && units * hs <= 8.0 * sms; ++hs) {
+    if (g % hs != 0) continue;
+    const double cost = std::ceil(units * hs / sms) * (steps / hs + 4) + 2 + units * hs / 100;
+    if (cost < 0.85 * best) {
+      best = cost;
+      p.hs = hs;
+    }
+  }
+  if (p.hs > 1) {
+    p.n_items *= p.hs;
+    p.srows = 128;
+  }
+}
+
+// fp32 parts of dK and dV, of 2 * srows * D elements each.
+size_t window_slots(const BwdParams& p) {
+  const size_t bh = static_cast<size_t>(p.B) * p.Hkv;
+  if (p.hs > 1) return bh * (p.n_kv + static_cast<size_t>(p.n_sink) * p.n_rest) * p.hs;
+  return p.n_rest ? bh * p.n_sink * (1 + p.n_rest) : 0;
 }
 
 size_t dq_bytes(int B, int L, int H, int D) {
   return (static_cast<size_t>(B) * H * padded_len(L) * D * sizeof(float) + 255) / 256 * 256;
 }
 
-BwdParams window_plan(int B, int Lq, int Lk, int Hkv, int window, int sinks) {
+BwdParams window_plan(int B, int Lq, int Lk, int H, int Hkv, int window, int sinks) {
   BwdParams p = {};
+  p.B = B;
+  p.H = H;
   p.Lq = Lq;
   p.Lk = Lk;
   p.past = Lk - Lq;
@@ -90,9 +123,8 @@ BwdParams window_plan(int B, int Lq, int Lk, int Hkv, int window, int sinks) {
 }  // namespace
 
 size_t window_bwd_workspace_size(int B, int Lq, int Lk, int H, int Hkv, int D, int window, int sinks) {
-  const BwdParams p = window_plan(B, Lq, Lk, Hkv, window, sinks);
-  const size_t slots = p.n_rest ? static_cast<size_t>(B) * Hkv * p.n_sink * (1 + p.n_rest) : 0;
-  return dq_bytes(B, Lq, H, D) + slots * 2 * p.srows * D * sizeof(float);
+  const BwdParams p = window_plan(B, Lq, Lk, H, Hkv, window, sinks);
+  return dq_bytes(B, Lq, H, D) + window_slots(p) * 2 * p.srows * D * sizeof(float);
 }
 
 // window > 0 (WIN, causal calls only): the backward of run_window_fwd.
@@ -219,7 +251,7 @@ static fa_status launch_window_bwd(const void* Q, const void* K, const void* V, 
                                    const float* LSE, const float* Delta, void* dQ, void* dK,
                                    void* dV, float* ws, int zero_accum, int B, int Lq, int Lk,
                                    int H, int Hkv, int window, int sinks, cudaStream_t s) {
-  BwdParams p = window_plan(B, Lq, Lk, Hkv, window, sinks);
+  BwdParams p = window_plan(B, Lq, Lk, H, Hkv, window, sinks);
   p.dK = dK;
   p.dV = dV;
   p.scale = 1.f / sqrtf(static_cast<float>(D));
@@ -228,10 +260,13 @@ static fa_status launch_window_bwd(const void* Q, const void* K, const void* V, 
       launch_bwd<D, BF16, true>(Q, K, V, dO, LSE, Delta, dK, dV, ws, zero_accum, B, Lq, Lk, H, Hkv,
                                 1, s, window, sinks, p.sink_part);
   if (st != FA_OK) return st;
-  if (p.n_rest > 0 &&
-      !launch_after(fa_sink_sum_kernel<D, BF16>, dim3(B * Hkv * p.n_sink, (p.srows + 3) / 4),
-                    dim3(2 * D), s, p))
-    return FA_ERR_CUDA;
+  if (p.hs > 1) {
+    if (!launch_after(fa_head_sum_kernel<D, BF16>, dim3(B * Hkv * p.n_kv, 16), dim3(2 * D), s, p))
+      return FA_ERR_CUDA;
+  } else if (p.n_rest > 0) {
+    if (!launch_after(fa_sink_sum_kernel<D, BF16>, dim3(B * Hkv * p.n_sink, (p.srows + 3) / 4), dim3(2 * D), s, p))
+      return FA_ERR_CUDA;
+  }
   return launch_post<D, BF16>(ws, dQ, B, Lq, H, s);
 }
 

@@ -93,9 +93,13 @@ struct BwdParams {
   // every later query; the Q tiles past their windows form n_rest further units
   // each, of `chunk` Q tiles, whose dK, dV of the sink keys (at most srows a
   // tile) go to sink_part [B * Hkv, n_sink, 1 + n_rest, 2, srows, D] (slot 0:
-  // the tile's own unit) and are added up by fa_sink_sum_kernel.
+  // the tile's own unit) and are added up by fa_sink_sum_kernel.  With hs > 1
+  // every unit is cut into hs units of (H / Hkv) / hs query heads; then all rows
+  // of all tiles are joined: sink_part holds [B * Hkv, n_kv, hs, 2, 128, D] for
+  // the tiles' own units, then [B * Hkv, n_sink, n_rest, hs, 2, 128, D] (srows =
+  // 128), and fa_head_sum_kernel adds them up.
   int window, sinks;
-  int n_sink, n_rest, chunk, srows;
+  int n_sink, n_rest, chunk, srows, hs;
   float* sink_part;
 };
 
@@ -167,6 +171,7 @@ struct BwdItem {
   int b, hkv, j;
   int i0;      // first Q tile visited
   int per;     // Q tiles visited per query head
+  int h0;      // WIN: first query head
   int slot;    // WIN: sink_part slot of its sink keys, or -1
   bool rest;   // WIN: a sink tile's Q tiles past its window
   int ntiles;  // (query heads of the group) x (Q tiles visited)
@@ -187,9 +192,11 @@ template <bool WIN>
 __device__ __forceinline__ BwdItem bwd_decode(int item, const BwdParams& p) {
   BwdItem it;
   if constexpr (WIN) {
-    const int units = p.n_kv + p.n_sink * p.n_rest;  // of one (batch, K/V head)
+    const int units = (p.n_kv + p.n_sink * p.n_rest) * p.hs;  // of one (batch, K/V head)
     const int bh = item / units;
     int x = item - bh * units, r = 0;
+    const int part = x % p.hs, heads = p.H / p.Hkv / p.hs;
+    x /= p.hs;
     it.rest = x >= p.n_kv;
     if (it.rest) {
       x -= p.n_kv;
@@ -199,6 +206,7 @@ __device__ __forceinline__ BwdItem bwd_decode(int item, const BwdParams& p) {
     it.j = x;
     it.b = bh / p.Hkv;
     it.hkv = bh - it.b * p.Hkv;
+    it.h0 = it.hkv * (p.H / p.Hkv) + part * heads;
     int lo, reach;
     bwd_win_range(p, it.j, lo, reach);
     if (it.rest) {
@@ -208,10 +216,14 @@ __device__ __forceinline__ BwdItem bwd_decode(int item, const BwdParams& p) {
       it.i0 = lo;
       it.per = reach - lo;
     }
-    it.slot = (p.n_rest > 0 && it.j < p.n_sink)
-                  ? (bh * p.n_sink + it.j) * (1 + p.n_rest) + (it.rest ? 1 + r : 0)
-                  : -1;
-    it.ntiles = (p.H / p.Hkv) * it.per;
+    if (p.hs > 1)
+      it.slot = (it.rest ? p.B * p.Hkv * p.n_kv + (bh * p.n_sink + it.j) * p.n_rest + r : bh * p.n_kv + it.j) * p.hs +
+                part;
+    else
+      it.slot = (p.n_rest > 0 && it.j < p.n_sink)
+                    ? (bh * p.n_sink + it.j) * (1 + p.n_rest) + (it.rest ? 1 + r : 0)
+                    : -1;
+    it.ntiles = heads * it.per;
     return it;
   }
   it.j = item % p.n_kv;
@@ -271,6 +283,7 @@ __device__ __forceinline__ bool bwd_unit_item(int u, int s, const BwdParams& p, 
 }
 
 // n-th (head, Q tile) pair of an item: heads of the group outer, tiles inner.
+template <bool WIN>
 __device__ __forceinline__ void bwd_tile(const BwdItem& it, const BwdParams& p, int n, int& h,
                                          int& i) {
   const int per = it.per;
@@ -279,7 +292,7 @@ __device__ __forceinline__ void bwd_tile(const BwdItem& it, const BwdParams& p, 
   // so the CTAs working on one head at the same time read different Q / dO
   // tiles and add into different dQ accumulator tiles.
   i = it.i0 + (n - g * per + it.j) % per;
-  h = it.hkv * (p.H / p.Hkv) + g;
+  h = (WIN ? it.h0 : it.hkv * (p.H / p.Hkv)) + g;
 }
 
 template <int D, bool BF16, bool WIN = false>
@@ -391,7 +404,7 @@ __global__ void __launch_bounds__(512, 1)
     ++kv_cnt;
     for (int n = 0; n < it.ntiles; ++n) {
       int h, i;
-      bwd_tile(it, p, n, h, i);
+      bwd_tile<WIN>(it, p, n, h, i);
       // dO_i first: its slot frees after the previous occupant's last dV,
       // before Q's (its last dK).
       if (!mbar_wait_warp(bar(Ly::B_DOEMPTY + stage), phase ^ 1u, ab, err, 403)) { ok = false; break; }
@@ -621,7 +634,7 @@ __global__ void __launch_bounds__(512, 1)
     const int kr = it.j * 128 + r;
     for (int n = 0; ok && n < it.ntiles; ++n, ++g) {
       int h, i;
-      bwd_tile(it, p, n, h, i);
+      bwd_tile<WIN>(it, p, n, h, i);
       // S^T(g) and then P^T / dS^T in region R[g % 2]; dP^T(g) in the other.
       const uint32_t tSr = tmem + lane_off + Ly::tm_region(g);
       const uint32_t tPr = tmem + lane_off + Ly::tm_region(g + 1);
@@ -738,8 +751,9 @@ __global__ void __launch_bounds__(512, 1)
       const uint32_t tsrc = tmem + lane_off + (hc == 0 ? Ly::TM_DK : Ly::TM_DV);
       T* row = reinterpret_cast<T*>(dst_base) +
                ((static_cast<size_t>(it.b) * p.Lk + kr) * p.Hkv + it.hkv) * D;
-      // WIN: sink keys' sums are joined over units, in fp32.
-      const bool joint = WIN && it.slot >= 0 && kr < p.sinks;
+      // WIN: sums of sink keys, or of all when heads are cut, are joined over
+      // units, in fp32.
+      const bool joint = WIN && it.slot >= 0 && kr < (p.hs > 1 && !it.rest ? p.Lk : p.sinks);
       float* part = joint ? p.sink_part +
                                 ((static_cast<size_t>(it.slot) * 2 + hc) * p.srows + r) * D
                           : nullptr;
@@ -759,7 +773,7 @@ __global__ void __launch_bounds__(512, 1)
                 make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
           continue;
         }
-        if (WIN && it.rest) continue;  // its other keys are their own unit's
+        if (WIN && (it.rest || p.hs > 1)) continue;  // its other keys are their own unit's, or none
         uint32_t pk[16];
 #pragma unroll
         for (int u = 0; u < 16; ++u)
@@ -789,7 +803,7 @@ __global__ void __launch_bounds__(512, 1)
     if (WIN && it.rest && it.ntiles == 0) continue;
     for (int n = 0; n < it.ntiles; ++n, ++g) {
       int h, i;
-      bwd_tile(it, p, n, h, i);
+      bwd_tile<WIN>(it, p, n, h, i);
       if (!mbar_wait_warp(bar(Ly::B_DQFULL), g & 1, ab, err, 701)) { ok = false; break; }
       tc_fence_after();
       const int q = i * 128 + r;
@@ -864,6 +878,35 @@ __global__ void __launch_bounds__(2 * D) fa_sink_sum_kernel(const BwdParams p) {
   for (int r = blockIdx.y; r < min(128, p.sinks - j * 128); r += gridDim.y) {
     float sum = 0.f;
     for (int u = 0; u < units; ++u) sum += src[u * slot + static_cast<size_t>(r) * D];
+    dst[(static_cast<size_t>(b) * p.Lk + j * 128 + r) * p.Hkv * D] =
+        static_cast<T>(which == 0 ? sum * p.scale : sum);
+  }
+}
+
+// dK, dV of all keys when heads are cut (hs > 1): the sum of their units' fp32
+// parts, the tile's own first.  Block (bh, K/V tile); thread = element of a row.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(2 * D) fa_head_sum_kernel(const BwdParams p) {
+  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  pdl_wait();
+  const int bh = blockIdx.x / p.n_kv, j = blockIdx.x - bh * p.n_kv;
+  const int b = bh / p.Hkv, hkv = bh - b * p.Hkv;
+  const int which = threadIdx.x / D, d = threadIdx.x - which * D;  // 0: dK, 1: dV
+  int lo, reach;
+  bwd_win_range(p, j, lo, reach);
+  const int rest = j < p.n_sink ? (p.n_q - reach + p.chunk - 1) / p.chunk * p.hs : 0;
+  const size_t slot = static_cast<size_t>(2) * 128 * D;
+  const float* src = p.sink_part + static_cast<size_t>(which) * 128 * D + d;
+  const float* own = src + static_cast<size_t>(blockIdx.x) * p.hs * slot;
+  const float* far = src + (static_cast<size_t>(p.B) * p.Hkv * p.n_kv +
+                            (static_cast<size_t>(bh) * p.n_sink + j) * p.n_rest) * p.hs * slot;
+  T* dst = reinterpret_cast<T*>(which == 0 ? p.dK : p.dV) + hkv * D + d;
+  for (int r = blockIdx.y; r < min(128, p.Lk - j * 128); r += gridDim.y) {
+    float sum = 0.f;
+#pragma unroll 4
+    for (int u = 0; u < p.hs; ++u) sum += own[u * slot + static_cast<size_t>(r) * D];
+    if (j * 128 + r < p.sinks)
+      for (int u = 0; u < rest; ++u) sum += far[u * slot + static_cast<size_t>(r) * D];
     dst[(static_cast<size_t>(b) * p.Lk + j * 128 + r) * p.Hkv * D] =
         static_cast<T>(which == 0 ? sum * p.scale : sum);
   }
