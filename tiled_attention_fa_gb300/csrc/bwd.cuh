@@ -251,7 +251,9 @@ __device__ __forceinline__ BwdItem bwd_decode(int item, const BwdParams& p) {
 // heads), round r of the CTAs takes the next gridDim.x of them, CTA c the c-th
 // in even rounds and the (gridDim.x-1-c)-th in odd ones.  The CTAs' loops
 // then run over rounds x gridDim.x units; positions past the tiles are empty.
-// With a window (WIN) every unit costs about the same; units are dealt out one
+// With a window (WIN) every unit costs about the same (B4 H32/8 L4096 D128,
+// window 1024, 4 sinks: 0.72 ms, 0.84 PFLOP/s of visible products; contiguous
+// shares 1.28 ms, every step's Q, dO and dQ from DRAM); units are dealt out one
 // by one in the list's order, so the CTAs running together work on neighbouring
 // K/V tiles of a few heads and share their Q, dO and dQ tiles in L2.
 template <bool WIN>

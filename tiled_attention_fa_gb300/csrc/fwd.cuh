@@ -41,6 +41,10 @@
 // each with a maximum, sum and O of its own, joined by warpgroup 0 at the end
 // (O_0 and O_1 lie in the same TMEM lanes).  A single tile's chain S, softmax, PV
 // would take 3,100 cycles a step with nothing to overlap it.
+// Measured (D128 bf16, H32/8, window 1024, 4 sinks): B1 L8192 0.145 ms, B4 L4096
+// 0.285 ms, 840 TFLOP/s of visible products; visited tiles hold 20% more keys
+// than are visible, so the MMAs run at 1.1 PFLOP/s against the dense causal
+// call's 1.45.
 #pragma once
 
 #include <cuda_bf16.h>
