@@ -312,16 +312,24 @@ __device__ __forceinline__ PagedWalk paged_walk(const PagedParams& p, const int*
 // Count an arrival at an item of n parts; true for the last one.  The word needs
 // no initialisation: whatever lies there without this call's nonce counts as
 // none, and the last arrival leaves 0, so a captured call can be replayed.
-// `old`: the word as it was read a while ago, so that the first swap mostly fits.
+// `cur`: the word as it was read a while ago.  One arrival puts the nonce there,
+// all others add: at most three trips to the L2, however many come at once (with
+// a swap for each, 50 parts of one item took 50 trips).
 __device__ __forceinline__ int paged_count_in(unsigned long long* word, unsigned long long nonce, int n,
-                                              unsigned long long old) {
-  for (;;) {  // ends: a failed swap means that another part counted itself in
-    const unsigned long long seen = (old >> 16) == nonce ? (old & 0xFFFFu) : 0ull;
-    const bool last = static_cast<int>(seen) + 1 == n;
-    const unsigned long long now = atomicCAS(word, old, last ? 0ull : (nonce << 16 | (seen + 1)));
-    if (now == old) return last;
-    old = now;
+                                              unsigned long long cur) {
+  int seen = 0;
+  for (;;) {  // ends: a failed swap means that another part put the nonce there (nothing else writes)
+    if ((cur >> 16) == nonce) {  // (it stays until the last part is here)
+      seen = static_cast<int>(atomicAdd(word, 1ull) & 0xFFFFu);
+      break;
+    }
+    const unsigned long long was = atomicCAS(word, cur, nonce << 16 | 1u);
+    if (was == cur) break;
+    cur = was;
   }
+  const bool last = seen + 1 == n;
+  if (last) atomicExch(word, 0ull);
+  return last;
 }
 
 // The joined O and LSE of an item from `n` partials, in slots slot0, then
