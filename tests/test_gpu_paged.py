@@ -346,3 +346,11 @@ def test_many_runs_under_load_give_the_same_bits(B, Lq, page, lo, hi):
         fa.check_device_error()
         differ = [i for i, o in enumerate(outs) if not torch.equal(o, outs[0])]
         assert not differ
+
+
+@pytest.mark.parametrize("Lq,H,D,dtype,page,n", [(1, 4, 128, "bf16", 64, 9000), (16, 8, 128, "fp16", 64, 5000),
+                                                 (1, 2, 64, "fp16", 128, 9999), (5, 3, 64, "bf16", 16, 3000)])
+def test_one_item_in_many_parts(Lq, H, D, dtype, page, n):
+    """One sequence and K/V head: every part ends together and counts itself in at the same word."""
+    for seed in (1, 2):
+        check(1, Lq, H, 1, D, dtype, page, [n], seed=seed)

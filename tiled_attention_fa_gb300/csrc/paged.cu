@@ -141,7 +141,15 @@ fa_status run_paged_decode(const PagedDecodeArgs& a, cudaStream_t s) {
   const long long most = static_cast<long long>(a.B) * a.Hkv * ((cap + 127) / 128);
   if (most >= (1ll << 31) || sms >= 65536) return FA_ERR_UNSUPPORTED;
   if (a.weights != nullptr && static_cast<long long>(a.B) * a.Hkv > 65535) return FA_ERR_UNSUPPORTED;
-  const int G = most < sms ? static_cast<int>(most) : sms;
+  int G = most < sms ? static_cast<int>(most) : sms;
+  // Few items cut into many parts: whoever joins an item reads all its partials,
+  // rows * D floats each at some 40 GB/s, while a tile takes some 2 us.  So at
+  // most as many parts an item as make the sum of both smallest.  All SMs and so:
+  // B1 H8/1 D128, 16 tokens, 20,000 keys 295 and 96 us; B2 H16/2, 4 tokens, 8,000
+  // keys 64 and 39; B1 H4/1, a token, 30,000 keys 30 and 22.
+  const double parts = std::ceil(std::sqrt(((cap + 127) / 128) * 2.0 / (p.rows * a.D * 4 / 40e3)));
+  const double limit = parts * a.B * a.Hkv;
+  if (limit < G) G = static_cast<int>(limit);
   const bool bf16 = a.dtype == FA_BF16;
   if (a.D == 64) return bf16 ? pick_rows<64, true>(a, p, G, s) : pick_rows<64, false>(a, p, G, s);
   return bf16 ? pick_rows<128, true>(a, p, G, s) : pick_rows<128, false>(a, p, G, s);

@@ -9,7 +9,8 @@
 //
 // Bound by the read of K and V, so the kernel is built to keep that read
 // going without a pause:
-//   - one persistent CTA per SM.  The tiles of all items form one list (item by
+//   - one persistent CTA per SM (fewer when few items would be cut into so many
+//     parts that joining them took longer).  The tiles of all items form one list (item by
 //     item); CTA c takes the c-th of G equal contiguous parts of it, whatever
 //     the lengths are.  Lengths are read on the device: every CTA scans them
 //     once.  An item inside one CTA is written directly; only items cut by a
