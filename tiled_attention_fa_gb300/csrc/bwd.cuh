@@ -386,7 +386,11 @@ __global__ void __launch_bounds__(512, 1)
     int item;
     if (!bwd_unit_item<WIN>(u / p.ipu, u % p.ipu, p, item)) continue;
     const BwdItem it = bwd_decode<WIN>(item, p);
-    if (WIN && it.rest && it.ntiles == 0) continue;
+    // (WIN: keys that no query sees.  Such a unit takes no part in the pipeline;
+    // the compute warps write its zeros.  Nothing would hold the MMA warp back:
+    // only P^T and dS^T do, and dK/dV-full is one barrier waited on by parity, so
+    // two units on it would pass a compute warp that is still storing.)
+    if (WIN && it.ntiles == 0) continue;
     const int kvs = static_cast<int>(kv_cnt % Ly::KVS);
     const uint32_t kv_round = kv_cnt / Ly::KVS;
     if (kv_round > 0 &&
@@ -495,7 +499,7 @@ __global__ void __launch_bounds__(512, 1)
     int item;
     if (!bwd_unit_item<WIN>(u / p.ipu, u % p.ipu, p, item)) continue;
     const BwdItem it = bwd_decode<WIN>(item, p);
-    if (WIN && it.rest && it.ntiles == 0) continue;
+    if (WIN && it.ntiles == 0) continue;
     const int kvs = static_cast<int>(kv_cnt % Ly::KVS);
     if (!mbar_wait_warp(bar(Ly::B_KVFULL + kvs), (kv_cnt / Ly::KVS) & 1, ab, err, 501)) {
       ok = false;
@@ -745,9 +749,13 @@ __global__ void __launch_bounds__(512, 1)
     const int hc = sub;  // epilogue role: warps 0-3 write dK, warps 4-7 write dV
     // Epilogue: warpgroup A writes dK (scaled by 1/sqrt(D)), B writes dV.
     if (!ok) break;
-    if (!mbar_wait_warp(bar(Ly::B_DKVFULL), kv_cnt & 1, ab, err, 603)) { ok = false; break; }
-    {
+    const bool none = WIN && it.ntiles == 0;  // keys no query sees: zeros
+    if (!none) {
+      if (!mbar_wait_warp(bar(Ly::B_DKVFULL), kv_cnt & 1, ab, err, 603)) { ok = false; break; }
+      ++kv_cnt;
       tc_fence_after();
+    }
+    {
       void* dst_base = hc == 0 ? p.dK : p.dV;
       const float sc = hc == 0 ? p.scale : 1.f;
       const uint32_t tsrc = tmem + lane_off + (hc == 0 ? Ly::TM_DK : Ly::TM_DV);
@@ -762,11 +770,12 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
       for (int cc = 0; cc < D / 32; ++cc) {
         uint32_t o[32];
-        tmem_ld32(tsrc + 32 * cc, o);
-        tmem_ld_wait32(o);
-        if (WIN && it.ntiles == 0) {  // keys no query sees: nothing was accumulated
+        if (none) {
 #pragma unroll
           for (int u = 0; u < 32; ++u) o[u] = 0u;
+        } else {
+          tmem_ld32(tsrc + 32 * cc, o);
+          tmem_ld_wait32(o);
         }
         if (WIN && joint) {
 #pragma unroll
@@ -788,7 +797,6 @@ __global__ void __launch_bounds__(512, 1)
         }
       }
     }
-    ++kv_cnt;
     }
   } else if (warp < 12) {
     if constexpr (kSplitRegs) setmaxnreg_inc<Ly::REGS_DRAIN>();
@@ -802,7 +810,7 @@ __global__ void __launch_bounds__(512, 1)
     int item;
     if (!bwd_unit_item<WIN>(u / p.ipu, u % p.ipu, p, item)) continue;
     const BwdItem it = bwd_decode<WIN>(item, p);
-    if (WIN && it.rest && it.ntiles == 0) continue;
+    if (WIN && it.ntiles == 0) continue;
     for (int n = 0; n < it.ntiles; ++n, ++g) {
       int h, i;
       bwd_tile<WIN>(it, p, n, h, i);
