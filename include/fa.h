@@ -228,6 +228,9 @@ fa_status fa_key_weights(const void* Q, const void* K, const float* LSE, float* 
  * Written in full: kept [B, Hkv, keep] int32 (old positions, ascending; -1
  * behind the last), new_lens [B] int32 = min(n, keep), new_weights
  * [B, Hkv, dst_pages * page] fp32 (the survivors' weights, 0 behind them).
+ * new_lens may be lens itself (a cut in place); other than that no output may
+ * share memory with the tables, lens, weights or another output
+ * (FA_ERR_INVALID_ARG).
  * No workspace.  B * Hkv <= 65535 (FA_ERR_UNSUPPORTED otherwise).
  */
 fa_status fa_paged_evict(void* K_pool, void* V_pool, long long k_page_stride,

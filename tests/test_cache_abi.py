@@ -103,6 +103,23 @@ def test_paged_evict(lib):
     assert call(B=1 << 15, Hkv=2) == UNSUPPORTED
 
 
+def test_paged_evict_outputs_share_no_memory(lib):
+    """Outputs on inputs or on one another (B 2, Hkv 2, tables of 10 and 2 pages of 16, rows of 160).
+    Every call below is refused; none may reach a device, the buffers are not there."""
+    M = 1 << 20
+    kv, table, lens, w, dst, kept, new_lens, nw = (x * M for x in range(1, 9))
+    names = ("K V kst vst table lens w wst dst keep sinks recent kept new_lens nw B Hkv D page max_pages dst_pages "
+             "num_pages dtype").split()
+    call = caller(lib.fa_paged_evict, names,
+                  [kv, kv, 2048, 2048, table, lens, w, 160, dst, 32, 4, 8, kept, new_lens, nw, 2, 2, 64, 16, 10, 2, 30, 0])
+    for kw in (dict(nw=w), dict(nw=w + 639 * 4 // 16 * 16), dict(nw=w - 127 * 4 // 16 * 16), dict(w=nw), dict(kept=lens),
+               dict(kept=table + 19 * 4), dict(kept=dst - 127 * 4), dict(kept=w), dict(new_lens=table), dict(new_lens=dst + 12),
+               dict(new_lens=lens + 4), dict(new_lens=lens - 4), dict(new_lens=kept), dict(new_lens=nw + 127 * 4),
+               dict(kept=nw), dict(nw=kept + 127 * 4 // 16 * 16), dict(new_lens=w + 639 * 4), dict(new_lens=lens, nw=w),
+               dict(wst=1 << 40)):
+        assert call(**kw) == INVALID, kw
+
+
 def test_tensors_on_the_host_are_refused(lib):
     """The calls on torch tensors check their arguments before they touch the device."""
     import torch

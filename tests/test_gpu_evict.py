@@ -198,3 +198,38 @@ def test_clusters_of_every_size(cuda_lib, n, B, Hkv):
     w[0, 0] = (w[0, 0] * 4).round()
     w[-1, -1] = torch.randint(0, 2, w.shape[2:], generator=torch.Generator().manual_seed(1)).float()
     check(k, v, table, dst, lens, w, 300, 4, 30)
+
+
+@pytest.mark.parametrize("n,B,Hkv,keep", [(600, 3, 8, 200), (33000, 1, 2, 500), (20000, 40, 8, 300)])
+def test_lengths_cut_in_place(cuda_lib, n, B, Hkv, keep):
+    """new_lens = lens, every head and CTA of a sequence still choosing from its whole length; and a
+    second call on what the first one left (all survive)."""
+    lens = [max(n - 977 * b, 50) for b in range(B)]
+    k, v, table, dst, ln, w = setup(B, Hkv, 64, "bf16", 256, lens, keep, n)
+    n_d, wd = ln.cuda(), w.cuda()
+    for _ in range(5):
+        n_d.copy_(ln)
+        kept, out, new_w = fa.paged_evict(k, v, table.cuda(), n_d, wd, dst.cuda(), keep, 4, 30, new_lens=n_d)
+        assert out.data_ptr() == n_d.data_ptr()
+        torch.cuda.synchronize()
+        assert n_d.tolist() == [min(x, keep) for x in lens]
+        got = kept.cpu()
+        for b in range(B):
+            for h in range(Hkv):
+                idx = ref.survivors(w[b, h].numpy(), lens[b], keep, 4, 30)
+                assert got[b, h].tolist() == idx + [-1] * (keep - len(idx)), (b, h)
+                np.testing.assert_array_equal(new_w[b, h, : len(idx)].cpu().numpy(), w[b, h, idx].numpy())
+    kept, _, _ = fa.paged_evict(k, v, table.cuda(), n_d, wd, dst.cuda(), keep, 4, 30, new_lens=n_d)
+    assert (kept[0, :, : min(lens[0], keep)].cpu() == torch.arange(min(lens[0], keep))).all()
+
+
+def test_outputs_on_inputs_are_refused(cuda_lib):
+    k, v, table, dst, lens, w = setup(2, 2, 64, "fp16", 16, [64, 64], 32, 2)
+    t, d, n = table.cuda(), dst.cuda(), lens.cuda()
+    wd = torch.rand(2, 2, 64, device="cuda")
+    for kw in (dict(new_weights=wd.flatten()[:128].view(2, 2, 32)),
+               dict(kept=wd.flatten()[128:].view(torch.int32).view(2, 2, 32))):
+        with pytest.raises(_lib.FAError) as e:
+            fa.paged_evict(k, v, t, n, wd, d, 32, **kw)
+        assert e.value.status == _lib.FA_ERR_INVALID_ARG
+    torch.cuda.synchronize()

@@ -63,7 +63,8 @@ def paged_evict(k_cache, v_cache, block_table, lens, weights, dst_table, keep: i
     pages stay as they are.
     Returns kept [B, Hkv, keep] int32 (old positions, -1 behind the last),
     new_lens [B] int32 = min(lens, keep) and new_weights [B, Hkv, P2 * page]
-    (zero behind the survivors)."""
+    (zero behind the survivors).  ``new_lens`` may be ``lens`` itself; the other
+    outputs must not share memory with the inputs."""
     return _raise_on("fa_paged_evict", _lib.binding().paged_evict(
         k_cache, v_cache, block_table, lens, weights, dst_table, keep, sinks, recent, kept, new_lens,
         new_weights, stream))

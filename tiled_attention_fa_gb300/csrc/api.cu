@@ -16,6 +16,17 @@ bool ints_ok(const int* p) { return p != nullptr && (reinterpret_cast<uintptr_t>
 
 bool ptr_ok(const void* p) { return p != nullptr && aligned16(p); }
 
+// Do two buffers of na and nb bytes share any?
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+// Bytes of key weights [pairs, n] fp32 whose rows lie `stride` apart.
+size_t weights_bytes(long long pairs, long long stride, long long n) {
+  return static_cast<size_t>((pairs - 1) * stride + n) * sizeof(float);
+}
+
 // Lq query rows, Lk key rows (equal for the square entry points).
 fa_status check_shape(int B, int Lq, int Lk, int H, int Hkv, int D, int dtype) {
   if (B < 1 || Lq < 1 || Lk < 1 || H < 1 || Hkv < 1) return FA_ERR_INVALID_ARG;
@@ -349,7 +360,29 @@ fa_status fa_paged_evict(void* K_pool, void* V_pool, long long k_page_stride,
       !ints_ok(dst_table) || !ints_ok(kept) || !ints_ok(new_lens) || !ptr_ok(weights) ||
       !ptr_ok(new_weights) || dst_table == block_table)
     return FA_ERR_INVALID_ARG;
-  if (weights_stride < static_cast<long long>(max_pages) * page) return FA_ERR_INVALID_ARG;
+  const long long cap = static_cast<long long>(max_pages) * page, pairs = static_cast<long long>(B) * Hkv;
+  if (weights_stride < cap || weights_stride >= (1ll << 40)) return FA_ERR_INVALID_ARG;
+  {
+    // No output may share memory with an input or another output, but new_lens
+    // may be lens.
+    const struct {
+      const void* p;
+      size_t n;
+    } in[4] = {{block_table, sizeof(int) * B * static_cast<size_t>(max_pages)},
+               {dst_table, sizeof(int) * B * static_cast<size_t>(dst_pages)},
+               {weights, weights_bytes(pairs, weights_stride, cap)},
+               {lens, sizeof(int) * B}},
+      out[3] = {{kept, sizeof(int) * pairs * keep},
+                {new_weights, sizeof(float) * pairs * dst_pages * page},
+                {new_lens, sizeof(int) * B}};
+    for (int o = 0; o < 3; ++o) {
+      for (int i = 0; i < 4; ++i)
+        if (!(o == 2 && new_lens == lens && i == 3) && overlap(out[o].p, out[o].n, in[i].p, in[i].n))
+          return FA_ERR_INVALID_ARG;
+      for (int i = 0; i < o; ++i)
+        if (overlap(out[o].p, out[o].n, out[i].p, out[i].n)) return FA_ERR_INVALID_ARG;
+    }
+  }
   fa::PagedEvictArgs a;
   a.K = K_pool;
   a.V = V_pool;

@@ -52,6 +52,14 @@ __device__ __forceinline__ uint32_t evict_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// Keys of sequence b.  new_lens may be lens itself: the selection, whose CTAs
+// all read the length, leaves it alone; the move writes it, whose blocks need
+// min(n, keep) only, which is the same before and after that write.
+__device__ __forceinline__ int evict_len(const EvictParams& p, int b) {
+  return static_cast<int>(
+      min(static_cast<long long>(max(p.lens[b], 0)), static_cast<long long>(p.max_pages) * p.page));
+}
+
 constexpr int kEvictBins = 2048, kEvictCluster = 8;
 constexpr int evict_threads(int cs) { return cs == 1 ? 1024 : 512; }
 
@@ -105,10 +113,8 @@ __global__ void __launch_bounds__(evict_threads(CS)) fa_evict_select_kernel(cons
   pdl_launch_dependents();
   const int bh = blockIdx.x / CS, b = bh / p.Hkv;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int n = static_cast<int>(
-      min(static_cast<long long>(max(p.lens[b], 0)), static_cast<long long>(p.max_pages) * p.page));
+  const int n = evict_len(p, b);
   int* kept = p.kept + static_cast<long long>(bh) * p.keep;
-  if (rank == 0 && t == 0 && bh - b * p.Hkv == 0) p.new_lens[b] = min(n, p.keep);
   if (n <= p.keep) {  // (the whole cluster)
     for (int i = rank * NT + t; i < p.keep; i += CS * NT) kept[i] = i < n ? i : -1;
     return;
@@ -249,7 +255,8 @@ __global__ void __launch_bounds__(256) fa_evict_move_kernel(const EvictParams p)
   constexpr int PASSES = 4;
   pdl_wait();
   const int bh = blockIdx.y, b = bh / p.Hkv, h = bh - b * p.Hkv;
-  const int m = p.new_lens[b];
+  const int m = min(evict_len(p, b), p.keep);
+  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) p.new_lens[b] = m;
   const int* kept = p.kept + static_cast<long long>(bh) * p.keep;
   const int u = threadIdx.x % UNITS, r0 = threadIdx.x / UNITS;
   const int t0 = blockIdx.x * RPP * PASSES;
