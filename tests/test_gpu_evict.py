@@ -233,3 +233,10 @@ def test_outputs_on_inputs_are_refused(cuda_lib):
             fa.paged_evict(k, v, t, n, wd, d, 32, **kw)
         assert e.value.status == _lib.FA_ERR_INVALID_ARG
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("n,B,Hkv,sinks,recent", [(9000, 2, 2, 100, 200), (33000, 1, 1, 300, 0), (33000, 3, 2, 0, 300)])
+def test_clusters_with_nothing_to_choose(cuda_lib, n, B, Hkv, sinks, recent):
+    """keep = sinks + recent over several CTAs per pair: their counts are exchanged without any pass
+    over the weights before."""
+    check(*setup(B, Hkv, 64, "bf16", 256, [n - 1500 * b for b in range(B)], 300, n), sinks + recent, sinks, recent)

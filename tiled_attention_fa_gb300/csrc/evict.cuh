@@ -197,7 +197,9 @@ __global__ void __launch_bounds__(evict_threads(CS)) fa_evict_select_kernel(cons
       need -= found[1];
     }
   } else {
-    __syncthreads();
+    // (The counts below go to the other ranks' shared memory: all must have
+    // begun.  Above, the first pass's barrier sees to that.)
+    sync();
   }
   // Now prefix is the need-th largest key's value, and `need` of the keys
   // equal to it are taken (the first ones); want == 0 takes none.
