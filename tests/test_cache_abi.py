@@ -120,6 +120,24 @@ def test_paged_evict_outputs_share_no_memory(lib):
         assert call(**kw) == INVALID, kw
 
 
+@pytest.mark.parametrize("B,L,H,Hkv,D,window,sinks", [
+    (4, 8192, 32, 8, 128, 64, 8192),            # every key a sink: causal
+    (1, 32768, 8, 8, 128, 64, 32704),           # nothing hidden: causal
+    (1, 131072, 32, 8, 128, 128, 4096),
+    (1, 1 << 20, 8, 8, 64, 1, 1 << 19),         # 4,096 sink tiles of up to 8,191 far Q tiles
+    (2, 4096, 8, 8, 128, 64, 4),
+])
+def test_window_backward_workspace_is_bounded(lib, B, L, H, Hkv, D, window, sinks):
+    """Beyond the dQ accumulator: two fp32 parts of dK and dV a sink tile, or eight units an SM of at
+    most 256; nothing where no key is hidden."""
+    extra = lib.fa_window_bwd_workspace_size(B, L, L, H, Hkv, D, window, sinks) - lib.fa_bwd_workspace_size(B, L, H, D)
+    if window + sinks >= L:
+        assert extra == 0
+    else:
+        tiles = B * Hkv * -(-sinks // 128)
+        assert 0 < extra <= (2 * tiles + 8 * 256) * 2 * min(sinks, 128) * D * 4
+
+
 def test_tensors_on_the_host_are_refused(lib):
     """The calls on torch tensors check their arguments before they touch the device."""
     import torch

@@ -44,3 +44,34 @@ def test_many_units_that_no_query_sees(cuda_lib, B, Lq, Lk, H, Hkv, D, dtype, wi
     want = ref.backward(to64(q), to64(k[:, seen]), to64(v[:, seen]), to64(do), mask[:, seen.numpy()], dtype)
     for name, g, r, e in zip(("dQ", "dK", "dV"), got, *want):
         within(g, r, e, name)
+
+
+@pytest.mark.parametrize("D,dtype,window,sinks", [(64, "fp16", 1, 1000), (128, "bf16", 100, 1152), (64, "bf16", 300, 129)])
+def test_many_far_units(cuda_lib, D, dtype, window, sinks):
+    """Sink tiles whose later queries make more units than are worth their parts: longer units."""
+    B, L, H, Hkv = 2, 2304, 8, 8
+    q, k, v, do = make_qkv_kv(B, L, L, H, Hkv, D, dtype, sinks, with_do=True)
+    dev = [x.cuda() for x in (q, k, v, do)]
+    o, lse = fa.window_fwd(*dev[:3], window, sinks)
+    grads = fa.window_attention_backward(*dev[:3], o, lse, dev[3], window, sinks)[:3]
+    torch.cuda.synchronize()
+    fa.check_device_error()
+    mask = ref.seen(np.arange(L), L, window, sinks)
+    for name, g, r, e in zip(("dQ", "dK", "dV"), grads, *ref.backward(*(to64(x) for x in (q, k, v, do)), mask, dtype)):
+        within(to64(g), r, e, name)
+
+
+@pytest.mark.parametrize("window,sinks", [(200, 500), (200, 499), (1, 699), (1, 698)])
+def test_hiding_no_key_or_one(cuda_lib, window, sinks):
+    """sinks + window reaches the length (plain causal) or misses it by one key."""
+    L, D, dtype = 700, 64, "fp16"
+    q, k, v, do = make_qkv_kv(1, L, L, 4, 2, D, dtype, sinks, with_do=True)
+    dev = [x.cuda() for x in (q, k, v, do)]
+    o, lse = fa.window_fwd(*dev[:3], window, sinks)
+    grads = fa.window_attention_backward(*dev[:3], o, lse, dev[3], window, sinks)[:3]
+    torch.cuda.synchronize()
+    fa.check_device_error()
+    mask = ref.seen(np.arange(L), L, window, sinks)
+    assert (~np.tril(mask) & np.tril(np.ones((L, L), bool))).sum() == max(0, L - window - sinks)
+    for name, g, r, e in zip(("dQ", "dK", "dV"), grads, *ref.backward(*(to64(x) for x in (q, k, v, do)), mask, dtype)):
+        within(to64(g), r, e, name)

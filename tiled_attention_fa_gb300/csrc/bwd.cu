@@ -58,6 +58,10 @@ namespace {
 void plan_window(BwdParams& p, int B, int window, int sinks) {
   p.window = window < p.Lk ? window : p.Lk;  // as good as every key when larger
   p.sinks = sinks < p.Lk ? sinks : p.Lk;
+  if (static_cast<long long>(p.window) + p.sinks >= p.Lk) {  // hides no key: no sink tiles apart
+    p.window = p.Lk;
+    p.sinks = 0;
+  }
   p.n_sink = (p.sinks + 127) / 128;
   p.srows = p.sinks < 128 ? p.sinks : 128;
   p.chunk = (p.window + 254) / 128;  // Q tiles a window tile is seen by: equal units
@@ -67,6 +71,14 @@ void plan_window(BwdParams& p, int B, int window, int sinks) {
     bwd_win_range(p, j, lo, reach);
     const int left = p.n_q - reach;
     most = left > most ? left : most;
+  }
+  // Far units beyond 8 per SM only cost parts (a slot of 2 * srows * D floats each
+  // in the workspace, which would grow with sinks * Lq / window), so theirs are
+  // then longer: at most 8 per SM, or one per sink tile where those are more.
+  if (most > 0) {
+    const long long tiles = static_cast<long long>(B) * p.Hkv * p.n_sink, per = 8ll * sm_count() / tiles;
+    const int least = per > 1 ? static_cast<int>((most + per - 1) / per) : most;
+    if (p.chunk < least) p.chunk = least;
   }
   p.n_rest = (most + p.chunk - 1) / p.chunk;
   p.n_items = B * p.Hkv * (p.n_kv + p.n_sink * p.n_rest);
