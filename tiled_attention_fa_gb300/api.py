@@ -11,6 +11,8 @@ one batch overlapping the kernels of its neighbours.
 
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import _lib
@@ -48,6 +50,23 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _owner(stream):
+    """Context in which what a call allocates belongs to the stream it is given,
+    so that its memory is not given to another stream's work while the kernels
+    run."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _new(stream, *shape, like, dtype=None):
+    """An empty tensor on the device of ``like``, in its dtype unless given."""
+    with _owner(stream):
+        return torch.empty(*shape, device=like.device, dtype=dtype or like.dtype)
+
+
 def fwd(q, k, v, causal: bool = False, out=None, lse=None, stream=None):
     """O, LSE = attention(Q, K, V).  q [B, Lq, H, D]; k, v [B, Lk, Hkv, D].
 
@@ -59,9 +78,9 @@ def fwd(q, k, v, causal: bool = False, out=None, lse=None, stream=None):
     _need(k, "k", (B, Lk, Hkv, D), q.dtype)
     _need(v, "v", (B, Lk, Hkv, D), q.dtype)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, q.shape, like=q)
     if lse is None:
-        lse = torch.empty(B, H, L, device=q.device, dtype=torch.float32)
+        lse = _new(stream, B, H, L, like=q, dtype=torch.float32)
     _need(out, "out", q.shape, q.dtype)
     _need(lse, "lse", (B, H, L), torch.float32)
     lib = _lib.load()
@@ -117,9 +136,9 @@ def fwd_fp8(q8, k8, v8, q_scale: float, k_scale: float, v_scale: float, causal: 
     if out_dtype not in _OUT:
         raise TypeError("out_dtype must be torch.float16 or torch.bfloat16")
     if out is None:
-        out = torch.empty(B, L, H, D, device=q8.device, dtype=out_dtype)
+        out = _new(stream, B, L, H, D, like=q8, dtype=out_dtype)
     if lse is None:
-        lse = torch.empty(B, H, L, device=q8.device, dtype=torch.float32)
+        lse = _new(stream, B, H, L, like=q8, dtype=torch.float32)
     _need(out, "out", (B, L, H, D), out_dtype)
     _need(lse, "lse", (B, H, L), torch.float32)
     st = _lib.load().fa_fwd_fp8(q8.data_ptr(), k8.data_ptr(), v8.data_ptr(), float(q_scale),
@@ -138,11 +157,11 @@ def _decode_shapes(q, k, v):
     return B, Lq, Lk, H, Hkv, D
 
 
-def _decode_outputs(q, B, Lq, H, out, lse):
+def _decode_outputs(q, B, Lq, H, out, lse, stream):
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, q.shape, like=q)
     if lse is None:
-        lse = torch.empty(B, H, Lq, device=q.device, dtype=torch.float32)
+        lse = _new(stream, B, H, Lq, like=q, dtype=torch.float32)
     _need(out, "out", q.shape, q.dtype)
     _need(lse, "lse", (B, H, Lq), torch.float32)
     return out, lse
@@ -167,9 +186,10 @@ def decode(q, k, v, causal: bool = False, out=None, lse=None, workspace=None, st
     tensor of at least ``decode_workspace_size`` bytes) is allocated when not
     given."""
     B, Lq, Lk, H, Hkv, D = _decode_shapes(q, k, v)
-    out, lse = _decode_outputs(q, B, Lq, H, out, lse)
+    out, lse = _decode_outputs(q, B, Lq, H, out, lse, stream)
     if workspace is None:
-        workspace = alloc_decode_workspace(B, Lq, Lk, H, Hkv, D, q.device)
+        with _owner(stream):
+            workspace = alloc_decode_workspace(B, Lq, Lk, H, Hkv, D, q.device)
     st = _lib.load().fa_decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                lse.data_ptr(), workspace.data_ptr(), _nbytes(workspace), B, Lq, Lk,
                                H, Hkv, D, int(bool(causal)), _dtype_code(q), _stream(stream))
@@ -214,7 +234,7 @@ def bwd_preprocess(o, do, delta=None, dq_accum=None, stream=None):
     _need(o, "o")
     _need(do, "do", o.shape, o.dtype)
     if delta is None:
-        delta = torch.empty(B, H, L, device=o.device, dtype=torch.float32)
+        delta = _new(stream, B, H, L, like=o, dtype=torch.float32)
     _need(delta, "delta", (B, H, L), torch.float32)
     acc_ptr = 0
     if dq_accum is not None:
@@ -239,14 +259,15 @@ def bwd(q, k, v, o, do, lse, delta, causal: bool = False, dq=None, dk=None, dv=N
         _need(t, name, shp, q.dtype)
     _need(lse, "lse", (B, H, L), torch.float32)
     _need(delta, "delta", (B, H, L), torch.float32)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _new(stream, q.shape, like=q) if dq is None else dq
+    dk = _new(stream, k.shape, like=k) if dk is None else dk
+    dv = _new(stream, v.shape, like=v) if dv is None else dv
     _need(dq, "dq", q.shape, q.dtype)
     _need(dk, "dk", k.shape, q.dtype)
     _need(dv, "dv", v.shape, q.dtype)
     if dq_accum is None:
-        dq_accum = alloc_workspace(B, L, H, D, q.device)
+        with _owner(stream):
+            dq_accum = alloc_workspace(B, L, H, D, q.device)
         accum_zeroed = False
     _need(dq_accum, "dq_accum", dtype=torch.float32)
     if dq_accum.numel() * 4 < workspace_size(B, L, H, D):
@@ -306,8 +327,8 @@ def bwd_main(q, k, v, do, lse, delta, dq_accum, causal: bool = False, dk=None, d
     """Stage 2 alone: dK, dV and the fp32 dQ accumulator (added into)."""
     B, L, H, D = q.shape
     Hkv = k.shape[2]
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dk = _new(stream, k.shape, like=k) if dk is None else dk
+    dv = _new(stream, v.shape, like=v) if dv is None else dv
     for name, t in (("q", q), ("k", k), ("v", v), ("do", do), ("lse", lse), ("delta", delta),
                     ("dk", dk), ("dv", dv), ("dq_accum", dq_accum)):
         _need(t, name)
@@ -336,7 +357,8 @@ def attention_backward(q, k, v, o, lse, do, causal: bool = False, dq_accum=None,
     """Preprocess + backward in one call (Delta computed here, accumulator zeroed in the same pass)."""
     B, L, H, D = q.shape
     if dq_accum is None:
-        dq_accum = alloc_workspace(B, L, H, D, q.device)
+        with _owner(stream):
+            dq_accum = alloc_workspace(B, L, H, D, q.device)
     delta = bwd_preprocess(o, do, dq_accum=dq_accum, stream=stream)
     dq, dk, dv = bwd(q, k, v, o, do, lse, delta, causal, dq_accum=dq_accum, accum_zeroed=True,
                      stream=stream)
