@@ -86,9 +86,7 @@ def build(verbose_ptxas: bool = False, quiet: bool = False) -> str:
     with ThreadPoolExecutor(max_workers=len(UNITS) + 1) as ex:
         binding = ex.submit(_compile_binding)
         results = list(ex.map(lambda u: _compile(u, verbose_ptxas), UNITS))
-        binding = binding.result()
-    if binding[2] != 0:
-        raise RuntimeError("the binding failed to compile:\n" + binding[3])
+        binding = binding.exception() or binding.result()
     failed = [r for r in results if r[2] != 0]
     for unit, _, rc, out in results:
         if (rc != 0 or verbose_ptxas) and out.strip():
@@ -102,6 +100,12 @@ def build(verbose_ptxas: bool = False, quiet: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
     os.replace(tmp, LIB_PATH)
+    # The C library stands by now: it needs nvcc alone, the binding torch's and
+    # Python's headers too.
+    if isinstance(binding, BaseException):
+        raise RuntimeError("the binding was not compiled (the library was)") from binding
+    if binding[2] != 0:
+        raise RuntimeError("the binding failed to compile (the library did compile):\n" + binding[3])
     _link_binding(binding[1])
     if not quiet:
         print("built", LIB_PATH)
