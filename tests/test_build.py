@@ -15,6 +15,8 @@ def test_the_library_is_linked_without_the_binding(tmp_path, monkeypatch, how):
     monkeypatch.setattr(build, "BINDING_PATH", str(tmp_path / "binding.so"))
     monkeypatch.setattr(build, "_compile", lambda unit, verbose: (unit, str(tmp_path / unit), 0, ""))
 
+    (tmp_path / "binding.so").write_text("of an earlier build")
+
     def run(cmd, **kw):
         open(cmd[cmd.index("-o") + 1], "w").close()
         return subprocess.CompletedProcess(cmd, 0, "", "")

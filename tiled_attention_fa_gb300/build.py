@@ -101,7 +101,9 @@ def build(verbose_ptxas: bool = False, quiet: bool = False) -> str:
         raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
     os.replace(tmp, LIB_PATH)
     # The C library stands by now: it needs nvcc alone, the binding torch's and
-    # Python's headers too.
+    # Python's headers too.  One of an earlier build may not fit the new library.
+    if os.path.exists(BINDING_PATH):
+        os.remove(BINDING_PATH)
     if isinstance(binding, BaseException):
         raise RuntimeError("the binding was not compiled (the library was)") from binding
     if binding[2] != 0:
