@@ -382,7 +382,8 @@ __device__ __forceinline__ void paged_join(const PagedParams& p, int b, int hkv,
           const bool in = q0 + c < n;
           const float l = in ? ls[c][u] : -INFINITY;
           const float m = fmaxf(mx[u], l);
-          const float old = m == -INFINITY ? 0.f : ex2(mx[u] - m), w = m == -INFINITY ? 0.f : ex2(l - m);
+          // (each for itself: a NaN LSE has no part in m, but its weight is NaN)
+          const float old = mx[u] == -INFINITY ? 0.f : ex2(mx[u] - m), w = l == -INFINITY ? 0.f : ex2(l - m);
           den[u] = fmaf(den[u], old, w);
           acc[u].x = fmaf(acc[u].x, old, in ? w * o[c][u].x : 0.f);
           acc[u].y = fmaf(acc[u].y, old, in ? w * o[c][u].y : 0.f);
@@ -402,7 +403,7 @@ __device__ __forceinline__ void paged_join(const PagedParams& p, int b, int hkv,
             make_uint2(pack2<T>(acc[u].x * inv, acc[u].y * inv), pack2<T>(acc[u].z * inv, acc[u].w * inv));
         if (d == 0)
           p.LSE[(static_cast<size_t>(b) * p.H + h) * p.Lq + ql] =
-              den[u] > 0.f ? (mx[u] + __log2f(den[u])) * 0.6931471805599453f : -INFINITY;
+              den[u] == 0.f ? -INFINITY : (mx[u] + __log2f(den[u])) * 0.6931471805599453f;
       }
     }
   }
@@ -887,7 +888,7 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
             if constexpr (Ly::NG == 2) al[rr] = f[1] * inv;
           }
           if (wq == 0 && lane < CW && rr < p.rows) {
-            const float lse2 = sum > 0.f ? top * sl2 + __log2f(sum) : -INFINITY;
+            const float lse2 = sum == 0.f ? -INFINITY : top * sl2 + __log2f(sum);  // (NaN stays NaN)
             const int ql = rr * p.ginv >> 16;
             if (direct)
               p.LSE[(static_cast<size_t>(w.b) * p.H + w.hkv * p.g + rr - ql * p.g) * p.Lq + ql] =
@@ -1015,7 +1016,10 @@ __global__ void __launch_bounds__(256)
     const float* src = p.scores + (static_cast<size_t>(bh) * p.max_tiles + k) * p.rows * 128 + t;
     float sum = 0.f;
 #pragma unroll 4
-    for (int r = 0; r < p.rows; ++r) sum += ex2(fmaf(src[r * 128], p.sl2, -lse2[r]));
+    for (int r = 0; r < p.rows; ++r) {
+      const float x = src[r * 128];  // -inf: hidden, also from a row whose LSE is NaN
+      sum += x == -INFINITY ? 0.f : ex2(fmaf(x, p.sl2, -lse2[r]));
+    }
     dst[key0] += sum;
   }
 }
