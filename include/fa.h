@@ -207,7 +207,8 @@ fa_status fa_paged_decode(const void* Q, const void* K_pool, const void* V_pool,
  * in a fixed order: the result does not depend on timing.  `workspace`:
  * fa_key_weights_workspace_size() bytes, asked with the device that runs the
  * call current; no initialisation needed, not shared between calls that
- * overlap on the GPU.
+ * overlap on the GPU.  FA_ERR_UNSUPPORTED for 2^31 or more steps (query head, Q
+ * tile, K/V tile) per SM.
  */
 size_t fa_key_weights_workspace_size(void);
 fa_status fa_key_weights(const void* Q, const void* K, const float* LSE, float* W, void* workspace,

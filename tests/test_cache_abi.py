@@ -89,6 +89,12 @@ def test_key_weights(lib):
     assert call(ws_bytes=0) == SMALL and lib.fa_key_weights_workspace_size() > 0
 
 
+def test_key_weights_steps_fit_an_int(lib):
+    """2^46 steps of 128 x 128 over at most 2^10 SMs: a CTA's share would not fit its counter."""
+    L = 1 << 30
+    assert lib.fa_key_weights(FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 30, 1, L, L, 1, 1, 64, 0, 0, 0, 0, None) == UNSUPPORTED
+
+
 def test_paged_evict(lib):
     names = ("K V kst vst table lens w wst dst keep sinks recent kept new_lens nw B Hkv D page max_pages dst_pages "
              "num_pages dtype").split()

@@ -39,6 +39,9 @@ fa_status run_key_weights(const void* Q, const void* K, const float* LSE, float*
                           int window, int sinks, int dtype, cudaStream_t s) {
   if (ws_bytes < key_weights_workspace_size()) return FA_ERR_SCRATCH_TOO_SMALL;
   const int sms = sm_count();
+  const long long most = static_cast<long long>(B) * H * ((Lk + 127) / 128) * ((Lq + 127) / 128);
+  // A CTA counts its part's steps in an int (2^31 steps of half a microsecond).
+  if (most / (sms < 1 ? 1 : sms) >= (1ll << 31) - 1) return FA_ERR_UNSUPPORTED;
   KwParams p;
   p.LSE = LSE;
   p.W = W;
@@ -57,7 +60,6 @@ fa_status run_key_weights(const void* Q, const void* K, const float* LSE, float*
   p.window = window < Lk ? window : 0;  // wider than the sequence: every key
   p.sinks = p.window ? (sinks < Lk ? sinks : Lk) : 0;
   p.sl2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
-  const long long most = static_cast<long long>(B) * H * p.n_kv * p.n_q;
   const int G = most < sms ? static_cast<int>(most) : sms;
   const bool bf16 = dtype == FA_BF16;
   if (D == 64) return bf16 ? launch<64, true>(Q, K, p, G, s) : launch<64, false>(Q, K, p, G, s);
