@@ -154,7 +154,8 @@ fa_status fa_decode_merge(const void* workspace, size_t workspace_bytes, void* O
  * counts[b] tokens when counts [B] is given (a padded batch).  Positions
  * outside the table are skipped.  With `weights`, the weights of the slots
  * written become new_weights [B, Hkv, L] (fa_key_weights of the prompt), or 0
- * when that is NULL.  Two tokens of one call must not share a slot.
+ * when that is NULL; the two must not share memory (FA_ERR_INVALID_ARG).  Two
+ * tokens of one call must not share a slot.
  */
 fa_status fa_paged_write(const void* K, const void* V, void* K_pool, void* V_pool,
                          long long k_page_stride, long long v_page_stride, const int* block_table,

@@ -79,6 +79,16 @@ def test_paged_write(lib):
     assert call(D=96, kst=1 << 20, vst=1 << 20) == UNSUPPORTED and call(page=17) == UNSUPPORTED
 
 
+def test_paged_write_weights_share_no_memory(lib):
+    """weights rows of 160, new_weights [2, 2, 7]; every call below is refused."""
+    M = 1 << 20
+    names = "K V kc vc kst vst table start counts w wst nw B L Hkv D page max_pages num_pages dtype".split()
+    call = caller(lib.fa_paged_write, names, [M, 2 * M, 3 * M, 4 * M, 2048, 2048, 5 * M, 6 * M, None, 7 * M, 160, 8 * M, 2, 7, 2,
+                                              64, 16, 10, 30, 0])
+    for kw in (dict(nw=7 * M), dict(nw=7 * M + 636 * 4), dict(nw=7 * M - 24 * 4), dict(w=8 * M), dict(wst=1 << 40)):
+        assert call(**kw) == INVALID, kw
+
+
 def test_key_weights(lib):
     names = "Q K LSE W ws ws_bytes B Lq Lk H Hkv D causal window sinks dtype".split()
     call = caller(lib.fa_key_weights, names, [FAKE] * 5 + [1 << 30, 1, 50, 70, 4, 2, 64, 1, 0, 0, 0])

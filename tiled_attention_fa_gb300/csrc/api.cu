@@ -335,7 +335,14 @@ fa_status fa_paged_write(const void* K, const void* V, void* K_pool, void* V_poo
   if (weights == nullptr && new_weights != nullptr) return FA_ERR_INVALID_ARG;
   if (weights != nullptr &&
       (!aligned16(weights) || !aligned16(new_weights) ||
-       weights_stride < static_cast<long long>(max_pages) * page))
+       weights_stride < static_cast<long long>(max_pages) * page || weights_stride >= (1ll << 40)))
+    return FA_ERR_INVALID_ARG;
+  // A token's new weight may be another's slot: no order between the two.
+  if (new_weights != nullptr &&
+      overlap(weights,
+              weights_bytes(static_cast<long long>(B) * Hkv, weights_stride,
+                            static_cast<long long>(max_pages) * page),
+              new_weights, sizeof(float) * B * Hkv * static_cast<size_t>(L)))
     return FA_ERR_INVALID_ARG;
   return fa::run_paged_write(K, V, K_pool, V_pool, k_page_stride, v_page_stride, block_table, start,
                              counts, weights, weights_stride, new_weights, B, L, Hkv, D, page,
