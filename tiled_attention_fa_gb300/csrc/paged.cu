@@ -137,17 +137,26 @@ fa_status run_paged_decode(const PagedDecodeArgs& a, cudaStream_t s) {
   p.window = a.window < p.cap ? a.window : 0;  // wider than the cache: every key
   p.sinks = p.window ? (a.sinks < p.cap ? a.sinks : p.cap) : 0;
   p.sl2 = 1.4426950408889634f / sqrtf(static_cast<float>(a.D));
+  // Tiles an item visits at most: all of the table's, or with a window those that
+  // Lq - 1 + window keys in a row touch and the sinks'.
+  long long visit = p.max_tiles;
+  if (p.window) {
+    const long long reach = (static_cast<long long>(p.window) + a.Lq + 125) / 128 + 1 + (p.sinks + 127) / 128;
+    if (reach < visit) visit = reach;
+  }
   // One CTA per SM, fewer when even full sequences have fewer tiles.
-  const long long most = static_cast<long long>(a.B) * a.Hkv * ((cap + 127) / 128);
+  const long long most = static_cast<long long>(a.B) * a.Hkv * p.max_tiles;
   if (most >= (1ll << 31) || sms >= 65536) return FA_ERR_UNSUPPORTED;
   if (a.weights != nullptr && static_cast<long long>(a.B) * a.Hkv > 65535) return FA_ERR_UNSUPPORTED;
   int G = most < sms ? static_cast<int>(most) : sms;
   // Few items cut into many parts: whoever joins an item reads all its partials,
   // rows * D floats each at some 40 GB/s, while a tile takes some 2 us.  So at
-  // most as many parts an item as make the sum of both smallest.  All SMs and so:
-  // B1 H8/1 D128, 16 tokens, 20,000 keys 295 and 96 us; B2 H16/2, 4 tokens, 8,000
-  // keys 64 and 39; B1 H4/1, a token, 30,000 keys 30 and 22.
-  const double parts = std::ceil(std::sqrt(((cap + 127) / 128) * 2.0 / (p.rows * a.D * 4 / 40e3)));
+  // most as many parts an item as make the sum of both smallest for an item of
+  // `visit` tiles; a shorter one under a wide table is still cut into too many
+  // (the host does not know the lengths).  All SMs and so, tables as wide as the
+  // sequence: B1 H8/1 D128, 16 tokens, 20,000 keys 295 and 96 us; B2 H16/2, 4
+  // tokens, 8,000 keys 64 and 39; B1 H4/1, a token, 30,000 keys 30 and 22.
+  const double parts = std::ceil(std::sqrt(visit * 2.0 / (p.rows * a.D * 4 / 40e3)));
   const double limit = parts * a.B * a.Hkv;
   if (limit < G) G = static_cast<int>(limit);
   const bool bf16 = a.dtype == FA_BF16;
