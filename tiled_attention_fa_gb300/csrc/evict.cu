@@ -53,8 +53,8 @@ fa_status run_paged_evict(const PagedEvictArgs& a, cudaStream_t s) {
   p.sinks = a.sinks;
   p.recent = a.recent;
   // CTAs per (sequence, head): one per 4,096 keys of the longest sequence that
-  // the table allows, up to the portable cluster size, as long as that leaves
-  // every SM at most half a CTA.  Measured (cold): 32,768 keys, 8 pairs, one CTA
+  // the table allows (the lengths are not known here), up to the portable cluster
+  // size, as long as there are no more CTAs than SMs.  Measured (cold): 32,768 keys, 8 pairs, one CTA
   // 29 us, eight 16; 12,032 keys, 128 pairs, one CTA 18 us, four 25.
   const long long cap = static_cast<long long>(a.max_pages) * a.page;
   int cs = 1;
