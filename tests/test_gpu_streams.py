@@ -51,3 +51,69 @@ def test_the_default_stream_by_its_handle(cuda_lib):
         o, lse = fa.fwd(q, q, q, stream=0)
     torch.cuda.synchronize()
     assert owner(o) == [0] and owner(lse) == [0] and torch.equal(o, want)
+
+
+def _work(seed):
+    """Inputs of one run through the window and cache calls, and the run."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def rnd(*shape):
+        return torch.randn(*shape, device="cuda", generator=g).bfloat16()
+    B, H, Hkv, D, page, P = 3, 8, 2, 128, 32, 60
+    x, y, do = rnd(2, 500, H, D), rnd(2, 500, Hkv, D), rnd(2, 500, H, D)
+    q = rnd(B, 2, H, D)
+    pools = [rnd(B * (P + 10), page, Hkv, D) for _ in range(2)]
+    table = torch.randperm(B * (P + 10), device="cuda", generator=g).int().view(B, P + 10)
+    src, dst = table[:, :P].contiguous(), table[:, P:].contiguous()
+    lens = torch.tensor([1900, 700 + seed, 33], dtype=torch.int32, device="cuda")
+    w = torch.rand(B, Hkv, P * page, device="cuda", generator=g)
+
+    def run():
+        o, lse = fa.window_fwd(x, y, y, 130, 4)
+        grads = fa.window_attention_backward(x, y, y, o, lse, do, 130, 4)
+        kw = fa.key_weights(x, y, lse, True, 130, 4)
+        wi = w.clone()
+        d, dl = fa.paged_decode(q, *pools, src, lens, weights=wi)
+        kept, nl, nw = fa.paged_evict(*pools, src, lens, wi, dst, 300, 4, 50)
+        e, el = fa.paged_decode(q, *pools, dst, nl, 64, 2, weights=nw)
+        return [o, lse, *grads[1:], kw, wi, d, dl, kept, nl, nw, e, el]      # (dQ is summed by atomics)
+    return run
+
+
+def test_two_streams_at_once(cuda_lib):
+    """Every call on two streams at the same time, many rounds: the same bits as alone."""
+    runs = [_work(1), _work(2)]
+    alone = [r() for r in runs]
+    streams = [torch.cuda.Stream() for _ in runs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        outs = []
+        for r, s in zip(runs, streams):
+            with torch.cuda.stream(s):
+                outs.append(r())
+        torch.cuda.synchronize()
+        for got, want in zip(outs, alone):
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    fa.check_device_error()
+
+
+def test_two_graphs_at_once(cuda_lib):
+    """The same captured, both graphs replayed at the same time, eager calls between."""
+    runs = [_work(3), _work(4)]
+    alone = [r() for r in runs]
+    torch.cuda.synchronize()
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in runs]
+    for r in runs:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(r())
+        graphs.append(gr)
+    for _ in range(20):
+        for gr, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                gr.replay()
+        eager = runs[0]()
+        torch.cuda.synchronize()
+        for got, want in zip(outs + [eager], alone + [alone[0]]):
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    fa.check_device_error()
