@@ -6,7 +6,9 @@
  * `void*`, i.e. a cudaStream_t; NULL = the legacy default stream).  Argument
  * errors are reported synchronously by the return value and launch nothing.
  * The caller allocates and owns every buffer, including the backward
- * workspace; the library keeps only a per-device SM-count cache.
+ * workspace; the library keeps a per-device SM-count cache, a count of
+ * fa_paged_decode calls (each call's number marks its counters in its
+ * workspace) and fa_bwd_noalloc's fixed array.
  *
  * Layouts (all contiguous, row-major):
  *   Q, O, dO, dQ   [B, L, H,   D]   fp16 or bf16 ("BSHD")
@@ -172,14 +174,20 @@ fa_status fa_paged_write(const void* K, const void* V, void* K_pool, void* V_poo
  * below 0 as 0.  A query that sees nothing (a negative position, an empty
  * sequence) gives O = 0, LSE = -inf.  Keys that no query of the call sees are
  * never used, whatever their slots hold; pages wholly behind the length or
- * before the window are not read and may be absent from the table.
+ * before the window are not read and may be absent from the table.  V must be
+ * finite at a key that some query of the call sees: for the queries that do not
+ * see it, it is multiplied by a zero weight.  NaN in a query or in a key it sees
+ * gives that row NaN in O and LSE (and in the weights it adds).
  * Q, O [B, Lq, H, D]; LSE [B, H, Lq]; (H / Hkv) * Lq <= 128
  * (FA_ERR_UNSUPPORTED otherwise).  With `weights` the call adds to each
  * visible key's weight sum over the group's heads and the queries of
  * exp(q . k / sqrt(D) - LSE).  Every key is added to once, by one thread:
  * results do not depend on any order, and sequences may share pages.
  * `workspace`: fa_paged_decode_workspace_size bytes, asked with the device
- * that runs the call current (FA_ERR_SCRATCH_TOO_SMALL when smaller); its
+ * that runs the call current (FA_ERR_SCRATCH_TOO_SMALL when smaller); with
+ * `weights` it holds a raw score for every slot of the table and query head
+ * (B * Hkv * ceil(max_pages * page / 128) * (H / Hkv) * Lq * 512 bytes), whatever
+ * the lengths are, so a table no wider than needed saves memory.  Its
  * contents need no initialisation; calls (and replayed graphs) that overlap
  * on the GPU must not share one.  (After a device error in a replayed graph,
  * zero its workspace or capture it again before the next replay: the counts of
