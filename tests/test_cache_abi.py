@@ -168,3 +168,23 @@ def test_tensors_on_the_host_are_refused(lib):
                  lambda: fa.key_weights([1.0], q, q)):
         with pytest.raises(TypeError):
             call()
+
+
+def test_window_workspace_is_sized_on_its_device(lib, monkeypatch):
+    """How the work is cut depends on the SMs of the device that runs the call."""
+    import contextlib
+
+    import torch
+
+    import tiled_attention_fa_gb300 as fa
+    from tiled_attention_fa_gb300 import api
+    current = []
+
+    @contextlib.contextmanager
+    def device(d):
+        current.append(d)
+        yield
+        current.pop()
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(api, "window_workspace_size", lambda *a: 4000 if current == ["cpu"] else 16)
+    assert fa.alloc_window_workspace(1, 9, 9, 1, 1, 64, 4, 0, "cpu").numel() == 1000

@@ -295,7 +295,8 @@ def window_workspace_size(B: int, Lq: int, Lk: int, H: int, Hkv: int, D: int, wi
 
 def alloc_window_workspace(B: int, Lq: int, Lk: int, H: int, Hkv: int, D: int, window: int, sinks: int,
                            device) -> torch.Tensor:
-    n = window_workspace_size(B, Lq, Lk, H, Hkv, D, window, sinks) // 4
+    with torch.cuda.device(device):
+        n = window_workspace_size(B, Lq, Lk, H, Hkv, D, window, sinks) // 4
     return torch.empty(max(n, 4), device=device, dtype=torch.float32)
 
 
