@@ -63,6 +63,8 @@ def _owner(stream):
 
 def _new(stream, *shape, like, dtype=None):
     """An empty tensor on the device of ``like``, in its dtype unless given."""
+    if stream is None:
+        return torch.empty(*shape, device=like.device, dtype=dtype or like.dtype)
     with _owner(stream):
         return torch.empty(*shape, device=like.device, dtype=dtype or like.dtype)
 
