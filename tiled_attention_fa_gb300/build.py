@@ -101,14 +101,18 @@ def build(verbose_ptxas: bool = False, quiet: bool = False) -> str:
         raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
     os.replace(tmp, LIB_PATH)
     # The C library stands by now: it needs nvcc alone, the binding torch's and
-    # Python's headers too.  One of an earlier build may not fit the new library.
-    if os.path.exists(BINDING_PATH):
-        os.remove(BINDING_PATH)
-    if isinstance(binding, BaseException):
-        raise RuntimeError("the binding was not compiled (the library was)") from binding
-    if binding[2] != 0:
-        raise RuntimeError("the binding failed to compile (the library did compile):\n" + binding[3])
-    _link_binding(binding[1])
+    # Python's headers too.  Where that fails, no binding of an earlier build stays
+    # beside a library it may not fit.
+    try:
+        if isinstance(binding, BaseException):
+            raise RuntimeError("the binding was not compiled (the library was)") from binding
+        if binding[2] != 0:
+            raise RuntimeError("the binding failed to compile (the library did compile):\n" + binding[3])
+        _link_binding(binding[1])
+    except RuntimeError:
+        if os.path.exists(BINDING_PATH):
+            os.remove(BINDING_PATH)
+        raise
     if not quiet:
         print("built", LIB_PATH)
     return LIB_PATH
