@@ -205,6 +205,93 @@ fa_status fa_paged_decode(const void* Q, const void* K_pool, const void* V_pool,
                           int window, int sinks, int dtype, void* stream);
 
 /*
+ * Rotary positions.  A table of rotary / 2 entries, one per pair of a head's
+ * dims, 16-byte aligned: entry i holds in its low 8 bits the pair's axis and
+ * above them the turns that a position adds, f_i / (2 pi), as a fraction of 2^56
+ * modulo 1 (two's complement: negative frequencies turn backwards).  The first
+ * `rotary` dims of a head (a multiple of 16 up to D, FA_ERR_UNSUPPORTED
+ * otherwise) are the pairs: dims i and i + rotary / 2, or with `interleaved` dims
+ * 2 i and 2 i + 1; the others are copied.  Pair i (x, y) of a token at position n
+ * on the pair's axis becomes
+ *   (x cos t - y sin t, x sin t + y cos t),   t = n f_i,
+ * with angles that are exact to 2^-22 rad at every int32 position, computed in
+ * fp32, each result rounded once.  positions [axes, B, L] int32 (1 to 256 axes;
+ * a table's axis beyond the last counts as the last), or NULL with one axis: the
+ * token's number 0 .. L - 1.
+ *
+ * fa_rope: queries Q [B, L, H, D] and keys K [B, L, Hkv, D], turned, into Q_out
+ * and K_out; K and K_out NULL with Hkv = 0 for queries alone.  With `backward`
+ * it turns by -t: the gradients of Q and K from those of Q_out and K_out.  All four
+ * have free strides between batch entries and tokens, in elements and multiples
+ * of 8 (parts of a fused projection's rows; inputs may repeat, outputs may not);
+ * the last two dims are contiguous.  An output may be its input itself (the same
+ * pointer and strides); otherwise the two must not share memory
+ * (FA_ERR_INVALID_ARG), nor may an output share an element with the other
+ * tensor's operands.  H need not be a multiple of Hkv.
+ */
+fa_status fa_rope(const void* Q, long long q_batch, long long q_token, const void* K,
+                  long long k_batch, long long k_token, void* Q_out, long long q_out_batch,
+                  long long q_out_token, void* K_out, long long k_out_batch, long long k_out_token,
+                  const long long* table, const int* positions, int axes, int B, int L, int H,
+                  int Hkv, int D, int rotary, int interleaved, int backward, int dtype,
+                  void* stream);
+
+/*
+ * fa_paged_append: fa_rope and fa_paged_write in one pass.  Queries Q [B, L, H, D]
+ * are turned into Q_out, all of them; keys K and values V [B, L, Hkv, D] of the
+ * tokens that count go into the pages, the keys turned.  Slots, counts, pages and
+ * weights are fa_paged_write's, table and rotation fa_rope's; with positions NULL
+ * (one axis) a token's position is its slot, start[b] + j.  Q, K, V and Q_out have
+ * fa_rope's strides; Q_out may be Q itself, and shares no memory with anything
+ * else of the call.
+ */
+fa_status fa_paged_append(const void* Q, long long q_batch, long long q_token, const void* K,
+                          long long k_batch, long long k_token, const void* V, long long v_batch,
+                          long long v_token, void* Q_out, long long q_out_batch,
+                          long long q_out_token, void* K_pool, void* V_pool,
+                          long long k_page_stride, long long v_page_stride, const int* block_table,
+                          const int* start, const int* counts, const long long* table,
+                          const int* positions, int axes, float* weights, long long weights_stride,
+                          const float* new_weights, int B, int L, int H, int Hkv, int D, int rotary,
+                          int interleaved, int page, int max_pages, int num_pages, int dtype,
+                          void* stream);
+
+/*
+ * fa_paged_prefix_decode: fa_paged_decode (no window, no weights) for sequences
+ * that share key/value prefixes, each prefix read once for all of them.  Group i
+ * is the sequences group_starts[i] .. group_starts[i + 1] - 1 (group_starts
+ * [groups + 1] int32, never falling; NULL with one group: all of them); its
+ * prefix is the first prefix_lens[i] keys of the pages in row i of prefix_table
+ * [groups, prefix_pages].  block_table [B, max_pages] and lens [B] are the
+ * sequences' own keys behind the prefix, the new tokens' included: query i of
+ * sequence b sees its group's whole prefix and its own keys
+ * j <= lens[b] - Lq + i.  A query whose own position lens[b] - Lq + i is
+ * negative (an unused slot) is padding and gives O = 0, LSE = -inf.  A sequence
+ * of no group, or with a prefix of length 0, has its own keys alone.  Prefixes
+ * and own keys lie in the same two pools; tables, lengths and group_starts are
+ * read on the device, lengths clamped to their tables and starts to [0, B]
+ * (starts that fall anywhere give unspecified results).  Slots behind a length
+ * are never used, whatever they hold; V must be finite at a key that some query
+ * of the call sees, and NaN in a query or in a key it sees gives that row NaN.
+ * (H / Hkv) * Lq <= 128 (FA_ERR_UNSUPPORTED otherwise).
+ * Results do not depend on timing.  `workspace`:
+ * fa_paged_prefix_decode_workspace_size bytes, asked with the device that runs
+ * the call current (FA_ERR_SCRATCH_TOO_SMALL when smaller), under
+ * fa_paged_decode's rules; a part of it holds 128 x D floats for every tile of
+ * 128 / (H / Hkv) tokens, group and K/V head and every SM.
+ */
+size_t fa_paged_prefix_decode_workspace_size(int B, int Lq, int H, int Hkv, int D, int page,
+                                             int groups, int prefix_pages, int max_pages);
+fa_status fa_paged_prefix_decode(const void* Q, const void* K_pool, const void* V_pool,
+                                 long long k_page_stride, long long v_page_stride,
+                                 const int* prefix_table, const int* prefix_lens,
+                                 const int* group_starts, const int* block_table, const int* lens,
+                                 void* O, float* LSE, void* workspace, size_t workspace_bytes,
+                                 int B, int Lq, int H, int Hkv, int D, int page, int groups,
+                                 int prefix_pages, int max_pages, int num_pages, int dtype,
+                                 void* stream);
+
+/*
  * Key weights: how much attention each key of a prompt has received,
  *   W[b, hkv, j] = sum over the heads h of the group and the queries i that
  *                  see key j of exp(q_i . k_j / sqrt(D) - LSE[b, h, i]),

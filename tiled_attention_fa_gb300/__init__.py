@@ -35,11 +35,15 @@ from .api import (  # noqa: F401
 from .cache import (  # noqa: F401
     key_weights,
     key_weights_workspace_size,
+    paged_append,
     paged_decode,
     paged_decode_workspace_size,
     paged_evict,
+    paged_prefix_decode,
+    paged_prefix_decode_workspace_size,
     paged_write,
 )
+from .rope import rope_bwd, rope_fwd, rope_table  # noqa: F401
 
 __all__ = ["fwd", "bwd_preprocess", "bwd", "attention_backward", "bwd_main", "bwd_postprocess", "workspace_size",
            "alloc_workspace", "check_device_error", "HostRunner", "HostPipeline", "decode", "decode_workspace_size",
@@ -47,4 +51,6 @@ __all__ = ["fwd", "bwd_preprocess", "bwd", "attention_backward", "bwd_main", "bw
            "window_fwd", "window_bwd", "window_attention_backward", "window_workspace_size",
            "alloc_window_workspace",
            "paged_write", "paged_decode", "paged_decode_workspace_size", "key_weights",
-           "key_weights_workspace_size", "paged_evict"]
+           "key_weights_workspace_size", "paged_evict",
+           "rope_table", "rope_fwd", "rope_bwd", "paged_append", "paged_prefix_decode",
+           "paged_prefix_decode_workspace_size"]

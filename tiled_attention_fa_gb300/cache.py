@@ -53,6 +53,46 @@ def paged_decode(q, k_cache, v_cache, block_table, lens, window: int = 0, sinks:
         q, k_cache, v_cache, block_table, lens, window, sinks, weights, out, lse, workspace, stream))
 
 
+def paged_append(q, k, v, k_cache, v_cache, block_table, start, table, positions=None, counts=None,
+                 interleaved: bool = False, weights=None, new_weights=None, out=None, stream=None):
+    """``rope_fwd`` of the queries and ``paged_write`` of the turned keys and
+    the values in one pass.  q [B, L, H, D], k, v [B, L, Hkv, D], with any
+    strides between tokens and batch entries (parts of a fused projection);
+    k_cache, v_cache, block_table, start, counts, weights and new_weights as
+    for ``paged_write``, ``table`` (from ``rope_table``), ``positions``
+    [axes, B, L] int32 and ``interleaved`` as for ``rope_fwd``, except that
+    without positions a token's is its slot, start[b] + j.  Returns the turned
+    queries, of every token, counted or not (``out`` may be q itself)."""
+    return _raise_on("fa_paged_append", _lib.binding().paged_append(
+        q, k, v, k_cache, v_cache, block_table, start, table, positions, counts, interleaved, weights, new_weights,
+        out, stream))
+
+
+def paged_prefix_decode_workspace_size(B: int, Lq: int, H: int, Hkv: int, D: int, page: int, groups: int,
+                                       prefix_pages: int, max_pages: int) -> int:
+    """Bytes of the workspace ``paged_prefix_decode`` needs on the current device."""
+    return int(_lib.load().fa_paged_prefix_decode_workspace_size(B, Lq, H, Hkv, D, page, groups, prefix_pages,
+                                                                 max_pages))
+
+
+def paged_prefix_decode(q, k_cache, v_cache, prefix_table, prefix_lens, block_table, lens, group_starts=None,
+                        out=None, lse=None, workspace=None, stream=None):
+    """``paged_decode`` for sequences that share key/value prefixes, each
+    prefix read once for all of them.  O, LSE of the last Lq tokens of every
+    sequence, q [B, Lq, H, D].  Group i is the sequences group_starts[i] up to
+    group_starts[i + 1] (int32 [G + 1], never falling; None with one group: all
+    of them), its prefix the first prefix_lens[i] keys in the pages of
+    prefix_table [G, PP]; block_table [B, P] and lens [B] are the sequences'
+    own keys behind it, the new tokens' included.  Query i of sequence b sees
+    its group's prefix and its own keys j <= lens[b] - Lq + i; where that is
+    negative (an unused slot) O = 0, LSE = -inf.  (H / Hkv) * Lq <= 128.
+    ``workspace`` (a CUDA byte tensor of at least
+    ``paged_prefix_decode_workspace_size`` bytes) is allocated when not
+    given."""
+    return _raise_on("fa_paged_prefix_decode", _lib.binding().paged_prefix_decode(
+        q, k_cache, v_cache, prefix_table, prefix_lens, block_table, lens, group_starts, out, lse, workspace, stream))
+
+
 def paged_evict(k_cache, v_cache, block_table, lens, weights, dst_table, keep: int, sinks: int = 0,
                 recent: int = 0, kept=None, new_lens=None, new_weights=None, stream=None):
     """Cut every sequence's paged keys and values down to ``keep`` per K/V

@@ -262,6 +262,16 @@ fa_status check_pool(int B, int Hkv, int D, int page, int max_pages, int num_pag
     if (st < rows || st % 8 != 0 || st >= (1ll << 38)) return FA_ERR_INVALID_ARG;
   return FA_OK;
 }
+
+// Weights of `cap` slots a row that a write of L tokens resets, or to new ones.
+bool weights_ok(const float* weights, long long stride, const float* new_weights, int B, int L, int Hkv,
+                long long cap) {
+  if (weights == nullptr) return new_weights == nullptr;
+  if (!aligned16(weights) || !aligned16(new_weights) || stride < cap || stride >= (1ll << 40)) return false;
+  // A token's new weight may be another's slot: no order between the two.
+  return new_weights == nullptr || !overlap(weights, weights_bytes(static_cast<long long>(B) * Hkv, stride, cap),
+                                            new_weights, sizeof(float) * B * Hkv * static_cast<size_t>(L));
+}
 }  // namespace
 
 size_t fa_paged_decode_workspace_size(int B, int Lq, int H, int Hkv, int D, int page, int max_pages,
@@ -332,17 +342,7 @@ fa_status fa_paged_write(const void* K, const void* V, void* K_pool, void* V_poo
       !ints_ok(start))
     return FA_ERR_INVALID_ARG;
   if (counts != nullptr && !ints_ok(counts)) return FA_ERR_INVALID_ARG;
-  if (weights == nullptr && new_weights != nullptr) return FA_ERR_INVALID_ARG;
-  if (weights != nullptr &&
-      (!aligned16(weights) || !aligned16(new_weights) ||
-       weights_stride < static_cast<long long>(max_pages) * page || weights_stride >= (1ll << 40)))
-    return FA_ERR_INVALID_ARG;
-  // A token's new weight may be another's slot: no order between the two.
-  if (new_weights != nullptr &&
-      overlap(weights,
-              weights_bytes(static_cast<long long>(B) * Hkv, weights_stride,
-                            static_cast<long long>(max_pages) * page),
-              new_weights, sizeof(float) * B * Hkv * static_cast<size_t>(L)))
+  if (!weights_ok(weights, weights_stride, new_weights, B, L, Hkv, static_cast<long long>(max_pages) * page))
     return FA_ERR_INVALID_ARG;
   return fa::run_paged_write(K, V, K_pool, V_pool, k_page_stride, v_page_stride, block_table, start,
                              counts, weights, weights_stride, new_weights, B, L, Hkv, D, page,
@@ -416,6 +416,163 @@ fa_status fa_paged_evict(void* K_pool, void* V_pool, long long k_page_stride,
   return fa::run_paged_evict(a, static_cast<cudaStream_t>(stream));
 }
 
+namespace {
+
+// One operand of the rotary calls: [B, L, heads, D] with free batch and token
+// strides; an output's rows must lie apart.
+bool view_ok(const fa::RopeView& v, bool output, int B, int L, int heads, int D) {
+  const long long row = static_cast<long long>(heads) * D;
+  if (!ptr_ok(v.p) || v.batch < 0 || v.token < 0 || v.batch % 8 != 0 || v.token % 8 != 0 ||
+      v.batch >= (1ll << 38) || v.token >= (1ll << 38))
+    return false;
+  if (!output) return true;
+  if (B == 1) return L == 1 || v.token >= row;
+  if (L == 1) return v.batch >= row;
+  return (v.token >= row && v.batch >= (L - 1) * v.token + row) || (v.batch >= row && v.token >= (B - 1) * v.batch + row);
+}
+
+// The output is the input itself or shares no memory with it.
+bool in_place_or_apart(const fa::RopeView& x, const fa::RopeView& y, int B, int L, int heads, int D) {
+  auto bytes = [&](const fa::RopeView& v) {
+    return static_cast<size_t>((B - 1) * v.batch + (L - 1) * v.token + static_cast<long long>(heads) * D) * 2;
+  };
+  if (x.p == y.p && (B == 1 || x.batch == y.batch) && (L == 1 || x.token == y.token)) return true;
+  return !overlap(x.p, bytes(x), y.p, bytes(y));
+}
+
+fa_status check_rope(const fa::RopeArgs& a, int heads) {
+  if (a.Hkv < 0 || a.Hkv > (1 << 20) || a.H < 1 || a.H > (1 << 20)) return FA_ERR_INVALID_ARG;
+  const fa_status st = check_shape(a.B, a.L, a.L, heads, heads, a.D, a.dtype);
+  if (st != FA_OK) return st;
+  if (a.rotary < 16 || a.rotary > a.D || a.rotary % 16 != 0) return FA_ERR_UNSUPPORTED;
+  if (a.axes < 1 || a.axes > 256 || !ptr_ok(a.table)) return FA_ERR_INVALID_ARG;
+  if (a.positions == nullptr ? a.axes != 1 : !ints_ok(a.positions)) return FA_ERR_INVALID_ARG;
+  if (!view_ok(a.q, false, a.B, a.L, a.H, a.D) || !view_ok(a.qy, true, a.B, a.L, a.H, a.D) ||
+      !in_place_or_apart(a.q, a.qy, a.B, a.L, a.H, a.D))
+    return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+}  // namespace
+
+fa_status fa_rope(const void* Q, long long q_batch, long long q_token, const void* K, long long k_batch,
+                  long long k_token, void* Q_out, long long q_out_batch, long long q_out_token, void* K_out,
+                  long long k_out_batch, long long k_out_token, const long long* table, const int* positions,
+                  int axes, int B, int L, int H, int Hkv, int D, int rotary, int interleaved, int backward,
+                  int dtype, void* stream) {
+  const fa::RopeArgs a{{Q, q_batch, q_token}, {K, k_batch, k_token}, {Q_out, q_out_batch, q_out_token},
+                       {K_out, k_out_batch, k_out_token}, table, positions, axes, B, L, H, Hkv, D, rotary,
+                       interleaved, backward, dtype};
+  const fa_status st = check_rope(a, Hkv > 0 && H > 0 && Hkv <= (1 << 20) && H <= (1 << 20) ? H + Hkv : H);
+  if (st != FA_OK) return st;
+  if (Hkv == 0) {
+    if (K != nullptr || K_out != nullptr) return FA_ERR_INVALID_ARG;
+  } else if (!view_ok(a.k, false, B, L, Hkv, D) || !view_ok(a.ky, true, B, L, Hkv, D) ||
+             !in_place_or_apart(a.k, a.ky, B, L, Hkv, D)) {
+    return FA_ERR_INVALID_ARG;
+  }
+  return fa::run_rope(a, static_cast<cudaStream_t>(stream));
+}
+
+fa_status fa_paged_append(const void* Q, long long q_batch, long long q_token, const void* K, long long k_batch,
+                          long long k_token, const void* V, long long v_batch, long long v_token, void* Q_out,
+                          long long q_out_batch, long long q_out_token, void* K_pool, void* V_pool,
+                          long long k_page_stride, long long v_page_stride, const int* block_table,
+                          const int* start, const int* counts, const long long* table, const int* positions,
+                          int axes, float* weights, long long weights_stride, const float* new_weights, int B,
+                          int L, int H, int Hkv, int D, int rotary, int interleaved, int page, int max_pages,
+                          int num_pages, int dtype, void* stream) {
+  const fa::RopeArgs a{{Q, q_batch, q_token}, {K, k_batch, k_token}, {Q_out, q_out_batch, q_out_token},
+                       {}, table, positions, axes, B, L, H, Hkv, D, rotary, interleaved, 0, dtype};
+  if (Hkv < 1 || Hkv > (1 << 20) || H < 1 || H > (1 << 20)) return FA_ERR_INVALID_ARG;
+  fa_status st = check_rope(a, H + 2 * Hkv);
+  if (st != FA_OK) return st;
+  if (H % Hkv != 0) return FA_ERR_INVALID_ARG;
+  st = check_pool(B, Hkv, D, page, max_pages, num_pages, k_page_stride, v_page_stride, dtype);
+  if (st != FA_OK) return st;
+  const fa::RopeView v{V, v_batch, v_token};
+  if (!view_ok(a.k, false, B, L, Hkv, D) || !view_ok(v, false, B, L, Hkv, D) || !ptr_ok(K_pool) || !ptr_ok(V_pool) ||
+      !ints_ok(block_table) || !ints_ok(start) || (counts != nullptr && !ints_ok(counts)))
+    return FA_ERR_INVALID_ARG;
+  if (!weights_ok(weights, weights_stride, new_weights, B, L, Hkv, static_cast<long long>(max_pages) * page))
+    return FA_ERR_INVALID_ARG;
+  const fa::PagedAppendArgs c{v, K_pool, V_pool, block_table, start, counts, weights, new_weights, weights_stride,
+                              k_page_stride, v_page_stride, page, max_pages, num_pages};
+  return fa::run_paged_append(a, c, static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+fa::PrefixDecodeArgs prefix_sizes(int B, int Lq, int H, int Hkv, int D, int page, int groups, int prefix_pages,
+                                  int max_pages) {
+  fa::PrefixDecodeArgs a = {};
+  a.B = B;
+  a.Lq = Lq;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.page = page;
+  a.groups = groups;
+  a.prefix_pages = prefix_pages;
+  a.max_pages = max_pages;
+  return a;
+}
+
+// What both prefix calls refuse.
+fa_status check_prefix(int B, int Lq, int H, int Hkv, int D, int page, int groups, int prefix_pages, int max_pages,
+                       int dtype) {
+  fa_status st = check_shape(B, Lq, Lq, H, Hkv, D, dtype);
+  if (st != FA_OK) return st;
+  const long long least = static_cast<long long>(page < 1 ? 1 : page) * Hkv * D;
+  for (int pages : {prefix_pages, max_pages}) {
+    st = check_pool(B, Hkv, D, page, pages, 1, least, least, dtype);
+    if (st != FA_OK) return st;
+  }
+  if (groups < 1 || groups > (1 << 20)) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(H / Hkv) * Lq > 128) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+}  // namespace
+
+size_t fa_paged_prefix_decode_workspace_size(int B, int Lq, int H, int Hkv, int D, int page, int groups,
+                                             int prefix_pages, int max_pages) {
+  if (check_prefix(B, Lq, H, Hkv, D, page, groups, prefix_pages, max_pages, FA_F16) != FA_OK) return 0;
+  return fa::paged_prefix_workspace_size(prefix_sizes(B, Lq, H, Hkv, D, page, groups, prefix_pages, max_pages));
+}
+
+fa_status fa_paged_prefix_decode(const void* Q, const void* K, const void* V, long long k_page_stride,
+                                 long long v_page_stride, const int* prefix_table, const int* prefix_lens,
+                                 const int* group_starts, const int* block_table, const int* lens, void* O,
+                                 float* LSE, void* workspace, size_t workspace_bytes, int B, int Lq, int H, int Hkv,
+                                 int D, int page, int groups, int prefix_pages, int max_pages, int num_pages,
+                                 int dtype, void* stream) {
+  fa_status st = check_prefix(B, Lq, H, Hkv, D, page, groups, prefix_pages, max_pages, dtype);
+  if (st != FA_OK) return st;
+  st = check_pool(B, Hkv, D, page, max_pages, num_pages, k_page_stride, v_page_stride, dtype);
+  if (st != FA_OK) return st;
+  if (group_starts == nullptr ? groups != 1 : !ints_ok(group_starts)) return FA_ERR_INVALID_ARG;
+  if (!ptr_ok(Q) || !ptr_ok(K) || !ptr_ok(V) || !ints_ok(prefix_table) || !ints_ok(prefix_lens) ||
+      !ints_ok(block_table) || !ints_ok(lens) || !ptr_ok(O) || !ptr_ok(LSE) || !ptr_ok(workspace))
+    return FA_ERR_INVALID_ARG;
+  fa::PrefixDecodeArgs a = prefix_sizes(B, Lq, H, Hkv, D, page, groups, prefix_pages, max_pages);
+  a.Q = Q;
+  a.K = K;
+  a.V = V;
+  a.prefix_table = prefix_table;
+  a.prefix_lens = prefix_lens;
+  a.group_starts = group_starts;
+  a.table = block_table;
+  a.lens = lens;
+  a.O = O;
+  a.LSE = LSE;
+  a.k_page_stride = k_page_stride;
+  a.v_page_stride = v_page_stride;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  a.num_pages = num_pages;
+  a.dtype = dtype;
+  return fa::run_paged_prefix(a, static_cast<cudaStream_t>(stream));
+}
+
 size_t fa_key_weights_workspace_size(void) { return fa::key_weights_workspace_size(); }
 
 fa_status fa_key_weights(const void* Q, const void* K, const float* LSE, float* W, void* workspace,
@@ -433,9 +590,10 @@ fa_status fa_key_weights(const void* Q, const void* K, const float* LSE, float* 
 
 fa_status fa_check_device_error(void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned int words[5] = {fa::fwd_read_error(s), fa::bwd_read_error(s),
-                                 fa::decode_read_error(s), fa::paged_read_error(s),
-                                 fa::weights_read_error(s)};
+  const unsigned int words[7] = {fa::fwd_read_error(s),     fa::bwd_read_error(s),
+                                 fa::decode_read_error(s),  fa::paged_read_error(s),
+                                 fa::weights_read_error(s), fa::paged_own_read_error(s),
+                                 fa::prefix_read_error(s)};
   unsigned int site = 0;
   for (unsigned int w : words) {
     if (w == 0xFFFFFFFFu) return FA_ERR_CUDA;

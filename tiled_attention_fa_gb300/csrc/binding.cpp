@@ -157,8 +157,9 @@ Pools pools(PyObject* ko, PyObject* vo, at::ScalarType dt, int dev) {
   const Tensor &k = tensor(ko, "k_cache"), &v = tensor(vo, "v_cache");
   const Four s = four(k, "k_cache");
   Pools p{k, v, s.a, s.b, s.c, s.d, 0, 0};
-  for (const Tensor* t : {&k, &v}) {
-    const char* name = t == &k ? "k_cache" : "v_cache";
+  for (const bool of_k : {true, false}) {  // (the two may be one Python object)
+    const Tensor* t = of_k ? &k : &v;
+    const char* name = of_k ? "k_cache" : "v_cache";
     if (t->scalar_type() != dt)
       fail(PyExc_TypeError, "%s has dtype %s, expected %s", name, c10::toString(t->scalar_type()),
                              c10::toString(dt));
@@ -169,7 +170,7 @@ Pools pools(PyObject* ko, PyObject* vo, at::ScalarType dt, int dev) {
     if (t->get_device() != dev)
       fail(PyExc_ValueError, "%s lies on cuda:%d, the current device is cuda:%d", name,
            static_cast<int>(t->get_device()), dev);
-    (t == &k ? p.kst : p.vst) = s.a > 1 ? t->stride(0) : s.b * s.c * s.d;
+    (of_k ? p.kst : p.vst) = s.a > 1 ? t->stride(0) : s.b * s.c * s.d;
   }
   return p;
 }
@@ -345,6 +346,171 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// An operand of the rotary calls: [B, L, heads, D] whose last two dims are
+// contiguous, with the strides of the first two (0 where they do not count).
+struct View {
+  void* p;
+  long long batch, token;
+  int64_t heads;
+};
+View view(const Tensor& t, const char* name, at::IntArrayRef shape, at::ScalarType dt, int dev) {
+  if (t.scalar_type() != dt)
+    fail(PyExc_TypeError, "%s has dtype %s, expected %s", name, c10::toString(t.scalar_type()), c10::toString(dt));
+  if (t.sizes() != shape)
+    fail(PyExc_ValueError, "%s has shape %s, expected %s", name, text(t.sizes()).c_str(), text(shape).c_str());
+  const int64_t heads = shape[2], d = shape[3];
+  if ((d > 1 && t.stride(3) != 1) || (heads > 1 && t.stride(2) != d))
+    fail(PyExc_ValueError, "the heads of a token of %s must be contiguous", name);
+  if (t.get_device() != dev)
+    fail(PyExc_ValueError, "%s lies on cuda:%d, the current device is cuda:%d", name,
+         static_cast<int>(t.get_device()), dev);
+  return {t.data_ptr(), shape[0] > 1 ? t.stride(0) : 0, shape[1] > 1 ? t.stride(1) : 0, heads};
+}
+
+// The table [rotary / 2] int64 and the positions [axes, B, L] int32 or None.
+struct Angles {
+  const long long* table;
+  const int* pos;
+  int axes, rotary;
+};
+Angles angles(PyObject* to, PyObject* po, int64_t B, int64_t L, int dev) {
+  const Tensor& t = tensor(to, "table");
+  if (t.dim() != 1) fail(PyExc_ValueError, "table must have one dimension");
+  want(t, "table", t.sizes(), at::kLong, dev);
+  Angles r{reinterpret_cast<const long long*>(t.data_ptr<int64_t>()), nullptr, 1, small(2 * t.size(0))};
+  if (po != Py_None) {
+    const Tensor& p = tensor(po, "positions");
+    if (p.dim() != 3) fail(PyExc_ValueError, "positions must be [axes, B, L]");
+    const int64_t ps[3] = {p.size(0), B, L};
+    want(p, "positions", ps, kI32, dev);
+    r.pos = ints(p);
+    r.axes = small(p.size(0));
+  }
+  return r;
+}
+
+// (q, k or None, table, positions, interleaved, backward, out_q, out_k, stream)
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 9);
+  const Tensor& q = tensor(a[0], "q");
+  const int dev = c10::cuda::current_device();
+  const Four s = four(q, "q");
+  const auto dt = q.scalar_type();
+  const int code = dtype_code(q);
+  const View qv = view(q, "q", q.sizes(), dt, dev);
+  View kv{nullptr, 0, 0, 0}, ko{nullptr, 0, 0, 0};
+  int64_t ks[4] = {s.a, s.b, 0, s.d};
+  if (a[1] != Py_None) {
+    const Tensor& k = tensor(a[1], "k");
+    ks[2] = four(k, "k").c;
+    kv = view(k, "k", ks, dt, dev);
+  }
+  const Angles g = angles(a[2], a[3], s.a, s.b, dev);
+  const int interleaved = truth(a[4]) ? 1 : 0, backward = truth(a[5]) ? 1 : 0;
+  const Stream stream(a[8], dev);
+  const Tensor out = a[6] == Py_None ? at::empty(q.sizes(), q.options()) : tensor(a[6], "out_q");
+  const View qo = view(out, "out_q", q.sizes(), dt, dev);
+  Tensor out_k;
+  if (a[1] != Py_None) {
+    out_k = a[7] == Py_None ? at::empty(ks, q.options()) : tensor(a[7], "out_k");
+    ko = view(out_k, "out_k", ks, dt, dev);
+  } else if (a[7] != Py_None) {
+    fail(PyExc_ValueError, "out_k without k");
+  }
+  const fa_status st = fa_rope(qv.p, qv.batch, qv.token, kv.p, kv.batch, kv.token, qo.p, qo.batch, qo.token, ko.p,
+                               ko.batch, ko.token, g.table, g.pos, g.axes, small(s.a), small(s.b), small(s.c),
+                               small(kv.heads), small(s.d), g.rotary, interleaved, backward, code, stream);
+  if (st != FA_OK) return status(st);
+  if (a[1] != Py_None) return tuple_of({out, out_k});
+  PyObject* r = PyTuple_New(2);
+  if (r == nullptr) return nullptr;
+  PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(out));
+  Py_INCREF(Py_None);
+  PyTuple_SET_ITEM(r, 1, Py_None);
+  return r;
+  END_HANDLE_TH_ERRORS
+}
+
+// (q, k, v, k_cache, v_cache, block_table, start, table, positions, counts, interleaved, weights,
+//  new_weights, out, stream)
+PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 15);
+  const Tensor& q = tensor(a[0], "q");
+  const int dev = c10::cuda::current_device();
+  const Four s = four(q, "q");
+  const auto dt = q.scalar_type();
+  const int code = dtype_code(q);
+  const Pools p = pools(a[3], a[4], dt, dev);
+  const int64_t qs[4] = {s.a, s.b, s.c, p.d}, ks[4] = {s.a, s.b, p.hkv, p.d};
+  const View qv = view(q, "q", qs, dt, dev), kv = view(tensor(a[1], "k"), "k", ks, dt, dev),
+             vv = view(tensor(a[2], "v"), "v", ks, dt, dev);
+  const Tensor& table = tensor(a[5], "block_table");
+  const int64_t P = columns(table, "block_table"), ts[2] = {s.a, P}, bs[1] = {s.a};
+  want(table, "block_table", ts, kI32, dev);
+  const Tensor& start = wanted(a[6], "start", bs, kI32, dev);
+  const Angles g = angles(a[7], a[8], s.a, s.b, dev);
+  const int* counts = a[9] == Py_None ? nullptr : ints(wanted(a[9], "counts", bs, kI32, dev));
+  const int interleaved = truth(a[10]) ? 1 : 0;
+  long long wst = 0;
+  float* w = a[11] == Py_None ? nullptr : weights_of(a[11], s.a, p.hkv, P * p.page, dev, wst);
+  const int64_t ns[3] = {s.a, p.hkv, s.b};
+  const float* nw =
+      a[12] == Py_None ? nullptr : wanted(a[12], "new_weights", ns, kF32, dev).data_ptr<float>();
+  const Stream stream(a[14], dev);
+  const Tensor out = a[13] == Py_None ? at::empty(qs, q.options()) : tensor(a[13], "out");
+  const View qo = view(out, "out", qs, dt, dev);
+  const fa_status st = fa_paged_append(
+      qv.p, qv.batch, qv.token, kv.p, kv.batch, kv.token, vv.p, vv.batch, vv.token, qo.p, qo.batch, qo.token,
+      p.k.data_ptr(), p.v.data_ptr(), p.kst, p.vst, ints(table), ints(start), counts, g.table, g.pos, g.axes, w, wst,
+      nw, small(s.a), small(s.b), small(s.c), small(p.hkv), small(p.d), g.rotary, interleaved, small(p.page), small(P),
+      small(p.pages), code, stream);
+  return st == FA_OK ? THPVariable_Wrap(out) : status(st);
+  END_HANDLE_TH_ERRORS
+}
+
+// (q, k_cache, v_cache, prefix_table, prefix_lens, block_table, lens, group_starts, out, lse, workspace, stream)
+PyObject* paged_prefix_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 12);
+  const Tensor& q = tensor(a[0], "q");
+  const int dev = c10::cuda::current_device();
+  const Four s = four(q, "q");
+  const auto dt = q.scalar_type();
+  const int code = dtype_code(q);
+  const Pools p = pools(a[1], a[2], dt, dev);
+  const int64_t qs[4] = {s.a, s.b, s.c, p.d}, ls[3] = {s.a, s.c, s.b}, bs[1] = {s.a};
+  want(q, "q", qs, dt, dev);
+  const Tensor& ptable = tensor(a[3], "prefix_table");
+  const int64_t PP = columns(ptable, "prefix_table"), groups = ptable.size(0), ps[2] = {groups, PP}, gs[1] = {groups},
+                ss[1] = {groups + 1};
+  want(ptable, "prefix_table", ps, kI32, dev);
+  const Tensor& plens = wanted(a[4], "prefix_lens", gs, kI32, dev);
+  const Tensor& table = tensor(a[5], "block_table");
+  const int64_t P = columns(table, "block_table"), ts[2] = {s.a, P};
+  want(table, "block_table", ts, kI32, dev);
+  const Tensor& lens = wanted(a[6], "lens", bs, kI32, dev);
+  const int* starts = nullptr;
+  if (a[7] != Py_None)
+    starts = ints(wanted(a[7], "group_starts", ss, kI32, dev));
+  else if (groups != 1)
+    fail(PyExc_ValueError, "group_starts is needed for %lld groups", static_cast<long long>(groups));
+  const int B = small(s.a), Lq = small(s.b), H = small(s.c), Hkv = small(p.hkv), D = small(p.d),
+            page = small(p.page), G = small(groups);
+  const Stream stream(a[11], dev);
+  const Tensor out = output(a[8], "out", qs, dt, dev, q);
+  const Tensor lse = output(a[9], "lse", ls, kF32, dev, q);
+  const Tensor ws = workspace(
+      a[10], fa_paged_prefix_decode_workspace_size(B, Lq, H, Hkv, D, page, G, small(PP), small(P)), dev, q);
+  const fa_status st = fa_paged_prefix_decode(
+      q.data_ptr(), p.k.data_ptr(), p.v.data_ptr(), p.kst, p.vst, ints(ptable), ints(plens), starts, ints(table),
+      ints(lens), out.data_ptr(), lse.data_ptr<float>(), ws.data_ptr(), ws.numel() * ws.element_size(), B, Lq, H, Hkv,
+      D, page, G, small(PP), small(P), small(p.pages), code, stream);
+  return st == FA_OK ? tuple_of({out, lse}) : status(st);
+  END_HANDLE_TH_ERRORS
+}
+
 // (k_cache, v_cache, block_table, lens, weights, dst_table, keep, sinks, recent, kept,
 //  new_lens, new_weights, stream)
 PyObject* paged_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -408,6 +574,7 @@ PyObject* key_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
   { #f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {FA_METHOD(window_fwd),   FA_METHOD(window_bwd),  FA_METHOD(paged_write),
                          FA_METHOD(paged_decode), FA_METHOD(paged_evict), FA_METHOD(key_weights),
+                         FA_METHOD(rope),         FA_METHOD(paged_append), FA_METHOD(paged_prefix_decode),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods};
 

@@ -79,6 +79,47 @@ fa_status run_paged_write(const void* K, const void* V, void* Kc, void* Vc, long
                           float* weights, long long wstride, const float* new_w, int B, int L,
                           int Hkv, int D, int page, int max_pages, int num_pages, cudaStream_t s);
 unsigned int paged_read_error(cudaStream_t s);
+// Over the sequences' own keys behind a shared prefix: O in fp32 (paged_own.cu).
+fa_status run_paged_own(const PagedDecodeArgs& a, cudaStream_t s);
+unsigned int paged_own_read_error(cudaStream_t s);
+
+// Decoding behind shared prefixes (prefix.cu).
+struct PrefixDecodeArgs {
+  const void *Q, *K, *V;
+  const int *prefix_table, *prefix_lens, *group_starts, *table, *lens;
+  void* O;
+  float* LSE;
+  long long k_page_stride, v_page_stride;
+  void* workspace;
+  size_t workspace_bytes;
+  int B, Lq, H, Hkv, D, page, groups, prefix_pages, max_pages, num_pages, dtype;
+};
+size_t paged_prefix_workspace_size(const PrefixDecodeArgs& a);
+fa_status run_paged_prefix(const PrefixDecodeArgs& a, cudaStream_t s);
+unsigned int prefix_read_error(cudaStream_t s);
+
+// Rotary positions and the append to the paged cache (rope.cu).
+struct RopeView {  // [B, L, heads, D], the last two dims contiguous
+  const void* p;
+  long long batch, token;  // elements between two batch entries, two tokens
+};
+struct RopeArgs {
+  RopeView q, k, qy, ky;
+  const void* table;
+  const int* positions;
+  int axes, B, L, H, Hkv, D, rotary, neighbours, back, dtype;
+};
+struct PagedAppendArgs {
+  RopeView v;
+  void *K_pool, *V_pool;
+  const int *table, *start, *counts;
+  float* weights;
+  const float* new_weights;
+  long long weights_stride, k_page_stride, v_page_stride;
+  int page, max_pages, num_pages;
+};
+fa_status run_rope(const RopeArgs& a, cudaStream_t s);
+fa_status run_paged_append(const RopeArgs& a, const PagedAppendArgs& c, cudaStream_t s);
 
 // Eviction (evict.cu).
 struct PagedEvictArgs {

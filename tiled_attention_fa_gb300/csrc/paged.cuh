@@ -343,7 +343,7 @@ __device__ __forceinline__ int paged_count_in(unsigned long long* word, unsigned
 // rows of 3 partials: 17,500 cycles with conditions and a float per read, 7400
 // without the meeting, 3500 so).
 // Reads past L1: other SMs wrote them.
-template <int D, typename T, int R>
+template <int D, typename TO, int R>
 __device__ __forceinline__ void paged_join(const PagedParams& p, int b, int hkv, int slot0, int slot1,
                                            int n) {
   constexpr int U = R * (D / 4) >= 512 ? 4 : R * (D / 4) >= 256 ? 2 : 1, C = 16 / U;
@@ -398,9 +398,13 @@ __device__ __forceinline__ void paged_join(const PagedParams& p, int b, int hkv,
       if (row < p.rows) {
         const int ql = row * p.ginv >> 16, h = hkv * p.g + row - ql * p.g;
         const float inv = den[u] > 0.f ? __fdividef(1.f, den[u]) : 0.f;
-        *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.O) +
-                                  ((static_cast<size_t>(b) * p.Lq + ql) * p.H + h) * D + d) =
-            make_uint2(pack2<T>(acc[u].x * inv, acc[u].y * inv), pack2<T>(acc[u].z * inv, acc[u].w * inv));
+        TO* dst = reinterpret_cast<TO*>(p.O) + ((static_cast<size_t>(b) * p.Lq + ql) * p.H + h) * D + d;
+        if constexpr (sizeof(TO) == 4)
+          *reinterpret_cast<float4*>(dst) =
+              make_float4(acc[u].x * inv, acc[u].y * inv, acc[u].z * inv, acc[u].w * inv);
+        else
+          *reinterpret_cast<uint2*>(dst) =
+              make_uint2(pack2<TO>(acc[u].x * inv, acc[u].y * inv), pack2<TO>(acc[u].z * inv, acc[u].w * inv));
         if (d == 0)
           p.LSE[(static_cast<size_t>(b) * p.H + h) * p.Lq + ql] =
               den[u] == 0.f ? -INFINITY : (mx[u] + __log2f(den[u])) * 0.6931471805599453f;
@@ -409,13 +413,18 @@ __device__ __forceinline__ void paged_join(const PagedParams& p, int b, int hkv,
   }
 }
 
-template <int D, bool BF16, int R>
+// OWN: the sequences' own keys behind a shared prefix.  O is left in fp32, to be
+// joined with the prefix's partials; the kernel runs beside the prefix kernel,
+// its predecessor in the stream, which let it start only after everything before
+// was done, and so waits for that kernel at its end instead of its beginning.
+template <int D, bool BF16, int R, bool OWN = false>
 __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
     fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ,
                            const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
   using Ly = PagedLayout<D, R>;
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  using TO = typename std::conditional<OWN, float, T>::type;
   constexpr int N = Ly::N;
   constexpr int CW = R < 32 ? R : 32, NCH = R / CW;
   constexpr uint32_t IDESC_S = idesc_f16(BF16, 128, N, false, false);
@@ -455,7 +464,7 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
   // Everything above overlaps the end of the kernel before; nothing of global
   // memory was touched.
   pdl_launch_dependents();
-  pdl_wait();
+  if constexpr (!OWN) pdl_wait();
   const int len = (p.B <= 32 && static_cast<int>(lane) < p.B) ? p.lens[lane] : 0;
   if (warp == 0) lens_s[lane] = len;
   paged_plan<Ly::NTHREADS>(p, blockIdx.x, gridDim.x, len, sums, plan);
@@ -904,7 +913,7 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
         const bool has[2] = {in_item >= 2 || i % Ly::NG == 0, in_item >= 2 || i % Ly::NG == 1};
         if (t < D) {
           const uint32_t tO = tmem + lane_off + Ly::TM_O + ob * Ly::NG * N;
-          T* dst = reinterpret_cast<T*>(p.O) + (static_cast<size_t>(w.b) * p.Lq * p.H + w.hkv * p.g) * D + t;
+          TO* dst = reinterpret_cast<TO*>(p.O) + (static_cast<size_t>(w.b) * p.Lq * p.H + w.hkv * p.g) * D + t;
           float* part = p.part_o + static_cast<size_t>(slot) * p.rows * D + t;
           constexpr int OC = 16;
           int hh = 0;
@@ -931,7 +940,7 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
 #pragma unroll
               for (int r = 0; r < OC; ++r)
                 if (c * OC + r < R && c * OC + r < p.rows) {
-                  dst[static_cast<size_t>(hh) * D] = static_cast<T>(v[r]);
+                  dst[static_cast<size_t>(hh) * D] = static_cast<TO>(v[r]);
                   if (++hh == p.g) {  // next query
                     hh = 0;
                     dst += static_cast<size_t>(p.H) * D;
@@ -965,7 +974,7 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
           ++joins;
           if (*flag) {
             const int slot0 = 2 * c0 + (start > paged_part(total, G, c0) ? 1 : 0);
-            paged_join<D, T, R>(p, w.b, w.hkv, slot0, 2 * (c0 + 1), c1 - c0 + 1);
+            paged_join<D, TO, R>(p, w.b, w.hkv, slot0, 2 * (c0 + 1), c1 - c0 + 1);
           }
         }
       }
@@ -973,8 +982,8 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
     // Empty sequences: O = 0, LSE = -inf.
     for (int b = blockIdx.x; gr == 0 && b < p.B; b += G) {
       if (p.lens[b] > 0) continue;
-      T* dst = reinterpret_cast<T*>(p.O) + static_cast<size_t>(b) * p.Lq * p.H * D;
-      for (int x = t; x < p.Lq * p.H * D; x += 128) dst[x] = static_cast<T>(0.f);
+      TO* dst = reinterpret_cast<TO*>(p.O) + static_cast<size_t>(b) * p.Lq * p.H * D;
+      for (int x = t; x < p.Lq * p.H * D; x += 128) dst[x] = static_cast<TO>(0.f);
       for (int x = t; x < p.Lq * p.H; x += 128)
         p.LSE[static_cast<size_t>(b) * p.Lq * p.H + x] = -INFINITY;
     }
@@ -987,12 +996,13 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, Ly::TMEM_COLS);
   }
+  if constexpr (OWN) pdl_wait();
 }
 
 // Add every visible key's attention weight, sum over the item's rows of
 // exp(s - LSE), from the raw scores the decode kernel left.  Block (x, bh):
 // tiles 8x .. 8x + 7 of the item's list; each key belongs to one thread.
-__global__ void __launch_bounds__(256)
+static __global__ void __launch_bounds__(256)
     fa_paged_weights_kernel(const PagedParams p, float* __restrict__ weights, long long wstride) {
   pdl_wait();
   __shared__ float lse2[128];
@@ -1027,7 +1037,7 @@ __global__ void __launch_bounds__(256)
 // Copy new keys and values into the pages, and set their slots' weights.
 // One thread per 16 bytes of K (and of V).  One token of 8 sequences, 32 heads of
 // D 64: 2.4 us, a launch.
-__global__ void __launch_bounds__(256)
+static __global__ void __launch_bounds__(256)
     fa_paged_write_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
                           uint4* __restrict__ kc, uint4* __restrict__ vc, long long k_page,
                           long long v_page, const int* __restrict__ table,
