@@ -25,7 +25,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB_NAME = "libfa_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 UNITS = ["api.cu", "fwd.cu", "bwd.cu", "decode.cu", "paged.cu", "weights.cu", "evict.cu", "rope.cu",
-         "prefix.cu", "paged_own.cu"]
+         "prefix.cu"]
 BINDING_PATH = os.path.join(HERE, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -590,10 +590,9 @@ fa_status fa_key_weights(const void* Q, const void* K, const float* LSE, float* 
 
 fa_status fa_check_device_error(void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned int words[7] = {fa::fwd_read_error(s),     fa::bwd_read_error(s),
-                                 fa::decode_read_error(s),  fa::paged_read_error(s),
-                                 fa::weights_read_error(s), fa::paged_own_read_error(s),
-                                 fa::prefix_read_error(s)};
+  const unsigned int words[6] = {fa::fwd_read_error(s), fa::bwd_read_error(s),
+                                 fa::decode_read_error(s), fa::paged_read_error(s),
+                                 fa::weights_read_error(s), fa::prefix_read_error(s)};
   unsigned int site = 0;
   for (unsigned int w : words) {
     if (w == 0xFFFFFFFFu) return FA_ERR_CUDA;

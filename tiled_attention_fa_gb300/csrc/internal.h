@@ -79,9 +79,6 @@ fa_status run_paged_write(const void* K, const void* V, void* Kc, void* Vc, long
                           float* weights, long long wstride, const float* new_w, int B, int L,
                           int Hkv, int D, int page, int max_pages, int num_pages, cudaStream_t s);
 unsigned int paged_read_error(cudaStream_t s);
-// Over the sequences' own keys behind a shared prefix: O in fp32 (paged_own.cu).
-fa_status run_paged_own(const PagedDecodeArgs& a, cudaStream_t s);
-unsigned int paged_own_read_error(cudaStream_t s);
 
 // Decoding behind shared prefixes (prefix.cu).
 struct PrefixDecodeArgs {

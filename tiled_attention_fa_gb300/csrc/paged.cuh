@@ -57,7 +57,7 @@
 
 namespace fa {
 
-struct PagedParams {
+struct PagedBase {
   const int* table;  // [B, max_pages]
   const int* lens;   // [B]
   void* O;           // [B, Lq, H, D]
@@ -66,13 +66,21 @@ struct PagedParams {
   unsigned long long nonce;   // nonce << 16 | arrivals, 0 again when all have come
   float* part_o;     // [2 G, rows, D]
   float* part_lse;   // [2 G, rows], log2 units
-  float* scores;     // [B * Hkv, max_tiles, rows, 128] raw scores for the weights, or NULL
   int B, Lq, H, Hkv, g, rows;
   int ginv;                  // 65536 / g + 1: row / g = row * ginv >> 16 for the rows there are (128 at most)
   int page, max_pages, cap;  // cap = max_pages * page
   int max_tiles;             // ceil(cap / 128)
-  int window, sinks;         // window 0: none (then sinks 0)
   float sl2;                 // log2(e) / sqrt(D)
+};
+struct PagedParams : PagedBase {
+  int window, sinks;  // window 0: none (then sinks 0)
+  float* scores;      // [B * Hkv, max_tiles, rows, 128] raw scores for the weights, or NULL
+};
+// Own keys behind a shared prefix: no window, no weights.
+struct PagedOwnParams : PagedBase {
+  static constexpr int window = 0, sinks = 0;
+  static constexpr float* scores = nullptr;
+  int* ends;  // [B * Hkv][2], an item's first and last part
 };
 
 // The tiles one sequence's items visit: ns sink tiles, then lo, lo + 1, ....
@@ -82,7 +90,8 @@ struct PagedSeq {
   int ns, lo, cnt;
 };
 
-__device__ __forceinline__ PagedSeq paged_seq_of(int len, const PagedParams& p) {
+template <class P>
+__device__ __forceinline__ PagedSeq paged_seq_of(int len, const P& p) {
   PagedSeq s;
   s.n = min(max(len, 0), p.cap);
   s.wlo = p.window ? max(max(s.n - p.Lq, 0) - p.window + 1, 0) : 0;
@@ -110,7 +119,8 @@ struct PagedWalk {
     left = min(s.cnt - k, rem);
     first = true;
   }
-  __device__ __forceinline__ void skip(const PagedParams& p, int n) {  // n <= left
+  template <class P>
+  __device__ __forceinline__ void skip(const P& p, int n) {  // n <= left
     rem -= n;
     left -= n;
     first = false;
@@ -122,6 +132,7 @@ struct PagedWalk {
       ++item;
       if (++hkv == p.Hkv) {
         hkv = 0;
+#pragma unroll 1
         do {
           if (++b >= p.B) {
             rem = 0;
@@ -133,7 +144,8 @@ struct PagedWalk {
       enter();
     }
   }
-  __device__ __forceinline__ void next(const PagedParams& p) { skip(p, 1); }
+  template <class P>
+  __device__ __forceinline__ void next(const P& p) { skip(p, 1); }
 };
 
 // Part c of G of `total` tiles begins at tile:
@@ -222,8 +234,8 @@ __device__ __forceinline__ float paged_rows_reduce(float (&x)[CW], uint32_t lane
 // Part c of G of the list of all tiles: the start and length of the walk in
 // `plan` {b, hkv, k, n}, t0 and the total in plan[4], plan[5].  Called by the
 // whole CTA (NT threads); `len` is lens[lane] for the small case, read early.
-template <int NT>
-__device__ __forceinline__ void paged_plan(const PagedParams& p, int c, int G, int len, int* sums,
+template <int NT, class P>
+__device__ __forceinline__ void paged_plan(const P& p, int c, int G, int len, int* sums,
                                            int* plan) {
   const uint32_t lane = lane_id();
   if (p.B <= 32) {
@@ -257,6 +269,7 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, int c, int G, i
   const int per = (p.B + NT - 1) / NT;
   const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
   int mine = 0;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) mine += paged_seq_of(p.lens[b], p).cnt * p.Hkv;
   int incl = mine;
 #pragma unroll
@@ -280,6 +293,7 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, int c, int G, i
   }
   if (n > 0 && t0 >= before && t0 < before + mine) {
     int at = before;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       const int cnt = paged_seq_of(p.lens[b], p).cnt, all = cnt * p.Hkv;
       if (t0 < at + all) {
@@ -294,7 +308,8 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, int c, int G, i
   __syncthreads();
 }
 
-__device__ __forceinline__ PagedWalk paged_walk(const PagedParams& p, const int* plan, const int* lens) {
+template <class P>
+__device__ __forceinline__ PagedWalk paged_walk(const P& p, const int* plan, const int* lens) {
   PagedWalk w;
   w.lens = lens;
   w.rem = plan[3];
@@ -319,6 +334,7 @@ __device__ __forceinline__ PagedWalk paged_walk(const PagedParams& p, const int*
 __device__ __forceinline__ int paged_count_in(unsigned long long* word, unsigned long long nonce, int n,
                                               unsigned long long cur) {
   int seen = 0;
+#pragma unroll 1
   for (;;) {  // ends: a failed swap means that another part put the nonce there (nothing else writes)
     if ((cur >> 16) == nonce) {  // (it stays until the last part is here)
       seen = static_cast<int>(atomicAdd(word, 1ull) & 0xFFFFu);
@@ -343,7 +359,7 @@ __device__ __forceinline__ int paged_count_in(unsigned long long* word, unsigned
 // rows of 3 partials: 17,500 cycles with conditions and a float per read, 7400
 // without the meeting, 3500 so).
 // Reads past L1: other SMs wrote them.
-template <int D, typename TO, int R>
+template <int D, typename T, int R>
 __device__ __forceinline__ void paged_join(const PagedParams& p, int b, int hkv, int slot0, int slot1,
                                            int n) {
   constexpr int U = R * (D / 4) >= 512 ? 4 : R * (D / 4) >= 256 ? 2 : 1, C = 16 / U;
@@ -398,13 +414,9 @@ __device__ __forceinline__ void paged_join(const PagedParams& p, int b, int hkv,
       if (row < p.rows) {
         const int ql = row * p.ginv >> 16, h = hkv * p.g + row - ql * p.g;
         const float inv = den[u] > 0.f ? __fdividef(1.f, den[u]) : 0.f;
-        TO* dst = reinterpret_cast<TO*>(p.O) + ((static_cast<size_t>(b) * p.Lq + ql) * p.H + h) * D + d;
-        if constexpr (sizeof(TO) == 4)
-          *reinterpret_cast<float4*>(dst) =
-              make_float4(acc[u].x * inv, acc[u].y * inv, acc[u].z * inv, acc[u].w * inv);
-        else
-          *reinterpret_cast<uint2*>(dst) =
-              make_uint2(pack2<TO>(acc[u].x * inv, acc[u].y * inv), pack2<TO>(acc[u].z * inv, acc[u].w * inv));
+        *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.O) +
+                                  ((static_cast<size_t>(b) * p.Lq + ql) * p.H + h) * D + d) =
+            make_uint2(pack2<T>(acc[u].x * inv, acc[u].y * inv), pack2<T>(acc[u].z * inv, acc[u].w * inv));
         if (d == 0)
           p.LSE[(static_cast<size_t>(b) * p.H + h) * p.Lq + ql] =
               den[u] == 0.f ? -INFINITY : (mx[u] + __log2f(den[u])) * 0.6931471805599453f;
@@ -413,63 +425,44 @@ __device__ __forceinline__ void paged_join(const PagedParams& p, int b, int hkv,
   }
 }
 
-// OWN: the sequences' own keys behind a shared prefix.  O is left in fp32, to be
-// joined with the prefix's partials; the kernel runs beside the prefix kernel,
-// its predecessor in the stream, which let it start only after everything before
-// was done, and so waits for that kernel at its end instead of its beginning.
-template <int D, bool BF16, int R, bool OWN = false>
-__global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
-    fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ,
-                           const __grid_constant__ CUtensorMap tmK,
-                           const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
+// The tiles' numbers among the groups: tile v is group v % NG's, its v / NG-th, and
+// has S buffer v % NB for the (v / NB)-th time.  In turn, the i-th tile of a part
+// is tile i; with whole items for a group, each group counts its own.
+template <bool OWN>
+struct PagedTurn {
+  bool single;
+  int n0 = 0, n1 = 0;
+  __device__ __forceinline__ bool alone() const { return OWN && single; }
+  __device__ __forceinline__ int of(const PagedWalk& w, int i) {
+    if (!alone()) return i;
+    return w.item & 1 ? 2 * n1++ + 1 : 2 * n0++;
+  }
+};
+
+// The roles of one CTA, part c of G of the list of all tiles, whose start `plan`
+// holds; every warp of the CTA comes here and leaves together.
+// OWN: for the join with a prefix's attention, every item's share in a part is a
+// partial (fp32, in slot item + part) and nothing is joined here.  Where items are
+// short (`single`), a group takes all tiles of every second item: with the tiles
+// in turn, each item's end waits for both groups, which are busy with the ends of
+// other items (items of 1 to 4 tiles: 11,000 cycles each).
+template <int D, bool BF16, int R, class P>
+__device__ __forceinline__ void paged_body(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                           const P& p, uint8_t* gbase, uint32_t base, uint32_t tmem,
+                                           AbortState* ab, int* plan, const int* lens, int part_c, int G,
+                                           bool single) {
   using Ly = PagedLayout<D, R>;
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  using TO = typename std::conditional<OWN, float, T>::type;
+  constexpr bool OWN = std::is_same<P, PagedOwnParams>::value;
   constexpr int N = Ly::N;
   constexpr int CW = R < 32 ? R : 32, NCH = R / CW;
   constexpr uint32_t IDESC_S = idesc_f16(BF16, 128, N, false, false);
   constexpr uint32_t IDESC_PV = idesc_f16(BF16, 128, N, true, false);
-
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* gbase = smem_raw + (base - raw);
+  static_assert(!OWN || (Ly::NG == 2 && Ly::PB == Ly::NB), "items of one group");
+  using Turn = PagedTurn<OWN>;
   auto bar = [&](int i) -> uint32_t { return base + Ly::BAR_OFF + 8u * i; };
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + Ly::MISC_OFF);
-  AbortState* ab = reinterpret_cast<AbortState*>(gbase + Ly::MISC_OFF + 8);
-  int* plan = reinterpret_cast<int*>(gbase + Ly::MISC_OFF + 16);
-  int* sums = reinterpret_cast<int*>(gbase + Ly::MISC_OFF + 48);      // NTHREADS / 32
-  int* lens_s = reinterpret_cast<int*>(gbase + Ly::MISC_OFF + 128);   // 32
-  const int* lens = p.B <= 32 ? lens_s : p.lens;
   unsigned int* err = device_error_word();
   const uint32_t warp = warp_id(), lane = lane_id();
-
-  // Query rows past g * Lq, and P rows no thread writes, are zero.
-  for (uint32_t i = threadIdx.x; i < (Ly::QS * Ly::QT + Ly::PB * Ly::PT) / 16u; i += Ly::NTHREADS)
-    reinterpret_cast<uint4*>(gbase + Ly::Q_OFF)[i] = make_uint4(0, 0, 0, 0);
-  fence_proxy_async_smem();
-  for (int i = threadIdx.x; i < Ly::NBAR; i += Ly::NTHREADS) mbar_init(bar(i), Ly::arrivals(i));
-  if (threadIdx.x == 0) ab->flag = 0;
-  fence_barrier_init();
-  if (warp == Ly::SW + 1) {
-    tmem_alloc(base + Ly::MISC_OFF, Ly::TMEM_COLS);
-    tmem_relinquish();
-  }
-  if (warp == Ly::SW && lane == 0) {
-    tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
-  }
-  tc_fence_before();
-  // Everything above overlaps the end of the kernel before; nothing of global
-  // memory was touched.
-  pdl_launch_dependents();
-  if constexpr (!OWN) pdl_wait();
-  const int len = (p.B <= 32 && static_cast<int>(lane) < p.B) ? p.lens[lane] : 0;
-  if (warp == 0) lens_s[lane] = len;
-  paged_plan<Ly::NTHREADS>(p, blockIdx.x, gridDim.x, len, sums, plan);
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
 
   if (warp == Ly::SW) {
     // ------------------------------------------------------------ producer
@@ -480,126 +473,151 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
     uint32_t stage = 0, phase = 0, used = 0, qcnt = 0;
     bool ok = true;
     const uint64_t stream = policy_evict_first();
-    // Page ids of the next tiles, one box per lane: `cur` for the tiles from
-    // cur_tile on, `nxt` for the batch behind it (of the same item or the next).
-    PagedWalk ahead = paged_walk(p, plan, lens);
+    // Page ids of the next tiles, one box per lane: `cur` for the tiles at hand,
+    // `nxt` for the batch behind it (of the same item or the next).
+    PagedWalk kw = paged_walk(p, plan, lens), ahead = kw;
     int nxt = -1, nxt_n = 0, cur = -1, cur_at = 0, cur_n = 0;
-    auto fetch = [&]() {
-      nxt_n = 0;
-      if (ahead.rem <= 0) return;
-      nxt_n = min(per_batch, ahead.left);
-      if (ahead.k < ahead.s.ns) nxt_n = min(nxt_n, ahead.s.ns - ahead.k);  // up to the gap
-      const int at = (ahead.tile * 128 + static_cast<int>(lane) * box) >> page_log;
-      nxt = (static_cast<int>(lane) < nxt_n * nbox && at < p.max_pages)
-                ? p.table[static_cast<size_t>(ahead.b) * p.max_pages + at]
-                : -1;
-      ahead.skip(p, nxt_n);
-    };
-    // The page id of this lane's box of the next tile in order.
-    auto next_page = [&]() -> int {
-      if (cur_at == cur_n) {
-        cur = nxt;
-        cur_n = nxt_n;
-        cur_at = 0;
-        fetch();
+    // This lane's box of the K tiles whose V is still to come: page, row (-1: not
+    // loaded), K/V head, and how many boxes the tile has.
+    int v_page[Ly::NG + 1], v_row[Ly::NG + 1], v_head[Ly::NG + 1];
+    uint32_t v_boxes[Ly::NG + 1];
+    int v_left = kw.rem, pending = 0;
+#pragma unroll 1
+    while (ok && v_left > 0) {
+      const bool is_k = kw.rem > 0 && pending <= Ly::NG;
+      int page, row, head;
+      uint32_t boxes;
+      if (is_k) {
+        if (cur_at == cur_n) {
+#pragma unroll 1
+          do {  // (twice at the start)
+            cur = nxt;
+            cur_n = nxt_n;
+            cur_at = 0;
+            nxt_n = 0;
+            if (ahead.rem > 0) {
+              nxt_n = min(per_batch, ahead.left);
+              if (ahead.k < ahead.s.ns) nxt_n = min(nxt_n, ahead.s.ns - ahead.k);  // up to the gap
+              const int at = (ahead.tile * 128 + static_cast<int>(lane) * box) >> page_log;
+              nxt = (static_cast<int>(lane) < nxt_n * nbox && at < p.max_pages)
+                        ? p.table[static_cast<size_t>(ahead.b) * p.max_pages + at]
+                        : -1;
+              ahead.skip(p, nxt_n);
+            }
+          } while (cur_n == 0);
+        }
+        page = __shfl_sync(0xffffffffu, cur, (cur_at++ * nbox + static_cast<int>(lane)) & 31);
+        if (kw.first) {
+          const uint32_t slot = qcnt % Ly::QS, round = qcnt / Ly::QS;
+          if (round > 0 && !mbar_wait_warp_call(bar(Ly::B_QEMPTY + slot), (round - 1) & 1, ab, err, 1002)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(Ly::B_QFULL + slot), Ly::KCH * p.rows * 128u);
+#pragma unroll
+            for (int c = 0; c < Ly::KCH; ++c)
+              tma_load_4d(base + Ly::Q_OFF + slot * Ly::QT + c * Ly::QCH, &tmQ, bar(Ly::B_QFULL + slot), c * 64,
+                          kw.hkv * p.g, 0, kw.b);
+          }
+          ++qcnt;
+        }
+        // Boxes that hold a key some query sees; the others are not loaded.
+        const int k0 = kw.tile * 128 + static_cast<int>(lane) * box;
+        const bool go = static_cast<int>(lane) < nbox && k0 < kw.s.n && (k0 + box > kw.s.wlo || k0 < p.sinks);
+        boxes = __popc(__ballot_sync(0xffffffffu, go));
+        row = go ? k0 & (p.page - 1) : -1;
+        head = kw.hkv;
+#pragma unroll
+        for (int x = 0; x <= Ly::NG; ++x)
+          if (x == pending) {
+            v_page[x] = page;
+            v_row[x] = row;
+            v_head[x] = head;
+            v_boxes[x] = boxes;
+          }
+        ++pending;
+        kw.next(p);
+      } else {
+        page = v_page[0];
+        row = v_row[0];
+        head = v_head[0];
+        boxes = v_boxes[0];
+#pragma unroll
+        for (int x = 0; x < Ly::NG; ++x) {
+          v_page[x] = v_page[x + 1];
+          v_row[x] = v_row[x + 1];
+          v_head[x] = v_head[x + 1];
+          v_boxes[x] = v_boxes[x + 1];
+        }
+        --pending;
+        --v_left;
       }
-      return __shfl_sync(0xffffffffu, cur, (cur_at++ * nbox + static_cast<int>(lane)) & 31);
-    };
-    auto load = [&](const CUtensorMap* map, const PagedWalk& w, int pid) -> bool {
-      if (!mbar_wait_warp(bar(Ly::B_KVEMPTY + stage), phase ^ 1u, ab, err, 1001)) return false;
-      // Boxes that hold a key some query sees; the others are not loaded.
-      const int k0 = w.tile * 128 + static_cast<int>(lane) * box;
-      const bool go = static_cast<int>(lane) < nbox && k0 < w.s.n && (k0 + box > w.s.wlo || k0 < p.sinks);
-      const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, go));
+      if (!mbar_wait_warp_call(bar(Ly::B_KVEMPTY + stage), phase ^ 1u, ab, err, 1001)) {
+        ok = false;
+        break;
+      }
       if (lane == 0)
         mbar_arrive_expect_tx(bar(Ly::B_KVFULL + stage), boxes * box * static_cast<uint32_t>(D) * 2u);
       __syncwarp();
-      if (go) {
-        const int row0 = k0 & (p.page - 1);
+      if (row >= 0) {
+        const CUtensorMap* map = is_k ? &tmK : &tmV;
 #pragma unroll
         for (int c = 0; c < Ly::KCH; ++c)
-          tma_load_4d_hint(base + Ly::RING_OFF + stage * Ly::TILE + c * Ly::CHUNK + lane * box * 128u,
-                           map, bar(Ly::B_KVFULL + stage), c * 64, w.hkv, row0, pid, stream);
+          tma_load_4d_hint(base + Ly::RING_OFF + stage * Ly::TILE + c * Ly::CHUNK + lane * box * 128u, map,
+                           bar(Ly::B_KVFULL + stage), c * 64, head, row, page, stream);
       }
       used |= 1u << stage;
       if (++stage == Ly::STAGES) {
         stage = 0;
         phase ^= 1u;
       }
-      return true;
-    };
-    auto load_q = [&](const PagedWalk& w) -> bool {
-      const uint32_t slot = qcnt % Ly::QS, round = qcnt / Ly::QS;
-      if (round > 0 && !mbar_wait_warp(bar(Ly::B_QEMPTY + slot), (round - 1) & 1, ab, err, 1002))
-        return false;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar(Ly::B_QFULL + slot), Ly::KCH * p.rows * 128u);
-        for (int c = 0; c < Ly::KCH; ++c)
-          tma_load_4d(base + Ly::Q_OFF + slot * Ly::QT + c * Ly::QCH, &tmQ, bar(Ly::B_QFULL + slot),
-                      c * 64, w.hkv * p.g, 0, w.b);
-      }
-      ++qcnt;
-      return true;
-    };
-    PagedWalk kw = ahead, vw = ahead;
-    if (kw.rem > 0) {
-      fetch();
-      int pid[Ly::NG + 1];  // this lane's page of tiles i .. i + NG
-      auto load_k = [&](int x) -> bool {
-        if (kw.rem <= 0) return true;
-        pid[x] = next_page();
-        if (kw.first && !load_q(kw)) return false;
-        if (!load(&tmK, kw, pid[x])) return false;
-        kw.next(p);
-        return true;
-      };
-#pragma unroll
-      for (int x = 0; x < Ly::NG; ++x) ok = ok && load_k(x);
-      while (ok && vw.rem > 0) {
-        ok = load_k(Ly::NG) && load(&tmV, vw, pid[0]);
-        vw.next(p);
-#pragma unroll
-        for (int x = 0; x < Ly::NG; ++x) pid[x] = pid[x + 1];
-      }
-      if (!ok && lane == 0) {
-        // Unwinding: let copies in flight land.  The newest use of a stage
-        // before the write position has this round's parity, the others the
-        // last round's.
-        for (int s = 0; s < Ly::STAGES; ++s)
-          if (used >> s & 1u)
-            mbar_wait_drain(bar(Ly::B_KVFULL + s), s < static_cast<int>(stage) ? phase : phase ^ 1u);
-        for (uint32_t c = qcnt > Ly::QS ? qcnt - Ly::QS : 0; c < qcnt; ++c)
-          mbar_wait_drain(bar(Ly::B_QFULL + c % Ly::QS), (c / Ly::QS) & 1);
-      }
+    }
+    if (!ok && lane == 0) {
+      // Unwinding: let copies in flight land.  The newest use of a stage
+      // before the write position has this round's parity, the others the
+      // last round's.
+#pragma unroll 1
+      for (int s = 0; s < Ly::STAGES; ++s)
+        if (used >> s & 1u)
+          mbar_wait_drain(bar(Ly::B_KVFULL + s), s < static_cast<int>(stage) ? phase : phase ^ 1u);
+#pragma unroll 1
+      for (uint32_t c = qcnt > Ly::QS ? qcnt - Ly::QS : 0; c < qcnt; ++c)
+        mbar_wait_drain(bar(Ly::B_QFULL + c % Ly::QS), (c / Ly::QS) & 1);
     }
   } else if (warp == Ly::SW + 1) {
     // ------------------------------------------------------------ S^T = K Q^T
     // Ring place of K_j: j, or NG + 2 (j - NG) behind the first NG; of V_i:
     // the K tiles loaded before it, min(n, i + 1 + NG), plus i.
     PagedWalk w = paged_walk(p, plan, lens);
+    Turn turn{single};
     bool ok = true;
+#pragma unroll 1
     for (int i = 0; ok && w.rem > 0; w.skip(p, w.left)) {
       const uint32_t qslot = w.item % Ly::QS;
-      if (!mbar_wait_warp(bar(Ly::B_QFULL + qslot), (w.item / Ly::QS) & 1, ab, err, 1003)) { ok = false; break; }
+      if (!mbar_wait_warp_call(bar(Ly::B_QFULL + qslot), (w.item / Ly::QS) & 1, ab, err, 1003)) { ok = false; break; }
       const uint64_t qd = sdesc_sw128(base + Ly::Q_OFF + qslot * Ly::QT, 16, 1024);
+#pragma unroll 1
       for (int x = 0; x < w.left; ++x, ++i) {
         const uint32_t pos = i < Ly::NG ? i : 2 * i - Ly::NG, ks = pos % Ly::STAGES;
-        const int buf = i % Ly::NB;
+        const int vi = turn.of(w, i), buf = vi % Ly::NB;
         // The buffer's last tile is through: its scores are read, and its P is
         // too, so that the softmax may write P again once this S is there.
-        if (i >= Ly::NB &&
-            !mbar_wait_warp(bar(Ly::B_PVDONE + buf), (i / Ly::NB - 1) & 1, ab, err, 1017)) {
+        if (vi >= Ly::NB &&
+            !mbar_wait_warp_call(bar(Ly::B_PVDONE + buf), (vi / Ly::NB - 1) & 1, ab, err, 1017)) {
           ok = false;
           break;
         }
-        if (!mbar_wait_warp(bar(Ly::B_KVFULL + ks), (pos / Ly::STAGES) & 1, ab, err, 1004)) { ok = false; break; }
+        if (!mbar_wait_warp_call(bar(Ly::B_KVFULL + ks), (pos / Ly::STAGES) & 1, ab, err, 1004)) { ok = false; break; }
         tc_fence_after();
         const uint64_t kd = sdesc_sw128(base + Ly::RING_OFF + ks * Ly::TILE, 16, 1024);
         if (elect_one()) {
+#pragma unroll 1
+          for (int c = 0; c < Ly::KCH; ++c)
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_ss(tmem + Ly::TM_S + buf * N, kd + (((k >> 2) * Ly::CHUNK + (k & 3) * 32u) >> 4),
-                   qd + (((k >> 2) * Ly::QCH + (k & 3) * 32u) >> 4), IDESC_S, k > 0 ? 1u : 0u);
+            for (int k = 0; k < 4; ++k)
+              mma_ss(tmem + Ly::TM_S + buf * N, kd + ((c * Ly::CHUNK + k * 32u) >> 4),
+                     qd + ((c * Ly::QCH + k * 32u) >> 4), IDESC_S, (c > 0 || k > 0) ? 1u : 0u);
           tc_commit(bar(Ly::B_SFULL + buf));
           tc_commit(bar(Ly::B_KVEMPTY + ks));
           if (x + 1 == w.left) tc_commit(bar(Ly::B_QEMPTY + qslot));
@@ -614,36 +632,57 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
     // ------------------------------------------------------------ O^T += V^T P^T
     PagedWalk w = paged_walk(p, plan, lens);
     const int n_part = w.rem;
+    Turn turn{single};
     bool ok = true;
+#pragma unroll 1
     for (int i = 0; ok && w.rem > 0; w.skip(p, w.left)) {
       const int ob = w.item & 1;
       if (w.item >= 2 &&
-          !mbar_wait_warp(bar(Ly::B_OEMPTY + ob), ((w.item >> 1) - 1) & 1, ab, err, 1006)) {
+          !mbar_wait_warp_call(bar(Ly::B_OEMPTY + ob), ((w.item >> 1) - 1) & 1, ab, err, 1006)) {
         ok = false;
         break;
       }
+#pragma unroll 1
       for (int x = 0; x < w.left; ++x, ++i) {
         const uint32_t pos = min(n_part, i + 1 + Ly::NG) + i, vs = pos % Ly::STAGES;
-        const int buf = i % Ly::NB;
+        const int vi = turn.of(w, i), buf = vi % Ly::NB;
         // P first: then K_i and all before it have landed, one of which may
         // have had V_i's stage before it.  (A wait for a phase's parity passes
         // as well while the phase before it is still open, so whoever waits for
         // a stage must know that its last fill has landed.)
-        if (!mbar_wait_warp(bar(Ly::B_PFULL + buf), (i / Ly::NB) & 1, ab, err, 1007) ||
-            !mbar_wait_warp(bar(Ly::B_KVFULL + vs), (pos / Ly::STAGES) & 1, ab, err, 1005)) {
+        if (!mbar_wait_warp_call(bar(Ly::B_PFULL + buf), (vi / Ly::NB) & 1, ab, err, 1007) ||
+            !mbar_wait_warp_call(bar(Ly::B_KVFULL + vs), (pos / Ly::STAGES) & 1, ab, err, 1005)) {
           ok = false;
           break;
         }
+        // V rows of keys nobody sees (behind the length, before the window) are zero
+        // whatever the page holds there.  This warp waits for V anyway; when the
+        // softmax did it, V's arrival, up to two tiles after K's, held up its next tile.
+        const int k = w.k + x, key0 = (k < w.s.ns ? k : w.s.lo + k - w.s.ns) * 128;
+        const int z0[2] = {max(w.s.n - key0, 0), max(p.sinks - key0, 0)}, z1[2] = {128, min(w.s.wlo - key0, 128)};
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+          if (z0[z] < z1[z]) {
+            uint8_t* v = gbase + Ly::RING_OFF + vs * Ly::TILE;
+#pragma unroll 1
+            for (int u = z0[z] * 8 + static_cast<int>(lane); u < z1[z] * 8; u += 32)
+#pragma unroll
+              for (int c = 0; c < Ly::KCH; ++c) reinterpret_cast<uint4*>(v + c * Ly::CHUNK)[u] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
         tc_fence_after();
         const uint64_t vd = sdesc_sw128(base + Ly::RING_OFF + vs * Ly::TILE, Ly::CHUNK, 1024);
-        const uint64_t pd = sdesc_sw128(base + Ly::P_OFF + (i % Ly::PB) * Ly::PT, 16, 1024);
+        const uint64_t pd = sdesc_sw128(base + Ly::P_OFF + (vi % Ly::PB) * Ly::PT, 16, 1024);
         if (elect_one()) {
           // (a group's first tile of the item has no O to add to)
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_ss(tmem + Ly::TM_O + (ob * Ly::NG + i % Ly::NG) * N, vd + ((2048u * k) >> 4),
-                   pd + (((k >> 2) * Ly::QCH + (k & 3) * 32u) >> 4), IDESC_PV,
-                   (x >= Ly::NG || k > 0) ? 1u : 0u);
+            for (int k = 0; k < 4; ++k)
+              mma_ss(tmem + Ly::TM_O + (ob * Ly::NG + vi % Ly::NG) * N, vd + ((8192u * c + 2048u * k) >> 4),
+                     pd + ((c * Ly::QCH + k * 32u) >> 4), IDESC_PV,
+                     (x >= (turn.alone() ? 1 : Ly::NG) || c > 0 || k > 0) ? 1u : 0u);
           tc_commit(bar(Ly::B_PVDONE + buf));
           tc_commit(bar(Ly::B_KVEMPTY + vs));
           if (x + 1 == w.left) tc_commit(bar(Ly::B_OFULL + ob));
@@ -673,10 +712,13 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
     constexpr int NL = OWN_SUMS ? R : NCH;
     float m[NCH], l[NL];
     uint32_t joins = 0;
+    Turn turn{single};
+    int gi = 0;  // the group's exchanges: one a tile, and one at the end of an item of its own
     bool ok = true;
     PagedWalk w = paged_walk(p, plan, lens);
-    const int t0 = plan[4], total = plan[5], n_part = plan[3], G = gridDim.x;
+    const int t0 = plan[4], total = plan[5];
     int k_start = 0, in_item = 0;  // the item's first tile in this part; its tiles so far
+#pragma unroll 1
     for (int i = 0; ok && w.rem > 0; ++i, w.next(p)) {
       if (w.first) {
         k_start = w.k;
@@ -687,9 +729,10 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
         for (int r = 0; r < NL; ++r) l[r] = 0.f;
       }
       ++in_item;
-      if (i % Ly::NG == gr) {
-      const int buf = i % Ly::NB, pbuf = i % Ly::PB, gi = i / Ly::NG;  // gi: tiles of this group
-      if (!mbar_wait_warp(bar(Ly::B_SFULL + buf), (i / Ly::NB) & 1, ab, err, 1008)) { ok = false; break; }
+      const int vi = turn.of(w, i);
+      if (vi % Ly::NG == gr) {
+      const int buf = vi % Ly::NB, pbuf = vi % Ly::PB;
+      if (!mbar_wait_warp_call(bar(Ly::B_SFULL + buf), (vi / Ly::NB) & 1, ab, err, 1008)) { ok = false; break; }
       tc_fence_after();
       uint32_t sr[N];
       const uint32_t tS = tmem + lane_off + Ly::TM_S + buf * N;
@@ -735,7 +778,7 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(Ly::B_XMAX + gr));
-      if (!mbar_wait_warp(bar(Ly::B_XMAX + gr), gi & 1, ab, err, 1009)) { ok = false; break; }
+      if (!mbar_wait_warp_call(bar(Ly::B_XMAX + gr), gi & 1, ab, err, 1009)) { ok = false; break; }
       bool grow = false;
       float alpha[NCH];
 #pragma unroll
@@ -758,9 +801,9 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
       __syncwarp();
       // The group's four warps see the same maxima, so they agree here.
       if (__any_sync(0xffffffffu, grow)) {
-        // The group's O^T holds its earlier tiles of the item once PV(i-NG) is
+        // The group's O^T holds its earlier tiles of the item once its last PV is
         // done (the next phase of that barrier needs this warp's P first).
-        if (!mbar_wait_warp(bar(Ly::B_PVDONE + (i - Ly::NG) % Ly::NB), ((i - Ly::NG) / Ly::NB) & 1, ab, err, 1010)) {
+        if (!mbar_wait_warp_call(bar(Ly::B_PVDONE + (vi - Ly::NG) % Ly::NB), ((vi - Ly::NG) / Ly::NB) & 1, ab, err, 1010)) {
           ok = false;
           break;
         }
@@ -795,8 +838,8 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
       // operand); the row sums take the unrounded values.
       // (P's buffer: PV(i-NB) was done before S(i) was issued; with fewer P than
       // S buffers the later PV has to be waited for.)
-      if (Ly::PB < Ly::NB && i >= Ly::PB &&
-          !mbar_wait_warp(bar(Ly::B_PVDONE + (i - Ly::PB) % Ly::NB), ((i - Ly::PB) / Ly::NB) & 1, ab, err, 1016)) {
+      if (Ly::PB < Ly::NB && vi >= Ly::PB &&
+          !mbar_wait_warp_call(bar(Ly::B_PVDONE + (vi - Ly::PB) % Ly::NB), ((vi - Ly::PB) / Ly::NB) & 1, ab, err, 1016)) {
         ok = false;
         break;
       }
@@ -817,36 +860,11 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
           l[c] = l[c] * alpha[c] + paged_rows_reduce<CW, false>(x, lane);
         }
       }
-      if (!whole) {
-        // V rows of keys nobody sees: zero, whatever the page holds there.  The
-        // stage's last fill must have landed before its next one is waited for:
-        // it was a K up to K_i (S_i is here), or at the latest V_{i - STAGES/2},
-        // which PV_{i-NB}, done before S_i, does not cover when STAGES/2 < NB.
-        // (PV_{i-LAST+NB} needs this tile's P, so that barrier is at most one
-        // phase on.)
-        constexpr int LAST = Ly::STAGES / 2;
-        if (LAST < Ly::NB && i >= LAST &&
-            !mbar_wait_warp(bar(Ly::B_PVDONE + (i - LAST) % Ly::NB), ((i - LAST) / Ly::NB) & 1, ab, err, 1018)) {
-          ok = false;
-          break;
-        }
-        const uint32_t vpos = min(n_part, i + 1 + Ly::NG) + i;  // V's place in the ring's order
-        if (!mbar_wait_warp(bar(Ly::B_KVFULL + vpos % Ly::STAGES), (vpos / Ly::STAGES) & 1, ab, err, 1011)) {
-          ok = false;
-          break;
-        }
-        if (key >= w.s.n || (key < w.s.wlo && key >= p.sinks)) {
-          uint4* v = reinterpret_cast<uint4*>(gbase + Ly::RING_OFF + (vpos % Ly::STAGES) * Ly::TILE + t * 128);
-#pragma unroll
-          for (int c = 0; c < Ly::KCH; ++c)
-#pragma unroll
-            for (int u = 0; u < 8; ++u) v[c * (Ly::CHUNK / 16) + u] = make_uint4(0, 0, 0, 0);
-        }
-      }
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(Ly::B_PFULL + buf));  // (a group may be two tiles ahead of the MMA)
+      ++gi;
       }
 
       if (w.last()) {
@@ -855,6 +873,8 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
         // rest, so the other goes on with the next item.  (It comes back to
         // these areas two items later, after that item's exchange with this one.)
         const int ob = w.item & 1;
+        const bool alone = turn.alone();
+        if (alone && gr != ob) continue;
         float* sx = sum_x + ob * 4 * Ly::NG * N;
         float* mx = max_x + ob * Ly::NG * N;
 #pragma unroll
@@ -874,20 +894,29 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(Ly::B_XSUM + ob));
-        if (Ly::NG == 2 && gr != ob) continue;
-        if (!mbar_wait_warp(bar(Ly::B_XSUM + ob), (w.item >> 1) & 1, ab, err, 1012)) { ok = false; break; }
-        const bool direct = k_start == 0 && w.k + 1 == w.s.cnt;
-        const int slot = 2 * blockIdx.x + (w.item > 0 ? 1 : 0);
+        if (alone) {
+          if (lane == 0) mbar_arrive(bar(Ly::B_XMAX + gr));
+          if (!mbar_wait_warp_call(bar(Ly::B_XMAX + gr), gi & 1, ab, err, 1019)) { ok = false; break; }
+          ++gi;
+        } else {
+          if (lane == 0) mbar_arrive(bar(Ly::B_XSUM + ob));
+          if (Ly::NG == 2 && gr != ob) continue;
+          if (!mbar_wait_warp_call(bar(Ly::B_XSUM + ob), (w.item >> 1) & 1, ab, err, 1012)) { ok = false; break; }
+        }
+        const bool direct = !OWN && k_start == 0 && w.k + 1 == w.s.cnt;
+        const int slot = OWN ? w.b * p.Hkv + w.hkv + part_c : 2 * part_c + (w.item > 0 ? 1 : 0);
         // Factors of the groups' O^T rows: mbuf for group 0, al for group 1.
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
           const int rr = c * CW + row_l;
-          float top = mx[rr], f[Ly::NG], sum = 0.f;
-          if constexpr (Ly::NG == 2) top = fmaxf(top, mx[N + rr]);
+          float top = mx[(alone ? gr : 0) * N + rr], f[Ly::NG], sum = 0.f;
+          if constexpr (Ly::NG == 2)
+            if (!alone) top = fmaxf(top, mx[N + rr]);
 #pragma unroll
           for (int x = 0; x < Ly::NG; ++x) {
             const float* ls = sx + 4 * x * N + rr;
+            f[x] = 0.f;
+            if (alone && x != gr) continue;
             f[x] = mx[x * N + rr] == -INFINITY ? 0.f : ex2((mx[x * N + rr] - top) * sl2);
             sum += f[x] * ((ls[0] + ls[N]) + (ls[2 * N] + ls[3 * N]));
           }
@@ -907,13 +936,14 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
           }
         }
         __syncwarp();
-        if (!mbar_wait_warp(bar(Ly::B_OFULL + ob), (w.item >> 1) & 1, ab, err, 1013)) { ok = false; break; }
+        if (!mbar_wait_warp_call(bar(Ly::B_OFULL + ob), (w.item >> 1) & 1, ab, err, 1013)) { ok = false; break; }
         tc_fence_after();
         // A group that had no tile of the item left nothing in its O.
-        const bool has[2] = {in_item >= 2 || i % Ly::NG == 0, in_item >= 2 || i % Ly::NG == 1};
+        const bool has[2] = {alone ? gr == 0 : in_item >= 2 || i % Ly::NG == 0,
+                             alone ? gr == 1 : in_item >= 2 || i % Ly::NG == 1};
         if (t < D) {
           const uint32_t tO = tmem + lane_off + Ly::TM_O + ob * Ly::NG * N;
-          TO* dst = reinterpret_cast<TO*>(p.O) + (static_cast<size_t>(w.b) * p.Lq * p.H + w.hkv * p.g) * D + t;
+          T* dst = reinterpret_cast<T*>(p.O) + (static_cast<size_t>(w.b) * p.Lq * p.H + w.hkv * p.g) * D + t;
           float* part = p.part_o + static_cast<size_t>(slot) * p.rows * D + t;
           constexpr int OC = 16;
           int hh = 0;
@@ -932,7 +962,7 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
               v[r] = has[0] ? __uint_as_float(o[0][r]) * mbuf[rr] : 0.f;
               if constexpr (Ly::NG == 2) v[r] = has[1] ? fmaf(__uint_as_float(o[1][r]), al[rr], v[r]) : v[r];
             }
-            if (!direct) {
+            if (OWN || !direct) {
 #pragma unroll
               for (int r = 0; r < OC; ++r)
                 if (c * OC + r < R && c * OC + r < p.rows) part[(c * OC + r) * D] = v[r];
@@ -940,7 +970,7 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
 #pragma unroll
               for (int r = 0; r < OC; ++r)
                 if (c * OC + r < R && c * OC + r < p.rows) {
-                  dst[static_cast<size_t>(hh) * D] = static_cast<TO>(v[r]);
+                  dst[static_cast<size_t>(hh) * D] = static_cast<T>(v[r]);
                   if (++hh == p.g) {  // next query
                     hh = 0;
                     dst += static_cast<size_t>(p.H) * D;
@@ -952,7 +982,14 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(Ly::B_OEMPTY + ob));
-        if (!direct) {
+        if constexpr (OWN) {
+          // The item's first and last part, for the join.
+          if (t == 0) {
+            int* ends = p.ends + 2 * (static_cast<size_t>(w.b) * p.Hkv + w.hkv);
+            if (k_start == 0) ends[0] = part_c;
+            if (w.k + 1 == w.s.cnt) ends[1] = part_c;
+          }
+        } else if (!direct) {
           // ---- a partial: count it in; the CTA that comes last joins the item
           const int start = t0 + i - w.k;  // the item's first tile
           const int c0 = paged_part_of(total, G, start);
@@ -961,7 +998,7 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
           const unsigned long long word_was = t == 0 ? __ldcg(word) : 0ull;
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(Ly::B_JOIN + 2 * gr));
-          if (!mbar_wait_warp(bar(Ly::B_JOIN + 2 * gr), joins & 1, ab, err, 1014)) { ok = false; break; }
+          if (!mbar_wait_warp_call(bar(Ly::B_JOIN + 2 * gr), joins & 1, ab, err, 1014)) { ok = false; break; }
           int* flag = plan + 6 + gr;
           if (t == 0) {
             __threadfence();  // the group's partial, before the count
@@ -970,24 +1007,78 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
             *flag = last;
             mbar_arrive(bar(Ly::B_JOIN + 2 * gr + 1));
           }
-          if (!mbar_wait_warp(bar(Ly::B_JOIN + 2 * gr + 1), joins & 1, ab, err, 1015)) { ok = false; break; }
+          if (!mbar_wait_warp_call(bar(Ly::B_JOIN + 2 * gr + 1), joins & 1, ab, err, 1015)) { ok = false; break; }
           ++joins;
           if (*flag) {
             const int slot0 = 2 * c0 + (start > paged_part(total, G, c0) ? 1 : 0);
-            paged_join<D, TO, R>(p, w.b, w.hkv, slot0, 2 * (c0 + 1), c1 - c0 + 1);
+            paged_join<D, T, R>(p, w.b, w.hkv, slot0, 2 * (c0 + 1), c1 - c0 + 1);
           }
         }
       }
     }
     // Empty sequences: O = 0, LSE = -inf.
-    for (int b = blockIdx.x; gr == 0 && b < p.B; b += G) {
+#pragma unroll 1
+    for (int b = part_c; !OWN && gr == 0 && b < p.B; b += G) {
       if (p.lens[b] > 0) continue;
-      TO* dst = reinterpret_cast<TO*>(p.O) + static_cast<size_t>(b) * p.Lq * p.H * D;
-      for (int x = t; x < p.Lq * p.H * D; x += 128) dst[x] = static_cast<TO>(0.f);
+      T* dst = reinterpret_cast<T*>(p.O) + static_cast<size_t>(b) * p.Lq * p.H * D;
+#pragma unroll 1
+      for (int x = t; x < p.Lq * p.H * D; x += 128) dst[x] = static_cast<T>(0.f);
+#pragma unroll 1
       for (int x = t; x < p.Lq * p.H; x += 128)
         p.LSE[static_cast<size_t>(b) * p.Lq * p.H + x] = -INFINITY;
     }
   }
+}
+
+template <int D, bool BF16, int R>
+__global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
+    fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ,
+                           const __grid_constant__ CUtensorMap tmK,
+                           const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
+  using Ly = PagedLayout<D, R>;
+
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  auto bar = [&](int i) -> uint32_t { return base + Ly::BAR_OFF + 8u * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + Ly::MISC_OFF);
+  AbortState* ab = reinterpret_cast<AbortState*>(gbase + Ly::MISC_OFF + 8);
+  int* plan = reinterpret_cast<int*>(gbase + Ly::MISC_OFF + 16);
+  int* sums = reinterpret_cast<int*>(gbase + Ly::MISC_OFF + 48);      // NTHREADS / 32
+  int* lens_s = reinterpret_cast<int*>(gbase + Ly::MISC_OFF + 128);   // 32
+  const int* lens = p.B <= 32 ? lens_s : p.lens;
+  const uint32_t warp = warp_id(), lane = lane_id();
+
+  // Query rows past g * Lq, and P rows no thread writes, are zero.
+#pragma unroll 1
+  for (uint32_t i = threadIdx.x; i < (Ly::QS * Ly::QT + Ly::PB * Ly::PT) / 16u; i += Ly::NTHREADS)
+    reinterpret_cast<uint4*>(gbase + Ly::Q_OFF)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+#pragma unroll 1
+  for (int i = threadIdx.x; i < Ly::NBAR; i += Ly::NTHREADS) mbar_init(bar(i), Ly::arrivals(i));
+  if (threadIdx.x == 0) ab->flag = 0;
+  fence_barrier_init();
+  if (warp == Ly::SW + 1) {
+    tmem_alloc(base + Ly::MISC_OFF, Ly::TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (warp == Ly::SW && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  tc_fence_before();
+  // Everything above overlaps the end of the kernel before; nothing of global
+  // memory was touched.
+  pdl_launch_dependents();
+  pdl_wait();
+  const int len = (p.B <= 32 && static_cast<int>(lane) < p.B) ? p.lens[lane] : 0;
+  if (warp == 0) lens_s[lane] = len;
+  paged_plan<Ly::NTHREADS>(p, blockIdx.x, gridDim.x, len, sums, plan);
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  paged_body<D, BF16, R>(tmQ, tmK, tmV, p, gbase, base, tmem, ab, plan, lens, blockIdx.x, gridDim.x, false);
 
   tc_fence_before();
   __syncthreads();
@@ -996,7 +1087,6 @@ __global__ void __launch_bounds__(PagedLayout<D, R>::NTHREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, Ly::TMEM_COLS);
   }
-  if constexpr (OWN) pdl_wait();
 }
 
 // Add every visible key's attention weight, sum over the item's rows of
@@ -1048,6 +1138,7 @@ static __global__ void __launch_bounds__(256)
   pdl_launch_dependents();
   const int per = Hkv * units;  // 16-byte units of a token (units = D / 8 per head)
   const long long all = static_cast<long long>(B) * L * per;
+#pragma unroll 1
   for (long long i = blockIdx.x * 256ll + threadIdx.x; i < all; i += gridDim.x * 256ll) {
     const long long tok = i / per;
     const int u = static_cast<int>(i - tok * per);

@@ -3,7 +3,6 @@
 
 #include "common.cuh"
 #include "internal.h"
-#include "paged_launch.cuh"  // make_pool_map
 #include "prefix.cuh"
 
 namespace fa {
@@ -13,11 +12,11 @@ namespace {
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct PrefixPlan {
-  int mt;            // tiles of an item
-  int tok;           // tokens of a tile
-  long long items, units;  // at most
-  int G;             // CTAs
-  size_t own, own_o, own_lse, base, part_o, part_lse, bytes;
+  int tok, rows;          // tokens of a prefix's tile, rows of a sequence's
+  long long items, own;   // at most: items of prefixes, of sequences
+  long long most;         // at most: the weight of all items' units
+  int G;                  // CTAs
+  size_t part_o, part_lse, own_o, own_lse, ends, bytes;
 };
 
 PrefixPlan prefix_plan_of(const PrefixDecodeArgs& a) {
@@ -26,31 +25,45 @@ PrefixPlan prefix_plan_of(const PrefixDecodeArgs& a) {
   int sms = sm_count();
   if (sms < 1) sms = 1;
   w.tok = 128 / g;
+  w.rows = g * a.Lq;
   const long long tokens = static_cast<long long>(a.B) * a.Lq;
-  // Groups of one tile (in the mean) have a CTA's two softmax groups share it.
-  w.mt = tokens <= static_cast<long long>(w.tok) * a.groups ? 1 : 2;
-  const long long per = static_cast<long long>(w.tok) * w.mt;
-  const long long cap = static_cast<long long>(a.prefix_pages) * a.page;
-  w.items = a.Hkv * (tokens / per + a.groups);
-  w.units = w.items * ((cap + 127) / 128);
-  w.G = w.units < sms ? static_cast<int>(w.units) : sms;
-  const size_t rows = static_cast<size_t>(tokens) * a.H, chunks = static_cast<size_t>(w.items + w.G) * w.mt;
+  w.items = a.Hkv * (tokens / (2 * w.tok) + a.groups);
+  w.own = static_cast<long long>(a.B) * a.Hkv;
+  const long long prefix_units = w.items * ((static_cast<long long>(a.prefix_pages) * a.page + 127) / 128);
+  const long long own_units = w.own * ((static_cast<long long>(a.max_pages) * a.page + 127) / 128);
+  w.most = prefix_units * kPairWeight + own_units * kOneWeight;
+  // (two at least: prefixes and own keys may have CTAs of their own)
+  w.G = prefix_units + own_units < sms ? static_cast<int>(prefix_units + own_units) : sms;
+  if (w.G < 2) w.G = 2;
   size_t at = 0;
-  w.own = at;
-  at += align256(paged_decode_workspace_size(a.B, a.Lq, static_cast<long long>(a.max_pages) * a.page, a.H, a.Hkv,
-                                             a.D, false));
-  w.own_o = at;
-  at += align256(rows * a.D * sizeof(float));
-  w.own_lse = at;
-  at += align256(rows * sizeof(float));
-  w.base = at;
-  at += align256((2 * static_cast<size_t>(a.groups) + 1) * sizeof(int));
   w.part_o = at;
-  at += chunks * 128 * a.D * sizeof(float);
+  at += static_cast<size_t>(w.items + w.G) * 256 * a.D * sizeof(float);
   w.part_lse = at;
-  at += chunks * 128 * sizeof(float);
+  at += static_cast<size_t>(w.items + w.G) * 256 * sizeof(float);
+  w.own_o = at;
+  at += align256(static_cast<size_t>(w.own + w.G) * w.rows * a.D * sizeof(float));
+  w.own_lse = at;
+  at += align256(static_cast<size_t>(w.own + w.G) * w.rows * sizeof(float));
+  w.ends = at;
+  at += static_cast<size_t>(w.items + w.own) * 2 * sizeof(int);
   w.bytes = at;
   return w;
+}
+
+// K or V pool [pages, page, Hkv, D] with a free page stride, loaded as boxes of
+// 64 head-dim elements x min(page, 128) rows of one page and head.
+bool make_pool_map(CUtensorMap* map, const void* ptr, int pages, int page, int Hkv, int D, long long page_stride,
+                   bool bf16) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)page, (cuuint64_t)pages};
+  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)Hkv * D * 2, (cuuint64_t)page_stride * 2};
+  cuuint32_t box[4] = {64, 1, (cuuint32_t)(page < 128 ? page : 128), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+            const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Q as [B * Lq, H, D], loaded as boxes of 64 head-dim elements x g heads x the
@@ -68,87 +81,82 @@ bool make_rows_map(CUtensorMap* map, const void* Q, long long tokens, int H, int
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool BF16, int MT>
-fa_status launch_prefix(const PrefixDecodeArgs& a, const PrefixPlan& w, cudaStream_t s) {
-  using Ly = PrefixLayout<D, MT>;
+template <int D, bool BF16, int R>
+fa_status launch_prefix(const PrefixDecodeArgs& a, const PrefixPlan& w, PrefixJoinParams& j, cudaStream_t s) {
+  using Sh = PrefixShared<D, R>;
+  PrefixParams& p = j.p;
+  p.entries = R == 0 ? a.groups + a.B : a.groups;
+  PagedOwnParams o = {};
+  o.table = a.table;
+  o.lens = a.lens;
+  o.part_o = p.own_o;
+  o.part_lse = p.own_lse;
+  o.ends = p.ends + 2 * w.items;
+  o.B = a.B;
+  o.Lq = a.Lq;
+  o.H = a.H;
+  o.Hkv = a.Hkv;
+  o.g = p.g;
+  o.rows = p.rows;
+  o.ginv = p.ginv;
+  o.page = a.page;
+  o.max_pages = a.max_pages;
+  o.cap = p.cap;
+  o.max_tiles = (p.cap + 127) / 128;
+  o.sl2 = p.sl2;
+  CUtensorMap tq, to, tk, tv;
+  if (!make_rows_map(&tq, a.Q, static_cast<long long>(a.B) * a.Lq, a.H, p.g, p.tok, D, BF16) ||
+      !make_group_map(&to, a.Q, a.B, a.Lq, a.H, p.g, D, BF16) ||
+      !make_pool_map(&tk, a.K, a.num_pages, a.page, a.Hkv, D, a.k_page_stride, BF16) ||
+      !make_pool_map(&tv, a.V, a.num_pages, a.page, a.Hkv, D, a.v_page_stride, BF16))
+    return FA_ERR_CUDA;
+  auto kern = fa_prefix_kernel<D, BF16, R>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::ALLOC) != cudaSuccess)
+    return FA_ERR_CUDA;
+  if (!launch_after_smem(kern, dim3(w.G), dim3(Sh::NTHREADS), Sh::ALLOC, s, tq, to, tk, tv, p, o)) return FA_ERR_CUDA;
+  const dim3 grid(static_cast<unsigned>(a.B) * a.Lq * a.Hkv, (p.g * (D / 4) + 31) / 32);
+  return launch_after(fa_prefix_join_kernel<D, BF16>, grid, dim3(128), s, j) ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int D, bool BF16>
+fa_status pick_rows(const PrefixDecodeArgs& a, const PrefixPlan& w, cudaStream_t s) {
   char* ws = static_cast<char*>(a.workspace);
   PrefixJoinParams j;
   PrefixParams& p = j.p;
-  p.table = a.prefix_table;
-  p.lens = a.prefix_lens;
+  p.ptable = a.prefix_table;
+  p.plens = a.prefix_lens;
   p.starts = a.group_starts;
+  p.table = a.table;
+  p.lens = a.lens;
   p.part_o = reinterpret_cast<float*>(ws + w.part_o);
   p.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
-  p.base = reinterpret_cast<int*>(ws + w.base);
+  p.own_o = reinterpret_cast<float*>(ws + w.own_o);
+  p.own_lse = reinterpret_cast<float*>(ws + w.own_lse);
+  p.ends = reinterpret_cast<int*>(ws + w.ends);
+  p.most = static_cast<uint32_t>(w.most);
   p.B = a.B;
   p.Lq = a.Lq;
   p.H = a.H;
   p.Hkv = a.Hkv;
   p.g = a.H / a.Hkv;
   p.groups = a.groups;
+  p.rows = w.rows;
   p.tok = w.tok;
-  p.max_items = static_cast<int>(w.items);
+  p.items = static_cast<int>(w.items);
   p.ginv = 65536 / p.g + 1;
   p.page = a.page;
-  p.max_pages = a.prefix_pages;
-  p.cap = a.prefix_pages * a.page;
+  p.prefix_pages = a.prefix_pages;
+  p.max_pages = a.max_pages;
+  p.pcap = a.prefix_pages * a.page;
+  p.cap = a.max_pages * a.page;
   p.sl2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
-  CUtensorMap tq, tk, tv;
-  if (!make_rows_map(&tq, a.Q, static_cast<long long>(a.B) * a.Lq, a.H, p.g, p.tok, D, BF16) ||
-      !make_pool_map(&tk, a.K, a.num_pages, a.page, a.Hkv, D, a.k_page_stride, BF16) ||
-      !make_pool_map(&tv, a.V, a.num_pages, a.page, a.Hkv, D, a.v_page_stride, BF16))
-    return FA_ERR_CUDA;
-  auto kern = fa_prefix_kernel<D, BF16, MT>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::SMEM_ALLOC) != cudaSuccess)
-    return FA_ERR_CUDA;
-  if (!launch_after_smem(kern, dim3(w.G), dim3(Ly::NTHREADS), Ly::SMEM_ALLOC, s, tq, tk, tv, p))
-    return FA_ERR_CUDA;
-  // The sequences' own keys, in fp32.
-  PagedDecodeArgs o;
-  o.Q = a.Q;
-  o.K = a.K;
-  o.V = a.V;
-  o.table = a.table;
-  o.lens = a.lens;
-  o.O = ws + w.own_o;
-  o.LSE = reinterpret_cast<float*>(ws + w.own_lse);
-  o.weights = nullptr;
-  o.weights_stride = 0;
-  o.k_page_stride = a.k_page_stride;
-  o.v_page_stride = a.v_page_stride;
-  o.workspace = ws + w.own;
-  o.workspace_bytes = w.own_o - w.own;
-  o.B = a.B;
-  o.Lq = a.Lq;
-  o.H = a.H;
-  o.Hkv = a.Hkv;
-  o.D = a.D;
-  o.page = a.page;
-  o.max_pages = a.max_pages;
-  o.num_pages = a.num_pages;
-  o.window = 0;
-  o.sinks = 0;
-  o.dtype = a.dtype;
-  const fa_status st = run_paged_own(o, s);
-  if (st != FA_OK) return st;
-  j.own_lens = a.lens;
-  j.own_o = static_cast<const float*>(o.O);
-  j.own_lse = o.LSE;
   j.O = a.O;
   j.LSE = a.LSE;
-  j.own_cap = a.max_pages * a.page;
   j.G = w.G;
-  const int per = p.g * (D / 8), ppb = per <= 256 ? 256 / per : 1;
-  const long long pairs = static_cast<long long>(a.B) * a.Lq * a.Hkv;
-  return launch_after(fa_prefix_join_kernel<D, BF16, MT>, dim3(static_cast<unsigned>((pairs + ppb - 1) / ppb)),
-                      dim3(256), s, j)
-             ? FA_OK
-             : FA_ERR_CUDA;
-}
-
-template <int D, bool BF16>
-fa_status pick_tiles(const PrefixDecodeArgs& a, const PrefixPlan& w, cudaStream_t s) {
-  return w.mt == 1 ? launch_prefix<D, BF16, 1>(a, w, s) : launch_prefix<D, BF16, 2>(a, w, s);
+  if (w.rows <= 8) return launch_prefix<D, BF16, 8>(a, w, j, s);
+  if (w.rows <= 16) return launch_prefix<D, BF16, 16>(a, w, j, s);
+  if (w.rows <= 32) return launch_prefix<D, BF16, 32>(a, w, j, s);
+  return launch_prefix<D, BF16, 0>(a, w, j, s);
 }
 
 }  // namespace
@@ -157,13 +165,11 @@ size_t paged_prefix_workspace_size(const PrefixDecodeArgs& a) { return prefix_pl
 
 fa_status run_paged_prefix(const PrefixDecodeArgs& a, cudaStream_t s) {
   const PrefixPlan w = prefix_plan_of(a);
-  if (w.units >= (1ll << 31) || w.items >= (1ll << 30)) return FA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(a.B) * a.Hkv * ((static_cast<long long>(a.max_pages) * a.page + 127) / 128) >= (1ll << 31))
-    return FA_ERR_UNSUPPORTED;
+  if (w.most >= (1ll << 32) || w.items + w.own >= (1ll << 29)) return FA_ERR_UNSUPPORTED;
   if (a.workspace_bytes < w.bytes) return FA_ERR_SCRATCH_TOO_SMALL;
   const bool bf16 = a.dtype == FA_BF16;
-  if (a.D == 64) return bf16 ? pick_tiles<64, true>(a, w, s) : pick_tiles<64, false>(a, w, s);
-  return bf16 ? pick_tiles<128, true>(a, w, s) : pick_tiles<128, false>(a, w, s);
+  if (a.D == 64) return bf16 ? pick_rows<64, true>(a, w, s) : pick_rows<64, false>(a, w, s);
+  return bf16 ? pick_rows<128, true>(a, w, s) : pick_rows<128, false>(a, w, s);
 }
 
 unsigned int prefix_read_error(cudaStream_t s) { return read_and_clear_error(s); }

@@ -1,35 +1,39 @@
 // Attention of a batch's new tokens over key/value prefixes that several of its
-// sequences share, and the join with their attention over their own keys.
+// sequences share and over each sequence's own keys, both in a paged cache.
 //
-// Mathematics: softmax over the union of two sets of keys from the softmaxes of
-// both: LSE = ln sum_s exp(LSE_s), O = sum_s exp(LSE_s - LSE) O_s.  Every new
+// Mathematics: softmax over the union of sets of keys from the softmaxes of
+// each: LSE = ln sum_s exp(LSE_s), O = sum_s exp(LSE_s - LSE) O_s.  Every new
 // token behind a prefix sees all of it, so the prefix's part is one product
 // chain of all rows (tokens x query heads of a K/V head) with the prefix's keys
 // and values, which are read once, not once per sequence.
 //
-// Three launches.  fa_prefix_kernel: the prefixes' part, cut into partials.  The
-// paged decode kernel (its OWN form) over the sequences' own keys: it may start
-// as soon as SMs are free of the first.  fa_prefix_join_kernel: each row's
-// partials of both.
+// Two launches: fa_prefix_kernel cuts both parts into chunks and leaves each
+// chunk's partial O and LSE in fp32; fa_prefix_join_kernel joins each row's.
 //
-// fa_prefix_kernel.  A tile is up to 128 rows: 128 / g tokens (g query heads a
-// K/V head) of one group, row = token * g + head.  An item is one K/V head of a
-// group and MT tiles (2, or 1 where a group has few rows); its units are the
-// prefix's 128-key tiles.  The units of all items form one list and each CTA
-// takes one of G equal contiguous parts of it, so all SMs work whatever the
-// lengths and groups are.  A part's share of an item (a chunk) gives one
-// normalised fp32 partial and its LSE.  Chunks number item + part, which no two
-// share: the next chunk in the list is of the next item, the next part, or both.
-//   warps 0-3, 4-7  softmax, a thread per row.  MT = 2: of tile 0 and tile 1.
-//                   MT = 1: of the one tile's even and odd steps, each with a
-//                   maximum, a sum and an O of its own, joined at the end.
-//   warp 8          TMA: Q, then K_0, V_0, K_1, V_1, ... through one ring across
+// fa_prefix_kernel, a persistent CTA per SM.  A tile is up to 128 rows.  Of a
+// prefix: 128 / g tokens of the group (g query heads a K/V head), row = token * g
+// + head; an item is one K/V head of a group and two neighbouring tiles (the last
+// may have one).  Of own keys: an item is one sequence and K/V head, a tile of
+// Lq * g rows.  An item's units are its 128-key tiles.  The units of all items,
+// groups first, form one list, in which a unit weighs about what it takes, and
+// each CTA takes one of G equal parts of it, so all SMs work whatever the
+// lengths and groups are, and while some are bound by the products of the
+// prefixes others read own keys.  A part's share of an item is a chunk.  Chunks
+// are stored at item + part, which no two share: the next chunk in the list is of
+// a later item, a later part, or both.
+//   warps 0-3, 4-7  softmax, a thread per row.  Two tiles: one each.  One tile:
+//                   its even and its odd steps, each group with a maximum, a sum
+//                   and an O of its own; warps 4-7 join them at the chunk's end
+//                   while warps 0-3 begin the next.  Warps without a row wait.
+//   warp 10         TMA: Q, then K_0, V_0, K_1, V_1, ... through one ring across
 //                   chunks; lane i loads the i-th page of a tile
 //   warp 9          TMEM, MMAs: S_t = Q_t K_j^T, P over S as 16 bits, O_t += P V_j
-// Per 64 KB of K and V (D = 128) a CTA with 256 rows needs the tensor cores for
-// 2,150 cycles and the exponentials for 2,050; its share of the memory bandwidth
-// takes 2,790.  So up to 256 rows the read of the prefix bounds the kernel,
-// above it the products do and the other row tiles' reads hit the L2.
+// Per 64 KB of K and V (D = 128) two tiles take 2,930 cycles of products and
+// exponentials that overlap; a CTA's share of the memory bandwidth brings 64 KB in
+// 2,790.  So up to 256 rows the read of the prefix bounds the kernel about as much
+// as the products, above it the products do and the other tiles' reads hit the L2.
+// Own keys are bound by their read: their tiles' empty rows cost the tensor cores
+// 1,024 cycles a unit, which the read hides.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -37,445 +41,536 @@
 
 #include "common.cuh"
 #include "fwd.cuh"  // pack2
+#include "paged.cuh"
 #include "ptx.cuh"
 
 namespace fa {
 
 struct PrefixParams {
-  const int* table;   // [groups, max_pages]
-  const int* lens;    // [groups]
-  const int* starts;  // [groups + 1] first sequence of each group, or NULL: one group of all
-  float* part_o;      // [chunks][MT][D / 4][128][4]: a warp's rows lie together
-  float* part_lse;    // [chunks][MT][128], log2 units
-  int* base;          // [2 groups + 1] first unit and first item of each group; all units
-  int B, Lq, H, Hkv, g, groups;
-  int tok;            // tokens of a tile: 128 / g
-  int max_items;      // the workspace's
-  int ginv;           // 65536 / g + 1: row / g = row * ginv >> 16
-  int page, max_pages, cap;  // cap = max_pages * page
-  float sl2;          // log2(e) / sqrt(D)
+  const int *ptable, *plens;  // [groups, prefix_pages], [groups]
+  const int* starts;          // [groups + 1] first sequence of each group, or NULL: one group of all
+  const int *table, *lens;    // [B, max_pages], [B]: own keys
+  float* part_o;              // [prefix items + G][2][D / 4][128][4]: a warp's rows lie together
+  float* part_lse;            // [prefix items + G][2][128], log2 units
+  float* own_o;               // [B * Hkv + G][rows][D]
+  float* own_lse;             // [B * Hkv + G][rows], log2 units
+  int* ends;                  // [prefix items][2], then [B * Hkv][2]: an item's first and last part
+  uint32_t most;              // the list's weight can be no more (all sums fit 32 bits)
+  int B, Lq, H, Hkv, g, groups, rows;  // rows = g * Lq
+  int tok;                    // tokens of a prefix's tile: 128 / g
+  int items;                  // prefix items there may be
+  int entries;                // of the list: groups, or groups + B
+  int ginv;                   // 65536 / g + 1: row / g = row * ginv >> 16
+  int page, prefix_pages, max_pages, pcap, cap;  // caps: pages * page
+  float sl2;                  // log2(e) / sqrt(D)
 };
 
-// One group: its tokens [t0, t1) of the batch's B * Lq, its items per K/V head
-// and its units per item.
-struct PrefixGroup {
-  int n;  // prefix length
-  int t0, t1, items, cnt;
-};
-
-template <int MT>
-__device__ __forceinline__ PrefixGroup prefix_group(const PrefixParams& p, int i) {
-  PrefixGroup s;
-  int b0 = 0, b1 = p.B;
-  if (p.starts != nullptr) {
-    b0 = min(max(p.starts[i], 0), p.B);
-    b1 = min(max(p.starts[i + 1], b0), p.B);
+// mbar_wait_warp that reads the timer only once 32 polls have failed: most waits
+// here are short, and the read takes longer than they do.
+__device__ __forceinline__ bool prefix_wait(uint32_t bar, uint32_t parity, AbortState* ab, unsigned int* err,
+                                            unsigned int site) {
+  bool ok = false;
+  unsigned long long t0 = 0;
+#pragma unroll 1
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) {
+      ok = true;
+      break;
+    }
+    if ((it & 31u) == 0u) {
+      if (*reinterpret_cast<volatile int*>(&ab->flag)) break;
+      const unsigned long long now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitTimeoutNs) {
+        *reinterpret_cast<volatile int*>(&ab->flag) = 1;
+        atomicCAS(err, 0u, site);
+        break;
+      }
+    }
   }
-  s.n = min(max(p.lens[i], 0), p.cap);
-  s.t0 = b0 * p.Lq;
-  s.t1 = b1 * p.Lq;
-  s.cnt = (s.n + 127) >> 7;
-  s.items = s.cnt > 0 ? (s.t1 - s.t0 + MT * p.tok - 1) / (MT * p.tok) : 0;
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Arrive n times.
+__device__ __forceinline__ void prefix_arrive(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+
+// What a unit weighs: of two tiles, of one.  (Two tiles are bound by the products,
+// one by the read, which gets more than its share while others compute.)
+constexpr int kPairWeight = 3, kOneWeight = 2;
+// Own keys that have CTAs of their own: a tile and an item in the same measure.
+constexpr float kOwnTileWeight = 1.5f, kOwnItemWeight = 1.5f;
+// Items of at most so many tiles in the mean are short.
+constexpr uint32_t kShortItem = 5;
+
+// An entry of the list: group e, or the own keys of sequence e - groups.
+struct PrefixEntry {
+  int n;       // keys
+  int cnt;     // units of an item
+  int t0, t1;  // the group's tokens among the batch's B * Lq
+  int items;   // per K/V head
+  int weight;  // of a unit
+};
+
+__device__ __forceinline__ PrefixEntry prefix_entry(const PrefixParams& p, int e) {
+  PrefixEntry s;
+  if (e < p.groups) {
+    int b0 = 0, b1 = p.B;
+    if (p.starts != nullptr) {
+      b0 = min(max(p.starts[e], 0), p.B);
+      b1 = min(max(p.starts[e + 1], b0), p.B);
+    }
+    s.n = min(max(p.plens[e], 0), p.pcap);
+    s.t0 = b0 * p.Lq;
+    s.t1 = b1 * p.Lq;
+    s.cnt = (s.n + 127) >> 7;
+    s.items = s.cnt > 0 ? (s.t1 - s.t0 + 2 * p.tok - 1) / (2 * p.tok) : 0;
+    s.weight = s.t1 - s.t0 > p.tok ? kPairWeight : kOneWeight;
+  } else {
+    s.n = min(max(p.lens[e - p.groups], 0), p.cap);
+    s.t0 = s.t1 = 0;
+    s.cnt = (s.n + 127) >> 7;
+    s.items = s.cnt > 0 ? 1 : 0;
+    s.weight = kOneWeight;
+  }
   return s;
 }
 
-// Part c of G of `total` units begins at unit:
-__device__ __forceinline__ int prefix_part(int total, int G, int c) {
-  const int q = total / G, r = total - q * G;
-  return c * q + (c < r ? c : r);
-}
-// The part that holds unit t.
-__device__ __forceinline__ int prefix_part_of(int total, int G, int t) {
-  const int q = total / G, r = total - q * G, big = r * (q + 1);
-  return t < big ? t / (q + 1) : r + (t - big) / q;
+// A group's first item's number: groups' numbers lie apart whatever their sizes
+// (a group of n tokens has at most n / (2 tok) + 1 items a K/V head).
+__device__ __forceinline__ int prefix_first_item(const PrefixParams& p, const PrefixEntry& s, int grp) {
+  return (s.t0 / (2 * p.tok) + grp) * p.Hkv;
 }
 
-// Walk over the chunks of one part.
-template <int MT>
+// Walk over the chunks of one part.  OWN: own keys are in the list too.
+template <bool OWN>
 struct PrefixWalk {
-  int grp, hkv, it, k;  // group, K/V head, item of it, first unit of the chunk
-  int left;             // units of the chunk
-  int rem;              // units left in the part, the chunk's included
-  int chunk;            // its number
-  int done;             // chunks before it in the part
-  PrefixGroup s;
+  int e, hkv, it, k;  // entry, K/V head, item of it, first unit of the chunk
+  int left;           // units of the chunk; 0: the part is done
+  int rem;            // weight left in the part, the chunk's included
+  PrefixEntry s;
 
+  __device__ __forceinline__ int share() const {
+    return s.weight == kPairWeight ? rem / kPairWeight : rem / kOneWeight;
+  }
   __device__ __forceinline__ void next(const PrefixParams& p) {
-    rem -= left;
-    if (rem <= 0) return;
+    const bool ended = k + left < s.cnt;  // inside an item: the part's border
+    rem -= left * s.weight;
+    left = 0;
     k = 0;
-    ++chunk;
-    ++done;
+    if (ended) return;
     if (++it == s.items) {
       it = 0;
       if (++hkv == p.Hkv) {
         hkv = 0;
+#pragma unroll 1
         do {
-          if (++grp >= p.groups) {
-            rem = 0;
-            return;
-          }
-          s = prefix_group<MT>(p, grp);
+          if (++e >= p.entries || rem < kOneWeight) return;
+          s = prefix_entry(p, e);
         } while (s.items == 0);
       }
     }
-    left = min(s.cnt, rem);
+    left = min(s.cnt, share());
   }
+  __device__ __forceinline__ bool own(const PrefixParams& p) const { return OWN && e >= p.groups; }
   // First token of tile t of the item.
-  __device__ __forceinline__ int token(const PrefixParams& p, int t) const { return s.t0 + (it * MT + t) * p.tok; }
+  __device__ __forceinline__ int token(const PrefixParams& p, int t) const { return s.t0 + (2 * it + t) * p.tok; }
+  __device__ __forceinline__ bool pair(const PrefixParams& p) const { return !own(p) && token(p, 1) < s.t1; }
+  // Rows of tile t.
+  __device__ __forceinline__ int rows(const PrefixParams& p, int t) const {
+    return own(p) ? p.rows : min(p.tok, s.t1 - token(p, t)) * p.g;
+  }
 };
 
-template <int D, int MT>
+template <int D>
 struct PrefixLayout {
   static constexpr int KCH = D / 64;
   static constexpr uint32_t CHUNK = 128u * 128u;  // 128 rows x 64 columns
   static constexpr uint32_t TILE = KCH * CHUNK;
   static constexpr int STAGES = D == 128 ? 5 : 10;
-  static constexpr uint32_t Q_OFF = 0;
-  static constexpr uint32_t RING_OFF = MT * TILE;
-  static constexpr uint32_t BAR_OFF = RING_OFF + STAGES * TILE;
-  static constexpr int B_QFULL = 0, B_QEMPTY = 1, B_KVFULL = 2, B_KVEMPTY = B_KVFULL + STAGES,
+  static constexpr uint32_t Q_OFF = 0;            // two tiles
+  static constexpr uint32_t RING_OFF = 2 * TILE;
+  static constexpr uint32_t MATE_OFF = RING_OFF + STAGES * TILE;  // m, l [128]
+  static constexpr uint32_t BAR_OFF = MATE_OFF + 1024;
+  static constexpr int B_QFULL = 0, B_QEMPTY = 2, B_KVFULL = 4, B_KVEMPTY = B_KVFULL + STAGES,
                        B_SFULL = B_KVEMPTY + STAGES, B_PFULL = B_SFULL + 2, B_OFULL = B_PFULL + 4,
-                       B_OEMPTY = B_OFULL + 2, B_MATE = B_OEMPTY + 2, B_DONE = B_MATE + 1, NBAR = B_DONE + 1;
-  static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;  // tmem slot, abort flag, plan, sums
-  static constexpr uint32_t MATE_OFF = (MISC_OFF + 192 + 15) / 16 * 16;  // MT = 1: [2 chunks][2 groups][m, l][128]
-  static constexpr uint32_t SMEM_USED = MATE_OFF + (MT == 1 ? 4096 : 0);
-  static constexpr uint32_t SMEM_ALLOC = SMEM_USED + 1024;
-  static constexpr uint32_t TM_S = 0, TM_O = 256, TMEM_COLS = 512;
-  static constexpr int NTHREADS = 320;
-  static_assert(SMEM_ALLOC <= 232448, "shared memory");
+                       B_OEMPTY = B_OFULL + 2, B_MFULL = B_OEMPTY + 2, B_MEMPTY = B_MFULL + 1, B_DONE = B_MEMPTY + 1,
+                       NBAR = B_DONE + 1;
+  static constexpr uint32_t USED = BAR_OFF + NBAR * 8;
+  static constexpr uint32_t TM_S = 0, TM_O = 256;
+  // arrivals a barrier takes a phase
+  __device__ static constexpr int arrivals(int i) {
+    return (i >= B_PFULL && i < B_OFULL) || (i >= B_OEMPTY && i < B_DONE) ? 4 : 1;
+  }
 };
 
-// This CTA's part: the walk's start in plan {grp, hkv, it, k, n, first chunk}.
-// Called by the whole CTA; CTA 0 leaves the groups' bases for the join.
-template <int MT, int NT>
-__device__ __forceinline__ void prefix_plan(const PrefixParams& p, long long* sums, int* plan) {
-  const int lane = lane_id(), G = gridDim.x, c = blockIdx.x;
-  const int per = (p.groups + NT - 1) / NT;
-  const int i0 = min(p.groups, static_cast<int>(threadIdx.x) * per), i1 = min(p.groups, i0 + per);
-  // (64 bits: starts that fall make groups overlap, and any sum possible)
-  long long units = 0, items = 0;
-  for (int i = i0; i < i1; ++i) {
-    const PrefixGroup s = prefix_group<MT>(p, i);
-    units += static_cast<long long>(s.items) * s.cnt * p.Hkv;
-    items += static_cast<long long>(s.items) * p.Hkv;
+// What a CTA does: part c of the prefixes' list, or part c of G of the own keys'.
+struct PrefixShare {
+  bool own;
+  int c, G;
+};
+
+// How the CTAs are shared out, and this one's part.  Called by the whole CTA (NT
+// threads).  A CTA of the prefixes' list finds the start of its walk in plan
+// {e, hkv, it, k, rem}.  OWN: own keys are not in the list and have CTAs of their
+// own; plan[5] says whether their items are short.
+template <int NT, bool OWN>
+__device__ __forceinline__ PrefixShare prefix_plan(const PrefixParams& p, uint32_t* sums, int* plan) {
+  const int lane = lane_id(), all = p.groups + p.B, per = (all + NT - 1) / NT;
+  const int e0 = min(all, static_cast<int>(threadIdx.x) * per), e1 = min(all, e0 + per);
+  uint32_t mine = 0;                // weight of the list
+  uint32_t units = 0, items = 0;    // of own keys (OWN)
+  int pairs = 0;
+  PrefixEntry s = {};
+#pragma unroll 1
+  for (int e = e0; e < e1; ++e) {
+    s = prefix_entry(p, e);
+    const uint32_t n = static_cast<uint32_t>(s.items) * p.Hkv;
+    if (OWN && e >= p.groups) {
+      units += n * s.cnt;
+      items += n;
+    } else {
+      pairs |= s.items > 0 && s.weight == kPairWeight;
+      mine += n * s.cnt * s.weight;
+    }
   }
-  long long iu = units, ii = items;
-#pragma unroll
+  uint32_t incl = mine;
+#pragma unroll 1
   for (int h = 1; h < 32; h <<= 1) {
-    const long long a = __shfl_up_sync(0xffffffffu, iu, h), b = __shfl_up_sync(0xffffffffu, ii, h);
-    if (lane >= h) {
-      iu += a;
-      ii += b;
+    const uint32_t o = __shfl_up_sync(0xffffffffu, incl, h);
+    if (lane >= h) incl += o;
+    if (OWN) {
+      units += __shfl_xor_sync(0xffffffffu, units, h);
+      items += __shfl_xor_sync(0xffffffffu, items, h);
     }
   }
+  constexpr int W = NT / 32;
   if (lane == 31) {
-    sums[2 * warp_id()] = iu;
-    sums[2 * warp_id() + 1] = ii;
+    sums[warp_id()] = incl;
+    sums[W + warp_id()] = units;
+    sums[2 * W + warp_id()] = items;
+  }
+  if (threadIdx.x == 0) plan[4] = 0;
+  pairs = __syncthreads_or(pairs);
+  uint32_t at = incl - mine, total = 0;
+  units = items = 0;
+#pragma unroll 1
+  for (int w = 0; w < W; ++w) {
+    if (w < static_cast<int>(warp_id())) at += sums[w];
+    total += sums[w];
+    units += sums[W + w];
+    items += sums[2 * W + w];
+  }
+  // (starts that fall make groups overlap: more than there is room or time for)
+  if (total > p.most) total = 0;
+  const int CTAs = gridDim.x;
+  int G = CTAs;
+  if (OWN) {
+    const float w = static_cast<float>(units) * kOwnTileWeight + static_cast<float>(items) * kOwnItemWeight;
+    if (items > 0)
+      G = total > 0 ? min(max(static_cast<int>(CTAs * (total / (total + w))), 1), CTAs - 1) : 0;
+    if (threadIdx.x == 0) plan[5] = units <= kShortItem * items;
+  }
+  const PrefixShare r = {static_cast<int>(blockIdx.x) >= G, static_cast<int>(blockIdx.x) - (static_cast<int>(blockIdx.x) >= G ? G : 0),
+                         CTAs - G};
+  // Part c is [x0, x1); a unit that a border lies in is the next part's.  No part
+  // may be shorter than the longest unit, so that none between two parts of an item
+  // is without one; CTAs beyond that many parts have none.
+  const uint32_t room = total / (pairs ? kPairWeight : kOneWeight);
+  const uint32_t n = room < static_cast<uint32_t>(G) ? max(room, 1u) : max(G, 1);
+  const uint32_t q = total / n, rest = total - q * n, c = r.own ? n : r.c;
+  const uint32_t x0 = c * q + min(c, rest), x1 = x0 + q + (c < rest ? 1 : 0);
+  if (c < n && x1 > x0 && x0 - at < mine) {
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) {
+      if (per > 1) s = prefix_entry(p, e);
+      const uint32_t here = static_cast<uint32_t>(s.items) * s.cnt * p.Hkv * s.weight;
+      if (x0 - at < here) {
+        const int u = (x0 - at) / s.weight, item = u / s.cnt;
+        plan[0] = e;
+        plan[1] = item / s.items;
+        plan[2] = item - plan[1] * s.items;
+        plan[3] = u - item * s.cnt;
+        plan[4] = min(x1 - at - u * s.weight, 1u << 30);
+        break;
+      }
+      at += here;
+    }
   }
   __syncthreads();
-  long long before_u = iu - units, before_i = ii - items, all_u = 0, all_i = 0;
-#pragma unroll
-  for (int w = 0; w < NT / 32; ++w) {
-    if (w < static_cast<int>(warp_id())) {
-      before_u += sums[2 * w];
-      before_i += sums[2 * w + 1];
-    }
-    all_u += sums[2 * w];
-    all_i += sums[2 * w + 1];
-  }
-  // More items than the workspace has room for: starts that fall.  No prefix then.
-  const int total = all_i <= p.max_items && all_u < (1ll << 31) ? static_cast<int>(all_u) : 0;
-  int ub = static_cast<int>(before_u), ib = static_cast<int>(before_i);
-  const int t0 = prefix_part(total, G, c), n = prefix_part(total, G, c + 1) - t0;
-  if (threadIdx.x == 0) {
-    plan[4] = n;
-    if (c == 0) p.base[2 * p.groups] = total;
-  }
-  for (int i = i0; i < i1; ++i) {
-    const PrefixGroup s = prefix_group<MT>(p, i);
-    const int here = s.items * s.cnt * p.Hkv;
-    if (c == 0) {
-      p.base[2 * i] = ub;
-      p.base[2 * i + 1] = ib;
-    }
-    if (n > 0 && t0 >= ub && t0 < ub + here) {
-      const int item = (t0 - ub) / s.cnt;
-      plan[0] = i;
-      plan[1] = item / s.items;
-      plan[2] = item - plan[1] * s.items;
-      plan[3] = t0 - ub - item * s.cnt;
-      plan[5] = ib + item + c;
-    }
-    ub += here;
-    ib += s.items * p.Hkv;
-  }
-  __syncthreads();
+  return r;
 }
 
-template <int MT>
-__device__ __forceinline__ PrefixWalk<MT> prefix_walk(const PrefixParams& p, const int* plan) {
-  PrefixWalk<MT> w;
+template <bool OWN>
+__device__ __forceinline__ PrefixWalk<OWN> prefix_walk(const PrefixParams& p, const int* plan) {
+  PrefixWalk<OWN> w;
   w.rem = plan[4];
   w.left = 0;
-  w.done = 0;
   if (w.rem > 0) {
-    w.grp = plan[0];
+    w.e = plan[0];
     w.hkv = plan[1];
     w.it = plan[2];
     w.k = plan[3];
-    w.chunk = plan[5];
-    w.s = prefix_group<MT>(p, w.grp);
-    w.left = min(w.s.cnt - w.k, w.rem);
+    w.s = prefix_entry(p, w.e);
+    w.left = min(w.s.cnt - w.k, w.share());
   }
   return w;
 }
 
-template <int D, bool BF16, int MT>
-__global__ void __launch_bounds__(320, 1)
-    fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const PrefixParams p) {
-  using Ly = PrefixLayout<D, MT>;
+// The roles of a CTA of the list; every warp of the CTA comes here and leaves
+// together.
+template <int D, bool BF16, bool OWN>
+__device__ __forceinline__ void prefix_body(const CUtensorMap& tmQ, const CUtensorMap& tmOwnQ, const CUtensorMap& tmK,
+                                            const CUtensorMap& tmV, const PrefixParams& p, uint8_t* gbase,
+                                            uint32_t base, uint32_t tmem, AbortState* ab, const int* plan,
+                                            int part) {
+  using Ly = PrefixLayout<D>;
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  using Walk = PrefixWalk<MT>;
   constexpr uint32_t IDESC_S = idesc_f16(BF16, 128, 128, false, false);
   constexpr uint32_t IDESC_PV = idesc_f16(BF16, 128, D, false, true);
-
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* gbase = smem_raw + (base - raw);
   auto bar = [&](int i) -> uint32_t { return base + Ly::BAR_OFF + 8u * i; };
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + Ly::MISC_OFF);
-  AbortState* ab = reinterpret_cast<AbortState*>(gbase + Ly::MISC_OFF + 4);
-  int* plan = reinterpret_cast<int*>(gbase + Ly::MISC_OFF + 8);   // 6
-  long long* sums = reinterpret_cast<long long*>(gbase + Ly::MISC_OFF + 32);  // 2 x 10 warps
   unsigned int* err = device_error_word();
   const uint32_t warp = warp_id(), lane = lane_id();
 
-  // Rows of a tile that no head fills (g not a power of two) are zero.
-  const int rows = p.tok * p.g;
-  if (rows < 128) {
-    for (uint32_t i = threadIdx.x; i < MT * Ly::TILE / 16u; i += Ly::NTHREADS)
-      reinterpret_cast<uint4*>(gbase + Ly::Q_OFF)[i] = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
-  }
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < Ly::NBAR; ++i) {
-      const bool p_full = i >= Ly::B_PFULL && i < Ly::B_OFULL, o_empty = i >= Ly::B_OEMPTY && i < Ly::B_MATE;
-      // (MT = 1: both groups read both O)
-      mbar_init(bar(i), p_full ? 4 : o_empty ? (MT == 1 ? 8 : 4) : i == Ly::B_MATE ? 8 : 1);
-    }
-    ab->flag = 0;
-    fence_barrier_init();
-  }
-  if (warp == 8 && lane == 0) {
-    tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
-  }
-  if (warp == 9) {
-    tmem_alloc(base + Ly::MISC_OFF, Ly::TMEM_COLS);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  // What was before is done when the next kernel in the stream may start.
-  pdl_wait();
-  pdl_launch_dependents();
-  prefix_plan<MT, Ly::NTHREADS>(p, sums, plan);
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-
-  if (warp == 8) {
+  if (warp == 10) {
     // ------------------------------------------------------------ producer
     const int page_log = 31 - __clz(p.page);  // (a page is a power of two)
     const int box = min(p.page, 128), nbox = 128 >> min(page_log, 7), per_batch = 32 >> (7 - min(page_log, 7));
-    uint32_t stage = 0, phase = 0, used = 0, q_uses = 0;
+    uint32_t stage = 0, phase = 0, used = 0, slot = 0;
+    uint32_t q_used = 0, q_odd = 0;  // bit t: slot t was filled; an odd number of times
     bool ok = true;
-    for (Walk w = prefix_walk<MT>(p, plan); ok && w.rem > 0; w.next(p)) {
-      if (q_uses > 0 && !mbar_wait_warp(bar(Ly::B_QEMPTY), (q_uses - 1) & 1, ab, err, 1101)) {
-        ok = false;
-        break;
-      }
-      const int tiles = MT == 2 && w.token(p, 1) < w.s.t1 ? 2 : 1;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar(Ly::B_QFULL), static_cast<uint32_t>(tiles * Ly::KCH * rows) * 128u);
-        for (int t = 0; t < tiles; ++t)
-          for (int c = 0; c < Ly::KCH; ++c)
-            tma_load_4d(base + Ly::Q_OFF + t * Ly::TILE + c * Ly::CHUNK, &tmQ, bar(Ly::B_QFULL), c * 64,
-                        w.hkv * p.g, w.token(p, t), 0);
-      }
-      __syncwarp();
-      ++q_uses;
+    const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
+#pragma unroll 1
+    for (auto w = prefix_walk<OWN>(p, plan); ok && w.left > 0; w.next(p)) {
+      const bool own = w.own(p), pair = w.pair(p);
       // Page ids of the next tiles, one box per lane, a batch ahead.
-      const int* table = p.table + static_cast<size_t>(w.grp) * p.max_pages;
+      const int max_pages = own ? p.max_pages : p.prefix_pages;
+      const int* table = own ? p.table + static_cast<size_t>(w.e - p.groups) * p.max_pages
+                             : p.ptable + static_cast<size_t>(w.e) * p.prefix_pages;
       auto pages = [&](int j) -> int {
         const int at = ((w.k + j) * 128 + static_cast<int>(lane) * box) >> page_log;
-        return at < p.max_pages ? table[at] : -1;
+        return at < max_pages ? table[at] : -1;
       };
-      int ids = pages(0), ahead = per_batch < w.left ? pages(per_batch) : -1;
-      for (int j = 0; ok && j < w.left; ++j) {
-        const int x = j % per_batch;
-        if (x == 0 && j > 0) {
-          ids = ahead;
-          if (j + per_batch < w.left) ahead = pages(j + per_batch);
+      int ids = 0, ahead = pages(0);
+      // Q: both slots, or the two in turn.
+      const int t0 = pair ? 0 : slot, t1 = pair ? 2 : slot + 1;
+#pragma unroll 1
+      for (int t = t0; t < t1; ++t) {
+        if ((q_used >> t & 1u) && !mbar_wait_warp_call(bar(Ly::B_QEMPTY + t), (q_odd >> t & 1u) ^ 1u, ab, err, 1101)) {
+          ok = false;
+          break;
         }
-        const int pid = __shfl_sync(0xffffffffu, ids, (x * nbox + static_cast<int>(lane)) & 31);
-        const int k0 = (w.k + j) * 128 + static_cast<int>(lane) * box;
-        const bool go = static_cast<int>(lane) < nbox && k0 < w.s.n;
-        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, go));
+        q_used |= 1u << t;
+        q_odd ^= 1u << t;
+        if (lane == 0) {
+          const CUtensorMap* map = own ? &tmOwnQ : &tmQ;
+          mbar_arrive_expect_tx(bar(Ly::B_QFULL + t), Ly::KCH * static_cast<uint32_t>(own ? p.rows : p.tok * p.g) * 128u);
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          if (!mbar_wait_warp(bar(Ly::B_KVEMPTY + stage), phase ^ 1u, ab, err, 1102)) {
-            ok = false;
-            break;
+          for (int c = 0; c < Ly::KCH; ++c)
+            tma_load_4d(base + Ly::Q_OFF + t * Ly::TILE + c * Ly::CHUNK, map, bar(Ly::B_QFULL + t), c * 64,
+                        w.hkv * p.g, own ? 0 : w.token(p, pair ? t : 0), own ? w.e - p.groups : 0);
+        }
+        __syncwarp();
+      }
+      if (!pair) slot ^= 1;
+      // K_j, V_j: one ring step each.
+      int pid = 0, k0 = 0;
+      uint32_t boxes = 0;
+      bool go = false;
+#pragma unroll 1
+      for (int jv = 0; ok && jv < 2 * w.left; ++jv) {
+        if ((jv & 1) == 0) {
+          const int j = jv >> 1, x = j & (per_batch - 1);  // (a power of two)
+          if (x == 0) {
+            ids = ahead;
+            if (j + per_batch < w.left) ahead = pages(j + per_batch);
           }
-          if (lane == 0)
-            mbar_arrive_expect_tx(bar(Ly::B_KVFULL + stage), boxes * box * static_cast<uint32_t>(D) * 2u);
-          __syncwarp();
-          if (go) {
+          pid = __shfl_sync(0xffffffffu, ids, (x * nbox + static_cast<int>(lane)) & 31);
+          k0 = (w.k + j) * 128 + static_cast<int>(lane) * box;
+          go = static_cast<int>(lane) < nbox && k0 < w.s.n;
+          boxes = __popc(__ballot_sync(0xffffffffu, go));
+        }
+        if (!mbar_wait_warp_call(bar(Ly::B_KVEMPTY + stage), phase ^ 1u, ab, err, 1102)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0)
+          mbar_arrive_expect_tx(bar(Ly::B_KVFULL + stage), boxes * box * static_cast<uint32_t>(D) * 2u);
+        __syncwarp();
+        if (go) {
+          const uint32_t dst = base + Ly::RING_OFF + stage * Ly::TILE + lane * box * 128u;
+          const CUtensorMap* map = jv & 1 ? &tmV : &tmK;
 #pragma unroll
-            for (int c = 0; c < Ly::KCH; ++c)
-              tma_load_4d(base + Ly::RING_OFF + stage * Ly::TILE + c * Ly::CHUNK + lane * box * 128u,
-                          kv ? &tmV : &tmK, bar(Ly::B_KVFULL + stage), c * 64, w.hkv, k0 & (p.page - 1), pid);
-          }
-          used |= 1u << stage;
-          if (++stage == Ly::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          for (int c = 0; c < Ly::KCH; ++c)
+            tma_load_4d_hint(dst + c * Ly::CHUNK, map, bar(Ly::B_KVFULL + stage), c * 64, w.hkv, k0 & (p.page - 1), pid,
+                             own ? first : normal);
+        }
+        used |= 1u << stage;
+        if (++stage == Ly::STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
     }
     if (!ok && lane == 0) {
       // Unwinding: let copies in flight land.  The newest use of a stage before
       // the write position has this round's parity, the others the last round's.
-      if (q_uses > 0) mbar_wait_drain(bar(Ly::B_QFULL), (q_uses - 1) & 1);
-      for (int s = 0; s < Ly::STAGES; ++s)
-        if (used >> s & 1u)
-          mbar_wait_drain(bar(Ly::B_KVFULL + s), s < static_cast<int>(stage) ? phase : phase ^ 1u);
+#pragma unroll 1
+      for (int s = 0; s < Ly::STAGES + 2; ++s) {
+        const int t = s - Ly::STAGES;
+        if (t >= 0 ? q_used >> t & 1u : used >> s & 1u)
+          mbar_wait_drain(bar(t >= 0 ? Ly::B_QFULL + t : Ly::B_KVFULL + s),
+                          t >= 0 ? (q_odd >> t & 1u) ^ 1u : s < static_cast<int>(stage) ? phase : phase ^ 1u);
+      }
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer
-    uint32_t stage = 0, phase = 0, q_cnt = 0;
-    uint32_t p_cnt0 = 0, p_cnt1 = 0, o_uses0 = 0, o_uses1 = 0;  // (scalars: they stay in registers)
+    // Bits t: phases of slot t's Q, of tile t's P and O.
+    uint32_t stage = 0, phase = 0, slot = 0, q_odd = 0, p_odd = 0, o_used = 0, o_odd = 0;
     bool ok = true;
-    auto tS = [&](int t) { return tmem + Ly::TM_S + 128u * t; };
-    auto tO = [&](int t) { return tmem + Ly::TM_O + static_cast<uint32_t>(D) * t; };
     auto commit = [&](int b) {
       if (elect_one()) tc_commit(bar(b));
       __syncwarp();
     };
-    auto issue_s = [&](int t, uint32_t ks) {
-      const uint64_t qd = sdesc_sw128(base + Ly::Q_OFF + (MT == 2 ? t : 0) * Ly::TILE, 16, 1024);
-      const uint64_t kd = sdesc_sw128(base + Ly::RING_OFF + ks * Ly::TILE, 16, 1024);
-      if (elect_one()) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t off = ((k >> 2) * Ly::CHUNK + (k & 3) * 32u) >> 4;
-          mma_ss(tS(t), qd + off, kd + off, IDESC_S, k > 0 ? 1u : 0u);
-        }
-      }
-      __syncwarp();
-    };
-    auto issue_pv = [&](int t, uint32_t vs, bool acc, int k_lo, int k_hi) {
-      const uint64_t vd = sdesc_sw128(base + Ly::RING_OFF + vs * Ly::TILE, Ly::CHUNK, 1024);
-      if (elect_one()) {
-#pragma unroll
-        for (int k = k_lo; k < k_hi; ++k)
-          mma_ts(tO(t), tS(t) + 8u * k, vd + ((2048u * k) >> 4), IDESC_PV, (acc || k > 0) ? 1u : 0u);
-      }
-      __syncwarp();
-    };
-    auto take = [&](uint32_t& slot, unsigned int site) -> bool {
-      slot = stage;
-      if (!mbar_wait_warp(bar(Ly::B_KVFULL + stage), phase, ab, err, site)) return false;
+    auto take = [&](uint32_t& at, unsigned int site) -> bool {
+      at = stage;
+      if (!mbar_wait_warp_call(bar(Ly::B_KVFULL + stage), phase, ab, err, site)) return false;
       if (++stage == Ly::STAGES) {
         stage = 0;
         phase ^= 1u;
       }
-      tc_fence_after();
       return true;
     };
-    for (Walk w = prefix_walk<MT>(p, plan); ok && w.rem > 0; w.next(p)) {
+#pragma unroll 1
+    for (auto w = prefix_walk<OWN>(p, plan); ok && w.left > 0; w.next(p)) {
       const int n = w.left;
-      const int tiles = MT == 2 && w.token(p, 1) < w.s.t1 ? 2 : 1;
-      if (!mbar_wait_warp(bar(Ly::B_QFULL), q_cnt & 1, ab, err, 1103)) { ok = false; break; }
-      ++q_cnt;
-      tc_fence_after();
-      uint32_t ks, vs;
-      if (!take(ks, 1104)) { ok = false; break; }
-      for (int t = 0; t < tiles; ++t) {
-        issue_s(t, ks);
-        commit(Ly::B_SFULL + t);
+      const bool pair = w.pair(p);
+      const int s0 = pair ? 0 : slot, s1 = pair ? 2 : slot + 1;
+#pragma unroll 1
+      for (int t = s0; t < s1; ++t) {
+        if (!mbar_wait_warp_call(bar(Ly::B_QFULL + t), q_odd >> t & 1u, ab, err, 1103)) ok = false;
+        q_odd ^= 1u << t;
       }
-      commit(Ly::B_KVEMPTY + ks);
-      for (int j = 0; ok && j < n; ++j) {
-        if (!take(vs, 1105)) { ok = false; break; }
-        const bool more = j + 1 < n;
-        if (more && !take(ks, 1106)) { ok = false; break; }
-        if (MT == 1 && more) {
-          // The other group's next step, ahead of this one's P.
-          issue_s((j + 1) & 1, ks);
-          commit(Ly::B_SFULL + ((j + 1) & 1));
-          commit(Ly::B_KVEMPTY + ks);
-        }
+      uint32_t ks = 0, vs = 0;
+      // Step j: S of unit j and PV of unit j - 1.  Two tiles: PV and S of tile 0, then
+      // of tile 1.  One: S first, which is the other group's.
+#pragma unroll 1
+      for (int j = 0; ok && j <= n; ++j) {
+        if (j > 0) {
+          if (!take(vs, 1104)) { ok = false; break; }
+          const int valid = w.s.n - (w.k + j - 1) * 128;
+          if (valid < 128) {
+            // V's rows behind the last key are zero, whatever their slots hold (P is
+            // zero there, but 0 x NaN is not).
+#pragma unroll 1
+            for (int i = valid * 8 + static_cast<int>(lane); i < 128 * 8; i += 32)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (MT == 1 ? (j & 1) != t : t >= tiles) continue;
-          uint32_t& p_cnt = t ? p_cnt1 : p_cnt0;
-          uint32_t& o_uses = t ? o_uses1 : o_uses0;
-          const bool first = MT == 1 ? j < 2 : j == 0;
-          if (first && o_uses > 0 &&
-              !mbar_wait_warp(bar(Ly::B_OEMPTY + t), (o_uses - 1) & 1, ab, err, 1107)) {
-            ok = false;
-            break;
-          }
-          if (!mbar_wait_warp(bar(Ly::B_PFULL + 2 * t), p_cnt & 1, ab, err, 1108)) { ok = false; break; }
-          tc_fence_after();
-          issue_pv(t, vs, !first, 0, 4);
-          if (!mbar_wait_warp(bar(Ly::B_PFULL + 2 * t + 1), p_cnt & 1, ab, err, 1109)) { ok = false; break; }
-          ++p_cnt;
-          tc_fence_after();
-          issue_pv(t, vs, true, 4, 8);
-          if (MT == 1 ? j + 2 >= n : !more) {  // the tile's (or the group's) last step
-            commit(Ly::B_OFULL + t);
-            ++o_uses;
-          }
-          if (MT == 2 && more) {
-            issue_s(t, ks);
-            commit(Ly::B_SFULL + t);
+              for (int c = 0; c < Ly::KCH; ++c)
+                reinterpret_cast<uint4*>(gbase + Ly::RING_OFF + vs * Ly::TILE + c * Ly::CHUNK)[i] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
           }
         }
-        if (!ok) break;
-        commit(Ly::B_KVEMPTY + vs);
-        if (MT == 2 && more) commit(Ly::B_KVEMPTY + ks);
+        if (j < n && !take(ks, 1105)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll 1
+        for (int o = pair ? 0 : 1; o < (pair ? 4 : 3); ++o) {
+          const bool is_s = o & 1;
+          if (is_s ? j == n : j == 0) continue;
+          const int t = pair ? o >> 1 : (is_s ? j : j - 1) & 1;
+          const uint32_t tS = tmem + Ly::TM_S + 128u * t;
+          if (is_s) {
+            const uint64_t qd = sdesc_sw128(base + Ly::Q_OFF + (pair ? t : slot) * Ly::TILE, 16, 1024);
+            const uint64_t kd = sdesc_sw128(base + Ly::RING_OFF + ks * Ly::TILE, 16, 1024);
+            if (elect_one()) {
+#pragma unroll 1
+              for (uint32_t c = 0; c < Ly::KCH * (Ly::CHUNK >> 4); c += Ly::CHUNK >> 4)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_ss(tS, qd + c + 2 * k, kd + c + 2 * k, IDESC_S, (c > 0 || k > 0) ? 1u : 0u);
+              tc_commit(bar(Ly::B_SFULL + t));
+              if (!pair || t == 1) tc_commit(bar(Ly::B_KVEMPTY + ks));
+            }
+            __syncwarp();
+          } else {
+            const bool start = pair ? j == 1 : j < 3;  // nothing to add to yet
+            if (start) {
+              if ((o_used >> t & 1u) &&
+                  !mbar_wait_warp_call(bar(Ly::B_OEMPTY + t), (o_odd >> t & 1u) ^ 1u, ab, err, 1106)) {
+                ok = false;
+                break;
+              }
+              o_used |= 1u << t;
+              o_odd ^= 1u << t;
+            }
+            const uint64_t vd = sdesc_sw128(base + Ly::RING_OFF + vs * Ly::TILE, Ly::CHUNK, 1024);
+            const bool last = pair ? j == n : j + 1 >= n;  // of the tile, or the group
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              // The first half of P while the softmax finishes the second.
+              if (!mbar_wait_warp_call(bar(Ly::B_PFULL + 2 * t + h), p_odd >> t & 1u, ab, err, 1107)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_ts(tmem + Ly::TM_O + static_cast<uint32_t>(D) * t, tS + 32u * h + 8u * k,
+                         vd + ((8192u * h + 2048u * k) >> 4), IDESC_PV, (!start || h > 0 || k > 0) ? 1u : 0u);
+                if (h == 1) {
+                  if (last) tc_commit(bar(Ly::B_OFULL + t));
+                  if (!pair || t == 1) tc_commit(bar(Ly::B_KVEMPTY + vs));
+                }
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+            p_odd ^= 1u << t;
+          }
+        }
       }
       if (!ok) break;
-      commit(Ly::B_QEMPTY);
+#pragma unroll 1
+      for (int t = s0; t < s1; ++t) commit(Ly::B_QEMPTY + t);
+      if (!pair) slot ^= 1;
     }
     commit(Ly::B_DONE);
     mbar_wait_drain(bar(Ly::B_DONE), 0);
-  } else {
+  } else if (warp < 8) {
     // ------------------------------------------------------------ softmax
-    const int t = warp >> 2;          // MT = 2: the tile; MT = 1: steps j % 2 = t
+    const int t = warp >> 2;          // two tiles: the tile; one: steps j % 2 = t
     const int r = threadIdx.x & 127;  // row of the tile == TMEM lane
     const uint32_t lane_off = ((warp & 3u) * 32u) << 16;
     const uint32_t tS = tmem + lane_off + Ly::TM_S + 128u * t;
-    const uint32_t tO = tmem + lane_off + Ly::TM_O + static_cast<uint32_t>(D) * t;
+    const uint32_t tO = tmem + lane_off + Ly::TM_O;
     const float sl2 = p.sl2;
-    uint32_t s_cnt = 0, o_cnt = 0, o1_cnt = 0, mates = 0;
-    uint32_t ring = 0;  // ring position of the chunk's first K
+    float* mate = reinterpret_cast<float*>(gbase + Ly::MATE_OFF);
+    uint32_t s_cnt = 0, o_cnt[2] = {0, 0}, mates = 0;
     bool ok = true;
-    for (Walk w = prefix_walk<MT>(p, plan); ok && w.rem > 0; ring += 2 * w.left, w.next(p)) {
-      const int tile = MT == 2 ? t : 0;
-      const int tok0 = w.token(p, tile);
-      if (MT == 2 && tok0 >= w.s.t1) continue;
-      const bool live = r < rows && tok0 + (r * p.ginv >> 16) < w.s.t1;
+#pragma unroll 1
+    for (auto w = prefix_walk<OWN>(p, plan); ok && w.left > 0; w.next(p)) {
+      const bool pair = w.pair(p), own = w.own(p);
+      const int rows = w.rows(p, pair ? t : 0), step = pair ? 1 : 2;
+      const bool live = r < rows, some = static_cast<int>((warp & 3u) * 32u) < rows;  // (some: this warp has a row)
+      // Own keys come last and all have as many rows: warps without one are done, and
+      // the first warp arrives for them.
+      if (own && !some) break;
+      const uint32_t arrive = own && (warp & 3u) == 0 ? 4 - (p.rows - 1) / 32 : 1;
+      const int seen = own ? w.s.n - p.Lq + 1 + (r * p.ginv >> 16) : w.s.n;  // keys this row sees
       float m = -INFINITY, l = 0.f;
-      for (int j = MT == 2 ? 0 : t; j < w.left; j += MT == 2 ? 1 : 2) {
-        if (!mbar_wait_warp(bar(Ly::B_SFULL + t), s_cnt & 1, ab, err, 1110)) { ok = false; break; }
+#pragma unroll 1
+      for (int j = pair ? 0 : t; j < w.left; j += step) {
+        if (!mbar_wait_warp_call(bar(Ly::B_SFULL + t), s_cnt & 1, ab, err, 1110)) { ok = false; break; }
         ++s_cnt;
+        if (!some) {
+          if (lane == 0) {
+            mbar_arrive(bar(Ly::B_PFULL + 2 * t));
+            mbar_arrive(bar(Ly::B_PFULL + 2 * t + 1));
+          }
+          continue;
+        }
         tc_fence_after();
         uint32_t sr[128];
         tmem_ld32(tS + 0, sr);
@@ -486,11 +581,11 @@ __global__ void __launch_bounds__(320, 1)
         tmem_ld_wait32(sr + 32);
         tmem_ld_wait32(sr + 64);
         tmem_ld_wait32(sr + 96);
-        const int valid = w.s.n - (w.k + j) * 128;  // keys of the tile, >= 1
-        if (valid < 128) {
+        const int lim = seen - (w.k + j) * 128;
+        if (__any_sync(0xffffffffu, lim < 128)) {
 #pragma unroll
           for (int c = 0; c < 128; ++c)
-            if (c >= valid) sr[c] = __float_as_uint(-INFINITY);
+            if (c >= lim) sr[c] = __float_as_uint(-INFINITY);
         }
         float mx8[8];
 #pragma unroll
@@ -506,52 +601,35 @@ __global__ void __launch_bounds__(320, 1)
         const float m_new = fmaxf(m, mx);
         float alpha = 1.f;
         bool rescale = false;
-        if (j == (MT == 2 ? 0 : t)) {
+        if (j < step) {
           m = m_new;
-        } else if (__any_sync(0xffffffffu, (m_new - m) * sl2 > 8.0f)) {
+        } else if (__any_sync(0xffffffffu, live && (m_new - m) * sl2 > 8.0f)) {
           // Some row's maximum grew by more than 2^8: this warp's rows move theirs.
-          // (A row whose scores were all -inf so far has O = l = 0.)
+          // (What the lanes without a row see is left of other chunks.)
+          // (A row that has seen nothing so far has O = l = 0.)
           if (m_new != -INFINITY) alpha = ex2((m - m_new) * sl2);
           m = m_new;
           rescale = true;
         }
         // Half h of P is in TMEM.  Before the first, O is scaled if the maximum
-        // moved (the commit behind this S covers the tile's, or group's, last PV),
-        // and V's rows behind the prefix's end, whatever their slots hold, are zero.
+        // moved (the commit behind this S covers the tile's, or group's, last PV).
         auto p_ready = [&](int h) {
           if (h == 0 && rescale) {
 #pragma unroll
             for (int cc = 0; cc < D / 32; ++cc) {
               uint32_t o[32];
-              tmem_ld32(tO + 32 * cc, o);
+              tmem_ld32(tO + D * t + 32 * cc, o);
               tmem_ld_wait32(o);
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st32(tO + 32 * cc, o);
+              tmem_st32(tO + D * t + 32 * cc, o);
             }
           }
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(Ly::B_PFULL + 2 * t + h));
+          if (lane == 0) prefix_arrive(bar(Ly::B_PFULL + 2 * t + h), arrive);
         };
-        if (valid < 128 && tile == 0) {
-          // (V's stage held, before it, a tile that S of this step or an earlier
-          // product has used, so the parity cannot be the fill before's.)
-          const uint32_t pos = ring + 2 * j + 1;
-          if (!mbar_wait_warp(bar(Ly::B_KVFULL + pos % Ly::STAGES), (pos / Ly::STAGES) & 1, ab, err, 1111)) {
-            ok = false;
-            break;
-          }
-          if (r >= valid) {
-            uint4* v = reinterpret_cast<uint4*>(gbase + Ly::RING_OFF + (pos % Ly::STAGES) * Ly::TILE + r * 128);
-#pragma unroll
-            for (int c = 0; c < Ly::KCH; ++c)
-#pragma unroll
-              for (int u = 0; u < 8; ++u) v[c * (Ly::CHUNK / 16) + u] = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-        }
         const float mb = m == -INFINITY ? 0.f : m * sl2;
         const uint64_t sl2x2 = f2_pack(sl2, sl2), nmb2 = f2_pack(-mb, -mb);
         uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
@@ -583,74 +661,163 @@ __global__ void __launch_bounds__(320, 1)
       }
       if (!ok) break;
       // ---- the chunk's partial: O / l and its LSE
-      float f0 = 1.f, f1 = 0.f;  // factors of O_0 and O_1 (MT = 1)
-      bool both = false;
-      if constexpr (MT == 1) {
-        // Both groups leave their maxima and sums; each stores half of the columns.
-        float* mate = reinterpret_cast<float*>(gbase + Ly::MATE_OFF) + (mates & 1) * 512;  // [2][m, l][128]
-        mate[256 * t + r] = m;
-        mate[256 * t + 128 + r] = l;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(Ly::B_MATE));
-        if (!mbar_wait_warp(bar(Ly::B_MATE), mates & 1, ab, err, 1112)) { ok = false; break; }
+      const bool two = !pair && w.left > 1;  // one tile's O in two parts
+      const uint32_t oc0 = o_cnt[0], oc1 = o_cnt[1];
+      ++o_cnt[0];  // (every chunk fills O_0, who waits for it or not)
+      if (pair || two) ++o_cnt[1];
+      float f0 = 1.f, f1 = 0.f;              // factors of O_t, or O_0 and O_1
+      if (!pair) {
+        if (t == 0) {
+          // Warps 4-7 finish the tile.
+          if (mates > 0 && !mbar_wait_warp_call(bar(Ly::B_MEMPTY), (mates - 1) & 1, ab, err, 1111)) { ok = false; break; }
+          ++mates;
+          mate[r] = m;
+          mate[128 + r] = l;
+          __syncwarp();
+          if (lane == 0) prefix_arrive(bar(Ly::B_MFULL), arrive);
+          continue;
+        }
+        if (!mbar_wait_warp_call(bar(Ly::B_MFULL), mates & 1, ab, err, 1112)) { ok = false; break; }
         ++mates;
-        const float m0 = mate[r], m1 = mate[256 + r];
-        const float top = fmaxf(m0, m1);
+        const float m0 = mate[r], l0 = mate[128 + r], top = fmaxf(m0, m);
+        __syncwarp();
+        if (lane == 0) prefix_arrive(bar(Ly::B_MEMPTY), arrive);
         f0 = m0 == -INFINITY ? 0.f : ex2((m0 - top) * sl2);
-        f1 = m1 == -INFINITY ? 0.f : ex2((m1 - top) * sl2);
-        l = mate[128 + r] * f0 + mate[384 + r] * f1;
+        f1 = m == -INFINITY ? 0.f : ex2((m - top) * sl2);
+        l = l0 * f0 + l * f1;
         m = top;
-        both = w.left > 1;
-        if (!mbar_wait_warp(bar(Ly::B_OFULL), o_cnt & 1, ab, err, 1113)) { ok = false; break; }
-        ++o_cnt;
-        if (both) {
-          if (!mbar_wait_warp(bar(Ly::B_OFULL + 1), o1_cnt & 1, ab, err, 1114)) { ok = false; break; }
-          ++o1_cnt;
-        }
-      } else {
-        if (!mbar_wait_warp(bar(Ly::B_OFULL + t), o_cnt & 1, ab, err, 1115)) { ok = false; break; }
-        ++o_cnt;
       }
-      tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      f0 *= inv;
-      f1 *= inv;
-      const size_t at = static_cast<size_t>(w.chunk) * MT + tile;
-      float4* dst = reinterpret_cast<float4*>(p.part_o) + at * (D / 4) * 128 + r;
-      const int c0 = MT == 1 ? t * (D / 64) : 0, c1 = MT == 1 ? c0 + D / 64 : D / 32;
+      const int o0 = pair ? t : 0;
+      if (!mbar_wait_warp_call(bar(Ly::B_OFULL + o0), (o0 ? oc1 : oc0) & 1, ab, err, 1113) ||
+          (two && !mbar_wait_warp_call(bar(Ly::B_OFULL + 1), oc1 & 1, ab, err, 1114))) {
+        ok = false;
+        break;
+      }
+      const int item = own ? (w.e - p.groups) * p.Hkv + w.hkv
+                           : prefix_first_item(p, w.s, w.e) + w.hkv * w.s.items + w.it;
+      const size_t at = static_cast<size_t>(item) + part;
+      if (some) {
+        tc_fence_after();
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        f0 *= inv;
+        f1 *= inv;
+        const size_t tile = 2 * at + (pair ? t : 0);
+        float4* dst = own ? reinterpret_cast<float4*>(p.own_o) + (at * p.rows + r) * (D / 4)
+                          : reinterpret_cast<float4*>(p.part_o) + tile * (D / 4) * 128 + r;
+        const int pitch = own ? 1 : 128;
 #pragma unroll 1
-      for (int cc = c0; cc < c1; ++cc) {
-        uint32_t o[32];
-        tmem_ld32(tmem + lane_off + Ly::TM_O + (MT == 2 ? D * t : 0) + 32 * cc, o);
-        tmem_ld_wait32(o);
-        float v[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * f0;
-        if (MT == 1 && both) {
-          tmem_ld32(tmem + lane_off + Ly::TM_O + D + 32 * cc, o);
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t o[32];
+          tmem_ld32(tO + D * o0 + 32 * cc, o);
           tmem_ld_wait32(o);
+          float v[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(o[i]), f1, v[i]);
-        }
-        if (live) {
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * f0;
+          if (two) {
+            tmem_ld32(tO + D + 32 * cc, o);
+            tmem_ld_wait32(o);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[(8 * cc + i) * 128] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(o[i]), f1, v[i]);
+          }
+          if (live) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[(8 * cc + i) * pitch] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
         }
+        const float lse = l == 0.f ? -INFINITY : m * sl2 + __log2f(l);  // (NaN stays NaN)
+        if (live) (own ? p.own_lse + at * p.rows : p.part_lse + tile * 128)[r] = lse;
+        tc_fence_before();
       }
-      if (live && (MT == 2 || t == 0))
-        p.part_lse[at * 128 + r] = l == 0.f ? -INFINITY : m * sl2 + __log2f(l);  // (NaN stays NaN)
-      tc_fence_before();
+      // The item's first and last part, for the join.
+      if (r == 0 && (!pair || t == 0)) {
+        int* ends = p.ends + 2 * (own ? static_cast<size_t>(p.items) + item : static_cast<size_t>(item));
+        if (w.k == 0) ends[0] = part;
+        if (w.k + w.left == w.s.cnt) ends[1] = part;
+      }
       __syncwarp();
       if (lane == 0) {
-        if (MT == 2) {
-          mbar_arrive(bar(Ly::B_OEMPTY + t));
-        } else {
-          mbar_arrive(bar(Ly::B_OEMPTY));
-          if (both) mbar_arrive(bar(Ly::B_OEMPTY + 1));
-        }
+        prefix_arrive(bar(Ly::B_OEMPTY + o0), arrive);
+        if (two) prefix_arrive(bar(Ly::B_OEMPTY + 1), arrive);
       }
     }
+  }
+}
+
+// Shared memory of a CTA: the layout of its role, behind both the common words.
+template <int D, int R>
+struct PrefixShared {
+  static constexpr uint32_t OWN_USED = PagedLayout<D, R == 0 ? 8 : R>::SMEM_USED;
+  static constexpr uint32_t PREFIX_USED = PrefixLayout<D>::USED;
+  static constexpr uint32_t OFF = R > 0 && OWN_USED > PREFIX_USED ? (OWN_USED + 15) / 16 * 16 : (PREFIX_USED + 15) / 16 * 16;
+  // plan [8], lens [32], sums [3][11], tmem slot, abort flag
+  static constexpr uint32_t PLAN = OFF, LENS = OFF + 32, SUMS = OFF + 160, SLOT = OFF + 336, FLAG = OFF + 340;
+  static constexpr uint32_t ALLOC = OFF + 352 + 1024;
+  static constexpr int NTHREADS = 352;
+  static_assert(ALLOC <= 232448, "shared memory");
+};
+
+// R: query rows a thread of the paged decode's roles takes (g * Lq rounded up to
+// 8, 16 or 32), or 0: own keys are in the list of prefixes.
+template <int D, bool BF16, int R>
+__global__ void __launch_bounds__(352, 1)
+    fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmOwnQ,
+                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const PrefixParams p, const PagedOwnParams o) {
+  using Sh = PrefixShared<D, R>;
+  constexpr int NT = Sh::NTHREADS;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + Sh::SLOT);
+  AbortState* ab = reinterpret_cast<AbortState*>(gbase + Sh::FLAG);
+  int* plan = reinterpret_cast<int*>(gbase + Sh::PLAN);
+  uint32_t* sums = reinterpret_cast<uint32_t*>(gbase + Sh::SUMS);
+  const uint32_t warp = warp_id(), lane = lane_id();
+
+  if (threadIdx.x == 0) ab->flag = 0;
+  if (warp == 10 && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmOwnQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 9) {
+    tmem_alloc(base + Sh::SLOT, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  pdl_launch_dependents();
+  pdl_wait();
+  const PrefixShare mine = prefix_plan<NT, R != 0>(p, sums, plan);
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (R == 0 || !mine.own) {
+    using Ly = PrefixLayout<D>;
+    if (threadIdx.x < Ly::NBAR) mbar_init(base + Ly::BAR_OFF + 8u * threadIdx.x, Ly::arrivals(threadIdx.x));
+    fence_barrier_init();
+    __syncthreads();
+    prefix_body<D, BF16, R == 0>(tmQ, tmOwnQ, tmK, tmV, p, gbase, base, tmem, ab, plan, mine.c);
+  } else if constexpr (R != 0) {
+    using Ly = PagedLayout<D, R>;
+    // Query rows past g * Lq, and P rows no thread writes, are zero.
+#pragma unroll 1
+    for (uint32_t i = threadIdx.x; i < (Ly::QS * Ly::QT + Ly::PB * Ly::PT) / 16u; i += NT)
+      reinterpret_cast<uint4*>(gbase + Ly::Q_OFF)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+#pragma unroll 1
+    for (int i = threadIdx.x; i < Ly::NBAR; i += NT) mbar_init(base + Ly::BAR_OFF + 8u * i, Ly::arrivals(i));
+    fence_barrier_init();
+    const bool brief = plan[5] != 0;
+    int* lens_s = reinterpret_cast<int*>(gbase + Sh::LENS);
+    const int len = (o.B <= 32 && static_cast<int>(lane) < o.B) ? o.lens[lane] : 0;
+    if (warp == 0) lens_s[lane] = len;
+    __syncthreads();  // (plan is read, and written again)
+    paged_plan<NT>(o, mine.c, mine.G, len, reinterpret_cast<int*>(sums), plan);
+    paged_body<D, BF16, R>(tmOwnQ, tmK, tmV, o, gbase, base, tmem, ab, plan, o.B <= 32 ? lens_s : o.lens, mine.c, mine.G,
+                                 brief);
   }
 
   tc_fence_before();
@@ -658,41 +825,43 @@ __global__ void __launch_bounds__(320, 1)
   if (warp == 9) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, Ly::TMEM_COLS);
+    tmem_dealloc(tmem, 512);
   }
 }
 
 struct PrefixJoinParams {
   PrefixParams p;
-  const int* own_lens;   // [B]
-  const float* own_o;    // [B, Lq, H, D]
-  const float* own_lse;  // [B, H, Lq], natural log
-  void* O;               // [B, Lq, H, D]
-  float* LSE;            // [B, H, Lq], natural log
-  int own_cap;
-  int G;                 // CTAs of fa_prefix_kernel
+  void* O;     // [B, Lq, H, D]
+  float* LSE;  // [B, H, Lq], natural log
+  int G;       // CTAs of fa_prefix_kernel
 };
 
-// Join each row's partials: those of its prefix's chunks and that of its own
-// keys.  A thread joins 8 dims of one row; the lanes run over the g heads of a
-// K/V head, whose rows lie together in a partial, then over the dims.
-template <int D, bool BF16, int MT>
-__global__ void __launch_bounds__(256) fa_prefix_join_kernel(const PrefixJoinParams a) {
+// Join each row's partials: those of its prefix's chunks and of its own keys'.
+// Four threads join 4 dims of one row, each every fourth partial; the lanes run
+// over the g heads of a K/V head, whose rows lie together in a prefix's partial,
+// then over the dims.  Block (x, y): token and K/V head x, 32 cells from 32 y.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(128) fa_prefix_join_kernel(const PrefixJoinParams a) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   const PrefixParams& p = a.p;
+  const int pair = blockIdx.x;
+  const int tk = pair / p.Hkv, hkv = pair - tk * p.Hkv;
+  const int b = tk / p.Lq, ql = tk - b * p.Lq;
+  const int lane = lane_id(), sp = lane >> 3;
+  const int cell = blockIdx.y * 32 + static_cast<int>(warp_id()) * 8 + (lane & 7);
+  const int d4 = cell / p.g, hg = cell - d4 * p.g;
+  const bool in = d4 < D / 4;
   pdl_launch_dependents();
   pdl_wait();
-  const int per = p.g * (D / 8), ppb = per <= 256 ? 256 / per : 1;
-  const int pl = static_cast<int>(threadIdx.x) / per;  // pair (token, K/V head) of the block
-  const long long pair = static_cast<long long>(blockIdx.x) * ppb + pl;
-  if (pl >= ppb || pair >= static_cast<long long>(p.B) * p.Lq * p.Hkv) return;
-  const int tk = static_cast<int>(pair / p.Hkv), hkv = static_cast<int>(pair - static_cast<long long>(tk) * p.Hkv);
-  const int b = tk / p.Lq, ql = tk - b * p.Lq;
-  const bool pad = min(max(a.own_lens[b], 0), a.own_cap) - p.Lq + ql < 0;
+  const int own_n = min(max(p.lens[b], 0), p.cap);
+  const bool pad = own_n - p.Lq + ql < 0;
+  const int own_item = b * p.Hkv + hkv;
+  const int2 oe = __ldcg(reinterpret_cast<const int2*>(p.ends) + p.items + own_item);
   // The sequence's group, and the chunks of its tile.
   int grp = 0;
   if (p.starts != nullptr) {
     int lo = 0, hi = p.groups;  // the last group that starts at or before b
+#pragma unroll 1
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (p.starts[mid] <= b) lo = mid;
@@ -700,64 +869,80 @@ __global__ void __launch_bounds__(256) fa_prefix_join_kernel(const PrefixJoinPar
     }
     grp = lo;
   }
-  const PrefixGroup s = prefix_group<MT>(p, grp);
-  int n = 0, chunk0 = 0, row0 = 0, tile = 0;
-  const int total = p.base[2 * p.groups];
-  if (!pad && total > 0 && s.items > 0 && tk >= s.t0 && tk < s.t1) {
-    tile = (tk - s.t0) / p.tok;
-    row0 = (tk - s.t0 - tile * p.tok) * p.g;
-    const int it = hkv * s.items + tile / MT;
-    const int first = p.base[2 * grp] + it * s.cnt;
-    const int c0 = prefix_part_of(total, a.G, first), c1 = prefix_part_of(total, a.G, first + s.cnt - 1);
-    chunk0 = p.base[2 * grp + 1] + it + c0;
-    n = c1 - c0 + 1;
-    tile %= MT;
-  }
-  for (int x = static_cast<int>(threadIdx.x) - pl * per; x < per; x += 256) {
-    const int d8 = x / p.g, hg = x - d8 * p.g, h = hkv * p.g + hg;
-    const size_t out = (static_cast<size_t>(tk) * p.H + h) * D + 8 * d8;
-    const size_t lse_at = (static_cast<size_t>(b) * p.H + h) * p.Lq + ql;
-    float mx = -INFINITY, den = 0.f, acc[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    if (!pad) {
-      auto add = [&](float lse, const float4& u, const float4& v) {
-        const float m = fmaxf(mx, lse);
-        // (each for itself: a NaN LSE has no part in m, but its weight is NaN)
-        const float old = mx == -INFINITY ? 0.f : ex2(mx - m), w = lse == -INFINITY ? 0.f : ex2(lse - m);
-        const float o[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-        den = fmaf(den, old, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = fmaf(acc[i], old, lse == -INFINITY ? 0.f : w * o[i]);
-        mx = m;
-      };
-      const float4* own = reinterpret_cast<const float4*>(a.own_o + out);
-      const float4 ou = own[0], ov = own[1];
-      const float ol = a.own_lse[lse_at] * 1.4426950408889634f;
-      constexpr int C = 4;
-#pragma unroll 1
-      for (int q0 = 0; q0 < n; q0 += C) {
-        float ls[C];
-        float4 u[C], v[C];
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const size_t at = static_cast<size_t>(chunk0 + min(q0 + c, n - 1)) * MT + tile;
-          const float4* src = reinterpret_cast<const float4*>(p.part_o) + (at * (D / 4) + 2 * d8) * 128 + row0 + hg;
-          ls[c] = q0 + c < n ? p.part_lse[at * 128 + row0 + hg] : -INFINITY;
-          u[c] = src[0];
-          v[c] = src[128];
-        }
-#pragma unroll
-        for (int c = 0; c < C; ++c) add(ls[c], u[c], v[c]);
-      }
-      add(ol, ou, ov);
+  const PrefixEntry s = prefix_entry(p, grp);
+  int n = 0, slot = 0, row = 0, n_own = 0, own_slot = 0;
+  if (!pad) {
+    if (s.items > 0 && tk >= s.t0 && tk < s.t1) {
+      const int tile = (tk - s.t0) / p.tok;
+      row = (tk - s.t0 - tile * p.tok) * p.g + hg;
+      const int item = prefix_first_item(p, s, grp) + hkv * s.items + (tile >> 1);
+      const int2 e = __ldcg(reinterpret_cast<const int2*>(p.ends) + item);
+      const int c0 = min(max(e.x, 0), a.G - 1);  // (in bounds even where starts fall)
+      n = min(max(e.y, c0), a.G - 1) - c0 + 1;
+      slot = 2 * (item + c0) + (tile & 1);
     }
-    const float inv = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);  // (NaN stays NaN)
-    *reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.O) + out) =
-        make_uint4(pack2<T>(acc[0] * inv, acc[1] * inv), pack2<T>(acc[2] * inv, acc[3] * inv),
-                   pack2<T>(acc[4] * inv, acc[5] * inv), pack2<T>(acc[6] * inv, acc[7] * inv));
-    if (d8 == 0) a.LSE[lse_at] = den == 0.f ? -INFINITY : (mx + __log2f(den)) * 0.6931471805599453f;
+    const int c0 = min(max(oe.x, 0), a.G - 1);
+    n_own = min(max(oe.y, c0), a.G - 1) - c0 + 1;
+    own_slot = own_item + c0;
   }
+  const int own_row = ql * p.g + hg, all = in ? n + n_own : 0;
+  float mx = -INFINITY, den = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int C = 5;
+  for (int q0 = sp; q0 < all; q0 += 4 * C) {
+    float ls[C];
+    float4 o[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int q = q0 + 4 * c;
+      ls[c] = -INFINITY;
+      o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (q < n) {
+        const size_t at = static_cast<size_t>(slot) + 2 * q;
+        ls[c] = __ldcg(p.part_lse + at * 128 + row);
+        o[c] = __ldcg(reinterpret_cast<const float4*>(p.part_o) + (at * (D / 4) + d4) * 128 + row);
+      } else if (q < all) {
+        const size_t at = (static_cast<size_t>(own_slot) + q - n) * p.rows + own_row;
+        ls[c] = __ldcg(p.own_lse + at);
+        o[c] = __ldcg(reinterpret_cast<const float4*>(p.own_o) + at * (D / 4) + d4);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const float m = fmaxf(mx, ls[c]);
+      // (each for itself: a NaN LSE has no part in m, but its weight is NaN)
+      const float old = mx == -INFINITY ? 0.f : ex2(mx - m), w = ls[c] == -INFINITY ? 0.f : ex2(ls[c] - m);
+      den = fmaf(den, old, w);
+      acc.x = fmaf(acc.x, old, w * o[c].x);
+      acc.y = fmaf(acc.y, old, w * o[c].y);
+      acc.z = fmaf(acc.z, old, w * o[c].z);
+      acc.w = fmaf(acc.w, old, w * o[c].w);
+      mx = m;
+    }
+  }
+#pragma unroll
+  for (int h = 8; h <= 16; h <<= 1) {
+    const float om = __shfl_xor_sync(0xffffffffu, mx, h), od = __shfl_xor_sync(0xffffffffu, den, h);
+    const float4 oa = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, h), __shfl_xor_sync(0xffffffffu, acc.y, h),
+                                  __shfl_xor_sync(0xffffffffu, acc.z, h), __shfl_xor_sync(0xffffffffu, acc.w, h));
+    const float m = fmaxf(mx, om);
+    const float u = mx == -INFINITY ? 0.f : ex2(mx - m), v = om == -INFINITY ? 0.f : ex2(om - m);
+    // (a side that has seen NaN alone has no maximum: its den carries it)
+    den = (mx == -INFINITY ? den : den * u) + (om == -INFINITY ? od : od * v);
+    acc.x = acc.x * u + oa.x * v;
+    acc.y = acc.y * u + oa.y * v;
+    acc.z = acc.z * u + oa.z * v;
+    acc.w = acc.w * u + oa.w * v;
+    mx = m;
+  }
+  if (!in || sp != 0) return;
+  const int h = hkv * p.g + hg;
+  const float inv = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);  // (NaN stays NaN)
+  *reinterpret_cast<uint2*>(reinterpret_cast<T*>(a.O) + (static_cast<size_t>(tk) * p.H + h) * D + 4 * d4) =
+      make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
+  if (d4 == 0)
+    a.LSE[(static_cast<size_t>(b) * p.H + h) * p.Lq + ql] =
+        den == 0.f ? -INFINITY : (mx + __log2f(den)) * 0.6931471805599453f;
 }
 
 }  // namespace fa
