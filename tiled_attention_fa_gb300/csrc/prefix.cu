@@ -1,4 +1,5 @@
 // Host side of the attention behind shared prefixes: workspace and launches.
+#include <mutex>
 #include <type_traits>
 
 #include "common.cuh"
@@ -113,9 +114,29 @@ fa_status launch_prefix(const PrefixDecodeArgs& a, const PrefixPlan& w, PrefixJo
   auto kern = fa_prefix_kernel<D, BF16, R>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::ALLOC) != cudaSuccess)
     return FA_ERR_CUDA;
-  if (!launch_after_smem(kern, dim3(w.G), dim3(Sh::NTHREADS), Sh::ALLOC, s, tq, to, tk, tv, p, o)) return FA_ERR_CUDA;
-  const dim3 grid(static_cast<unsigned>(a.B) * a.Lq * a.Hkv, (p.g * (D / 4) + 31) / 32);
-  return launch_after(fa_prefix_join_kernel<D, BF16>, grid, dim3(128), s, j) ? FA_OK : FA_ERR_CUDA;
+  // The kernel moves registers between its warpgroups; the budgets add up only when
+  // every thread starts with REGS.  Any other allocation would leave an increase
+  // waiting for registers that never come back, so refuse to launch instead.
+  static int num_regs = -1;
+  static std::once_flag once;
+  std::call_once(once, [&] {
+    cudaFuncAttributes at;
+    if (cudaFuncGetAttributes(&at, kern) == cudaSuccess) num_regs = at.numRegs;
+  });
+  if (num_regs != PrefixLayout<D>::REGS) return FA_ERR_UNSUPPORTED;
+  // Launched when all before is done, not before: CTAs then lie in order, neighbours
+  // on the two SMs that share an instruction cache, and have the same role.  Placed
+  // one by one as SMs fall free, 256 sequences behind 16,384 keys took 142 us
+  // instead of 105.
+  kern<<<w.G, Sh::NTHREADS, Sh::ALLOC, s>>>(tq, to, tk, tv, p, o);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  // Parts of a prefix's item in the mean: with more than 8, four threads share them.
+  const int cells = p.g * (D / 4), sp = w.G > 8 * w.items ? 4 : 1;
+  const dim3 grid(static_cast<unsigned>(a.B) * a.Lq * a.Hkv, (cells * sp + 127) / 128);
+  return (sp == 1 ? launch_after(fa_prefix_join_kernel<D, BF16, 1>, grid, dim3(128), s, j)
+                  : launch_after(fa_prefix_join_kernel<D, BF16, 4>, grid, dim3(128), s, j))
+             ? FA_OK
+             : FA_ERR_CUDA;
 }
 
 template <int D, bool BF16>

@@ -199,6 +199,11 @@ struct PrefixLayout {
                        NBAR = B_DONE + 1;
   static constexpr uint32_t USED = BAR_OFF + NBAR * 8;
   static constexpr uint32_t TM_S = 0, TM_O = 256;
+  static constexpr int NTHREADS = 384;
+  // Registers a thread at launch (65,536 / 384, in eights), and of the softmax
+  // warpgroups and the other in a CTA of the list.
+  static constexpr int REGS = 168, REGS_SOFTMAX = 200, REGS_OTHER = 104;
+  static_assert(2 * REGS_SOFTMAX + REGS_OTHER == 3 * REGS, "register budgets sum to the launch's");
   // arrivals a barrier takes a phase
   __device__ static constexpr int arrivals(int i) {
     return (i >= B_PFULL && i < B_OFULL) || (i >= B_OEMPTY && i < B_DONE) ? 4 : 1;
@@ -335,6 +340,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tmQ, const CUtens
 
   if (warp == 10) {
     // ------------------------------------------------------------ producer
+    setmaxnreg_dec<Ly::REGS_OTHER>();
     const int page_log = 31 - __clz(p.page);  // (a page is a power of two)
     const int box = min(p.page, 128), nbox = 128 >> min(page_log, 7), per_batch = 32 >> (7 - min(page_log, 7));
     uint32_t stage = 0, phase = 0, used = 0, slot = 0;
@@ -357,7 +363,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tmQ, const CUtens
       const int t0 = pair ? 0 : slot, t1 = pair ? 2 : slot + 1;
 #pragma unroll 1
       for (int t = t0; t < t1; ++t) {
-        if ((q_used >> t & 1u) && !mbar_wait_warp_call(bar(Ly::B_QEMPTY + t), (q_odd >> t & 1u) ^ 1u, ab, err, 1101)) {
+        if ((q_used >> t & 1u) && !prefix_wait(bar(Ly::B_QEMPTY + t), (q_odd >> t & 1u) ^ 1u, ab, err, 1101)) {
           ok = false;
           break;
         }
@@ -391,7 +397,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tmQ, const CUtens
           go = static_cast<int>(lane) < nbox && k0 < w.s.n;
           boxes = __popc(__ballot_sync(0xffffffffu, go));
         }
-        if (!mbar_wait_warp_call(bar(Ly::B_KVEMPTY + stage), phase ^ 1u, ab, err, 1102)) {
+        if (!prefix_wait(bar(Ly::B_KVEMPTY + stage), phase ^ 1u, ab, err, 1102)) {
           ok = false;
           break;
         }
@@ -426,6 +432,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tmQ, const CUtens
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer
+    setmaxnreg_dec<Ly::REGS_OTHER>();
     // Bits t: phases of slot t's Q, of tile t's P and O.
     uint32_t stage = 0, phase = 0, slot = 0, q_odd = 0, p_odd = 0, o_used = 0, o_odd = 0;
     bool ok = true;
@@ -435,111 +442,148 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tmQ, const CUtens
     };
     auto take = [&](uint32_t& at, unsigned int site) -> bool {
       at = stage;
-      if (!mbar_wait_warp_call(bar(Ly::B_KVFULL + stage), phase, ab, err, site)) return false;
+      if (!prefix_wait(bar(Ly::B_KVFULL + stage), phase, ab, err, site)) return false;
       if (++stage == Ly::STAGES) {
         stage = 0;
         phase ^= 1u;
       }
       return true;
     };
+    // Before the first PV of tile t: the last chunk's O has been read.
+    auto o_free = [&](int t) -> bool {
+      if ((o_used >> t & 1u) && !prefix_wait(bar(Ly::B_OEMPTY + t), (o_odd >> t & 1u) ^ 1u, ab, err, 1106)) return false;
+      o_used |= 1u << t;
+      o_odd ^= 1u << t;
+      return true;
+    };
+    // V's rows behind the last key are zero, whatever their slots hold (P is zero
+    // there, but 0 x NaN is not).
+    auto clear = [&](uint32_t vs, int valid) {
+#pragma unroll 1
+      for (int i = valid * 8 + static_cast<int>(lane); i < 128 * 8; i += 32)
+#pragma unroll
+        for (int c = 0; c < Ly::KCH; ++c)
+          reinterpret_cast<uint4*>(gbase + Ly::RING_OFF + vs * Ly::TILE + c * Ly::CHUNK)[i] = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    auto s_products = [&](int t, uint64_t qd, uint64_t kd) {  // one thread
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint64_t off = ((k >> 2) * Ly::CHUNK + (k & 3) * 32u) >> 4;
+        mma_ss(tmem + Ly::TM_S + 128u * t, qd + off, kd + off, IDESC_S, k > 0 ? 1u : 0u);
+      }
+      tc_commit(bar(Ly::B_SFULL + t));
+    };
+    auto pv_products = [&](int t, uint64_t vd, int h, bool start) {  // one thread; half h of the keys
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        mma_ts(tmem + Ly::TM_O + static_cast<uint32_t>(D) * t, tmem + Ly::TM_S + 128u * t + 32u * h + 8u * k,
+               vd + ((8192u * h + 2048u * k) >> 4), IDESC_PV, (!start || h > 0 || k > 0) ? 1u : 0u);
+    };
+    const uint64_t q0 = sdesc_sw128(base + Ly::Q_OFF, 16, 1024), k0 = sdesc_sw128(base + Ly::RING_OFF, 16, 1024),
+                   v0 = sdesc_sw128(base + Ly::RING_OFF, Ly::CHUNK, 1024);
+    constexpr uint64_t TILE16 = Ly::TILE >> 4;
 #pragma unroll 1
     for (auto w = prefix_walk<OWN>(p, plan); ok && w.left > 0; w.next(p)) {
-      const int n = w.left;
-      const bool pair = w.pair(p);
-      const int s0 = pair ? 0 : slot, s1 = pair ? 2 : slot + 1;
-#pragma unroll 1
-      for (int t = s0; t < s1; ++t) {
-        if (!mbar_wait_warp_call(bar(Ly::B_QFULL + t), q_odd >> t & 1u, ab, err, 1103)) ok = false;
-        q_odd ^= 1u << t;
-      }
+      const int n = w.left, last_valid = w.s.n - (w.k + n - 1) * 128;  // keys of the chunk's last tile
       uint32_t ks = 0, vs = 0;
-      // Step j: S of unit j and PV of unit j - 1.  Two tiles: PV and S of tile 0, then
-      // of tile 1.  One: S first, which is the other group's.
+      if (w.pair(p)) {
+        // Two tiles.  Between a tile's PV and the other's nothing but its next S: what
+        // this warp does in between, the tensor cores wait for.
+        if (!prefix_wait(bar(Ly::B_QFULL), q_odd & 1u, ab, err, 1103) ||
+            !prefix_wait(bar(Ly::B_QFULL + 1), q_odd >> 1 & 1u, ab, err, 1103) || !take(ks, 1104)) {
+          ok = false;
+          break;
+        }
+        q_odd ^= 3u;
+        tc_fence_after();
+        if (elect_one()) {
+          s_products(0, q0, k0 + ks * TILE16);
+          s_products(1, q0 + TILE16, k0 + ks * TILE16);
+          tc_commit(bar(Ly::B_KVEMPTY + ks));
+        }
+        __syncwarp();
+        if (!o_free(0) || !o_free(1)) { ok = false; break; }
+#pragma unroll 1
+        for (int j = 0; ok && j < n; ++j) {
+          const bool more = j + 1 < n;
+          if (!take(vs, 1104) || (more && !take(ks, 1105))) { ok = false; break; }
+          if (!more && last_valid < 128) clear(vs, last_valid);
+          const uint64_t vd = v0 + vs * TILE16, kd = k0 + ks * TILE16;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!prefix_wait(bar(Ly::B_PFULL + 2 * t), p_odd >> t & 1u, ab, err, 1107)) { ok = false; break; }
+            tc_fence_after();
+            if (elect_one()) pv_products(t, vd, 0, j == 0);
+            __syncwarp();
+            if (!prefix_wait(bar(Ly::B_PFULL + 2 * t + 1), p_odd >> t & 1u, ab, err, 1108)) { ok = false; break; }
+            tc_fence_after();
+            if (elect_one()) {
+              pv_products(t, vd, 1, false);
+              if (!more) tc_commit(bar(Ly::B_OFULL + t));
+              if (t == 1) tc_commit(bar(Ly::B_KVEMPTY + vs));
+              if (more) {
+                s_products(t, q0 + t * TILE16, kd);
+                if (t == 1) tc_commit(bar(Ly::B_KVEMPTY + ks));
+              }
+            }
+            __syncwarp();
+          }
+          p_odd ^= 3u;
+        }
+        if (!ok) break;
+        commit(Ly::B_QEMPTY);
+        commit(Ly::B_QEMPTY + 1);
+        continue;
+      }
+      // One tile: step j is S of unit j, which is one group's, then PV of unit j - 1,
+      // the other's.
+      if (!prefix_wait(bar(Ly::B_QFULL + slot), q_odd >> slot & 1u, ab, err, 1103)) { ok = false; break; }
+      q_odd ^= 1u << slot;
+      const uint64_t qd = q0 + slot * TILE16;
 #pragma unroll 1
       for (int j = 0; ok && j <= n; ++j) {
-        if (j > 0) {
-          if (!take(vs, 1104)) { ok = false; break; }
-          const int valid = w.s.n - (w.k + j - 1) * 128;
-          if (valid < 128) {
-            // V's rows behind the last key are zero, whatever their slots hold (P is
-            // zero there, but 0 x NaN is not).
-#pragma unroll 1
-            for (int i = valid * 8 + static_cast<int>(lane); i < 128 * 8; i += 32)
-#pragma unroll
-              for (int c = 0; c < Ly::KCH; ++c)
-                reinterpret_cast<uint4*>(gbase + Ly::RING_OFF + vs * Ly::TILE + c * Ly::CHUNK)[i] = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-        }
-        if (j < n && !take(ks, 1105)) { ok = false; break; }
+        if ((j > 0 && !take(vs, 1104)) || (j < n && !take(ks, 1105))) { ok = false; break; }
         tc_fence_after();
-#pragma unroll 1
-        for (int o = pair ? 0 : 1; o < (pair ? 4 : 3); ++o) {
-          const bool is_s = o & 1;
-          if (is_s ? j == n : j == 0) continue;
-          const int t = pair ? o >> 1 : (is_s ? j : j - 1) & 1;
-          const uint32_t tS = tmem + Ly::TM_S + 128u * t;
-          if (is_s) {
-            const uint64_t qd = sdesc_sw128(base + Ly::Q_OFF + (pair ? t : slot) * Ly::TILE, 16, 1024);
-            const uint64_t kd = sdesc_sw128(base + Ly::RING_OFF + ks * Ly::TILE, 16, 1024);
-            if (elect_one()) {
-#pragma unroll 1
-              for (uint32_t c = 0; c < Ly::KCH * (Ly::CHUNK >> 4); c += Ly::CHUNK >> 4)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mma_ss(tS, qd + c + 2 * k, kd + c + 2 * k, IDESC_S, (c > 0 || k > 0) ? 1u : 0u);
-              tc_commit(bar(Ly::B_SFULL + t));
-              if (!pair || t == 1) tc_commit(bar(Ly::B_KVEMPTY + ks));
-            }
-            __syncwarp();
-          } else {
-            const bool start = pair ? j == 1 : j < 3;  // nothing to add to yet
-            if (start) {
-              if ((o_used >> t & 1u) &&
-                  !mbar_wait_warp_call(bar(Ly::B_OEMPTY + t), (o_odd >> t & 1u) ^ 1u, ab, err, 1106)) {
-                ok = false;
-                break;
-              }
-              o_used |= 1u << t;
-              o_odd ^= 1u << t;
-            }
-            const uint64_t vd = sdesc_sw128(base + Ly::RING_OFF + vs * Ly::TILE, Ly::CHUNK, 1024);
-            const bool last = pair ? j == n : j + 1 >= n;  // of the tile, or the group
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              // The first half of P while the softmax finishes the second.
-              if (!mbar_wait_warp_call(bar(Ly::B_PFULL + 2 * t + h), p_odd >> t & 1u, ab, err, 1107)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              if (elect_one()) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mma_ts(tmem + Ly::TM_O + static_cast<uint32_t>(D) * t, tS + 32u * h + 8u * k,
-                         vd + ((8192u * h + 2048u * k) >> 4), IDESC_PV, (!start || h > 0 || k > 0) ? 1u : 0u);
-                if (h == 1) {
-                  if (last) tc_commit(bar(Ly::B_OFULL + t));
-                  if (!pair || t == 1) tc_commit(bar(Ly::B_KVEMPTY + vs));
-                }
-              }
-              __syncwarp();
-            }
-            if (!ok) break;
-            p_odd ^= 1u << t;
+        if (j < n) {
+          if (elect_one()) {
+            s_products(j & 1, qd, k0 + ks * TILE16);
+            tc_commit(bar(Ly::B_KVEMPTY + ks));
           }
+          __syncwarp();
         }
+        if (j == 0) continue;
+        if (j == n && last_valid < 128) clear(vs, last_valid);
+        const int t = (j - 1) & 1;
+        if (j < 3 && !o_free(t)) { ok = false; break; }
+        const uint64_t vd = v0 + vs * TILE16;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!prefix_wait(bar(Ly::B_PFULL + 2 * t + h), p_odd >> t & 1u, ab, err, 1109)) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) {
+            pv_products(t, vd, h, j < 3);
+            if (h == 1) {
+              if (j + 1 >= n) tc_commit(bar(Ly::B_OFULL + t));  // the group's last step
+              tc_commit(bar(Ly::B_KVEMPTY + vs));
+            }
+          }
+          __syncwarp();
+        }
+        p_odd ^= 1u << t;
       }
       if (!ok) break;
-#pragma unroll 1
-      for (int t = s0; t < s1; ++t) commit(Ly::B_QEMPTY + t);
-      if (!pair) slot ^= 1;
+      commit(Ly::B_QEMPTY + slot);
+      slot ^= 1;
     }
     commit(Ly::B_DONE);
     mbar_wait_drain(bar(Ly::B_DONE), 0);
-  } else if (warp < 8) {
+  } else if (warp >= 8) {
+    setmaxnreg_dec<Ly::REGS_OTHER>();
+  } else {
     // ------------------------------------------------------------ softmax
+    setmaxnreg_inc<Ly::REGS_SOFTMAX>();
     const int t = warp >> 2;          // two tiles: the tile; one: steps j % 2 = t
     const int r = threadIdx.x & 127;  // row of the tile == TMEM lane
     const uint32_t lane_off = ((warp & 3u) * 32u) << 16;
@@ -562,7 +606,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tmQ, const CUtens
       float m = -INFINITY, l = 0.f;
 #pragma unroll 1
       for (int j = pair ? 0 : t; j < w.left; j += step) {
-        if (!mbar_wait_warp_call(bar(Ly::B_SFULL + t), s_cnt & 1, ab, err, 1110)) { ok = false; break; }
+        if (!prefix_wait(bar(Ly::B_SFULL + t), s_cnt & 1, ab, err, 1110)) { ok = false; break; }
         ++s_cnt;
         if (!some) {
           if (lane == 0) {
@@ -669,7 +713,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tmQ, const CUtens
       if (!pair) {
         if (t == 0) {
           // Warps 4-7 finish the tile.
-          if (mates > 0 && !mbar_wait_warp_call(bar(Ly::B_MEMPTY), (mates - 1) & 1, ab, err, 1111)) { ok = false; break; }
+          if (mates > 0 && !prefix_wait(bar(Ly::B_MEMPTY), (mates - 1) & 1, ab, err, 1111)) { ok = false; break; }
           ++mates;
           mate[r] = m;
           mate[128 + r] = l;
@@ -677,7 +721,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tmQ, const CUtens
           if (lane == 0) prefix_arrive(bar(Ly::B_MFULL), arrive);
           continue;
         }
-        if (!mbar_wait_warp_call(bar(Ly::B_MFULL), mates & 1, ab, err, 1112)) { ok = false; break; }
+        if (!prefix_wait(bar(Ly::B_MFULL), mates & 1, ab, err, 1112)) { ok = false; break; }
         ++mates;
         const float m0 = mate[r], l0 = mate[128 + r], top = fmaxf(m0, m);
         __syncwarp();
@@ -688,8 +732,8 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tmQ, const CUtens
         m = top;
       }
       const int o0 = pair ? t : 0;
-      if (!mbar_wait_warp_call(bar(Ly::B_OFULL + o0), (o0 ? oc1 : oc0) & 1, ab, err, 1113) ||
-          (two && !mbar_wait_warp_call(bar(Ly::B_OFULL + 1), oc1 & 1, ab, err, 1114))) {
+      if (!prefix_wait(bar(Ly::B_OFULL + o0), (o0 ? oc1 : oc0) & 1, ab, err, 1113) ||
+          (two && !prefix_wait(bar(Ly::B_OFULL + 1), oc1 & 1, ab, err, 1114))) {
         ok = false;
         break;
       }
@@ -753,14 +797,14 @@ struct PrefixShared {
   // plan [8], lens [32], sums [3][11], tmem slot, abort flag
   static constexpr uint32_t PLAN = OFF, LENS = OFF + 32, SUMS = OFF + 160, SLOT = OFF + 336, FLAG = OFF + 340;
   static constexpr uint32_t ALLOC = OFF + 352 + 1024;
-  static constexpr int NTHREADS = 352;
+  static constexpr int NTHREADS = PrefixLayout<D>::NTHREADS;
   static_assert(ALLOC <= 232448, "shared memory");
 };
 
 // R: query rows a thread of the paged decode's roles takes (g * Lq rounded up to
 // 8, 16 or 32), or 0: own keys are in the list of prefixes.
 template <int D, bool BF16, int R>
-__global__ void __launch_bounds__(352, 1)
+__global__ void __launch_bounds__(384, 1)
     fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmOwnQ,
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const PrefixParams p, const PagedOwnParams o) {
@@ -837,29 +881,32 @@ struct PrefixJoinParams {
 };
 
 // Join each row's partials: those of its prefix's chunks and of its own keys'.
-// Four threads join 4 dims of one row, each every fourth partial; the lanes run
-// over the g heads of a K/V head, whose rows lie together in a prefix's partial,
-// then over the dims.  Block (x, y): token and K/V head x, 32 cells from 32 y.
-template <int D, bool BF16>
+// SP threads join 4 dims of one row, each every SP-th of the prefix's partials; the
+// lanes run over the g heads of a K/V head, whose rows lie together in a prefix's
+// partial, then over the dims.  Block (x, y): token and K/V head x, the 128 / SP
+// cells from y * 128 / SP on.  Bound by latency: three loads that depend on one
+// another (lengths, an item's parts, the partials), so what does not depend goes
+// out together, and SP is 1 where a row has few partials.
+template <int D, bool BF16, int SP>
 __global__ void __launch_bounds__(128) fa_prefix_join_kernel(const PrefixJoinParams a) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  constexpr int C = SP == 1 ? 6 : 5, CELLS = 32 / SP;  // partials at a time; cells of a warp
   const PrefixParams& p = a.p;
   const int pair = blockIdx.x;
   const int tk = pair / p.Hkv, hkv = pair - tk * p.Hkv;
   const int b = tk / p.Lq, ql = tk - b * p.Lq;
-  const int lane = lane_id(), sp = lane >> 3;
-  const int cell = blockIdx.y * 32 + static_cast<int>(warp_id()) * 8 + (lane & 7);
+  const int lane = lane_id(), sp = lane / CELLS;
+  const int cell = (blockIdx.y * 4 + static_cast<int>(warp_id())) * CELLS + lane % CELLS;
   const int d4 = cell / p.g, hg = cell - d4 * p.g;
   const bool in = d4 < D / 4;
   pdl_launch_dependents();
   pdl_wait();
   const int own_n = min(max(p.lens[b], 0), p.cap);
-  const bool pad = own_n - p.Lq + ql < 0;
   const int own_item = b * p.Hkv + hkv;
   const int2 oe = __ldcg(reinterpret_cast<const int2*>(p.ends) + p.items + own_item);
-  // The sequence's group, and the chunks of its tile.
+  // The sequence's group.
   int grp = 0;
-  if (p.starts != nullptr) {
+  if (p.groups > 1) {
     int lo = 0, hi = p.groups;  // the last group that starts at or before b
 #pragma unroll 1
     while (hi - lo > 1) {
@@ -870,8 +917,23 @@ __global__ void __launch_bounds__(128) fa_prefix_join_kernel(const PrefixJoinPar
     grp = lo;
   }
   const PrefixEntry s = prefix_entry(p, grp);
-  int n = 0, slot = 0, row = 0, n_own = 0, own_slot = 0;
-  if (!pad) {
+  const bool pad = own_n - p.Lq + ql < 0;
+  float mx = -INFINITY, den = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float lse, const float4& o) {
+    const float m = fmaxf(mx, lse);
+    // (each for itself: a NaN LSE has no part in m, but its weight is NaN)
+    const float old = mx == -INFINITY ? 0.f : ex2(mx - m), w = lse == -INFINITY ? 0.f : ex2(lse - m);
+    den = fmaf(den, old, w);
+    acc.x = fmaf(acc.x, old, w * o.x);
+    acc.y = fmaf(acc.y, old, w * o.y);
+    acc.z = fmaf(acc.z, old, w * o.z);
+    acc.w = fmaf(acc.w, old, w * o.w);
+    mx = m;
+  };
+  if (!pad && in) {
+    // The chunks of the row's tile.
+    int n = 0, slot = 0, row = 0;
     if (s.items > 0 && tk >= s.t0 && tk < s.t1) {
       const int tile = (tk - s.t0) / p.tok;
       row = (tk - s.t0 - tile * p.tok) * p.g + hg;
@@ -881,47 +943,41 @@ __global__ void __launch_bounds__(128) fa_prefix_join_kernel(const PrefixJoinPar
       n = min(max(e.y, c0), a.G - 1) - c0 + 1;
       slot = 2 * (item + c0) + (tile & 1);
     }
-    const int c0 = min(max(oe.x, 0), a.G - 1);
-    n_own = min(max(oe.y, c0), a.G - 1) - c0 + 1;
-    own_slot = own_item + c0;
-  }
-  const int own_row = ql * p.g + hg, all = in ? n + n_own : 0;
-  float mx = -INFINITY, den = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int C = 5;
-  for (int q0 = sp; q0 < all; q0 += 4 * C) {
-    float ls[C];
-    float4 o[C];
+    // The own keys' first partial, nearly always the only one, beside them.
+    const int o0 = min(max(oe.x, 0), a.G - 1), o1 = min(max(oe.y, o0), a.G - 1);
+    const size_t own_at = static_cast<size_t>(own_item + o0) * p.rows + ql * p.g + hg;
+    const float4* own_o = reinterpret_cast<const float4*>(p.own_o) + d4;
+    const float ol = __ldcg(p.own_lse + own_at);
+    const float4 oo = __ldcg(own_o + own_at * (D / 4));
+    const float* lses = p.part_lse + static_cast<size_t>(slot) * 128 + row;
+    const float4* os = reinterpret_cast<const float4*>(p.part_o) + (static_cast<size_t>(slot) * (D / 4) + d4) * 128 + row;
+#pragma unroll 1
+    for (int q0 = sp; q0 < n; q0 += SP * C) {
+      float ls[C];
+      float4 o[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int q = q0 + 4 * c;
-      ls[c] = -INFINITY;
-      o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (q < n) {
-        const size_t at = static_cast<size_t>(slot) + 2 * q;
-        ls[c] = __ldcg(p.part_lse + at * 128 + row);
-        o[c] = __ldcg(reinterpret_cast<const float4*>(p.part_o) + (at * (D / 4) + d4) * 128 + row);
-      } else if (q < all) {
-        const size_t at = (static_cast<size_t>(own_slot) + q - n) * p.rows + own_row;
-        ls[c] = __ldcg(p.own_lse + at);
-        o[c] = __ldcg(reinterpret_cast<const float4*>(p.own_o) + at * (D / 4) + d4);
+      for (int c = 0; c < C; ++c) {
+        const int q = q0 + SP * c;
+        ls[c] = -INFINITY;
+        o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (q < n) {
+          ls[c] = __ldcg(lses + static_cast<size_t>(q) * 256);
+          o[c] = __ldcg(os + static_cast<size_t>(q) * (2 * (D / 4) * 128));
+        }
       }
-    }
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const float m = fmaxf(mx, ls[c]);
-      // (each for itself: a NaN LSE has no part in m, but its weight is NaN)
-      const float old = mx == -INFINITY ? 0.f : ex2(mx - m), w = ls[c] == -INFINITY ? 0.f : ex2(ls[c] - m);
-      den = fmaf(den, old, w);
-      acc.x = fmaf(acc.x, old, w * o[c].x);
-      acc.y = fmaf(acc.y, old, w * o[c].y);
-      acc.z = fmaf(acc.z, old, w * o[c].z);
-      acc.w = fmaf(acc.w, old, w * o[c].w);
-      mx = m;
+      for (int c = 0; c < C; ++c) add(ls[c], o[c]);
+    }
+    if (sp == 0) {
+      add(ol, oo);
+#pragma unroll 1
+      for (int c = 1; c <= o1 - o0; ++c)
+        add(__ldcg(p.own_lse + own_at + static_cast<size_t>(c) * p.rows),
+            __ldcg(own_o + (own_at + static_cast<size_t>(c) * p.rows) * (D / 4)));
     }
   }
 #pragma unroll
-  for (int h = 8; h <= 16; h <<= 1) {
+  for (int h = CELLS; h < 32; h <<= 1) {
     const float om = __shfl_xor_sync(0xffffffffu, mx, h), od = __shfl_xor_sync(0xffffffffu, den, h);
     const float4 oa = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, h), __shfl_xor_sync(0xffffffffu, acc.y, h),
                                   __shfl_xor_sync(0xffffffffu, acc.z, h), __shfl_xor_sync(0xffffffffu, acc.w, h));
