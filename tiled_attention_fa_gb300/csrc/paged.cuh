@@ -693,7 +693,7 @@ __device__ __forceinline__ void paged_body(const CUtensorMap& tmQ, const CUtenso
     if (elect_one()) tc_commit(bar(Ly::B_DONE + 1));
     __syncwarp();
     mbar_wait_drain(bar(Ly::B_DONE + 1), 0);
-  } else {
+  } else if (warp < Ly::SW) {  // (the CTA may have more warps than roles)
     // ------------------------------------------------------------ softmax + epilogue
     const int gr = warp >> 2, wq = warp & 3;  // group, warp of the group (its TMEM lanes)
     const int t = threadIdx.x & 127;          // key of the tile; head dim of the epilogue

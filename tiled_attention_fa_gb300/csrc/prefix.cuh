@@ -102,7 +102,7 @@ constexpr int kPairWeight = 3, kOneWeight = 2;
 // Own keys that have CTAs of their own: a tile and an item in the same measure.
 constexpr float kOwnTileWeight = 1.5f, kOwnItemWeight = 1.5f;
 // Items of at most so many tiles in the mean are short.
-constexpr uint32_t kShortItem = 5;
+constexpr uint32_t kShortItem = 12;
 
 // An entry of the list: group e, or the own keys of sequence e - groups.
 struct PrefixEntry {
@@ -218,7 +218,7 @@ struct PrefixShare {
 
 // How the CTAs are shared out, and this one's part.  Called by the whole CTA (NT
 // threads).  A CTA of the prefixes' list finds the start of its walk in plan
-// {e, hkv, it, k, rem}.  OWN: own keys are not in the list and have CTAs of their
+// {e, hkv, it, k, rem} and its entry behind.  OWN: own keys are not in the list and have CTAs of their
 // own; plan[5] says whether their items are short.
 template <int NT, bool OWN>
 __device__ __forceinline__ PrefixShare prefix_plan(const PrefixParams& p, uint32_t* sums, int* plan) {
@@ -241,7 +241,7 @@ __device__ __forceinline__ PrefixShare prefix_plan(const PrefixParams& p, uint32
     }
   }
   uint32_t incl = mine;
-#pragma unroll 1
+#pragma unroll
   for (int h = 1; h < 32; h <<= 1) {
     const uint32_t o = __shfl_up_sync(0xffffffffu, incl, h);
     if (lane >= h) incl += o;
@@ -260,7 +260,7 @@ __device__ __forceinline__ PrefixShare prefix_plan(const PrefixParams& p, uint32
   pairs = __syncthreads_or(pairs);
   uint32_t at = incl - mine, total = 0;
   units = items = 0;
-#pragma unroll 1
+#pragma unroll
   for (int w = 0; w < W; ++w) {
     if (w < static_cast<int>(warp_id())) at += sums[w];
     total += sums[w];
@@ -298,6 +298,7 @@ __device__ __forceinline__ PrefixShare prefix_plan(const PrefixParams& p, uint32
         plan[2] = item - plan[1] * s.items;
         plan[3] = u - item * s.cnt;
         plan[4] = min(x1 - at - u * s.weight, 1u << 30);
+        *reinterpret_cast<PrefixEntry*>(plan + 8) = s;
         break;
       }
       at += here;
@@ -317,7 +318,7 @@ __device__ __forceinline__ PrefixWalk<OWN> prefix_walk(const PrefixParams& p, co
     w.hkv = plan[1];
     w.it = plan[2];
     w.k = plan[3];
-    w.s = prefix_entry(p, w.e);
+    w.s = *reinterpret_cast<const PrefixEntry*>(plan + 8);
     w.left = min(w.s.cnt - w.k, w.share());
   }
   return w;
@@ -794,8 +795,8 @@ struct PrefixShared {
   static constexpr uint32_t OWN_USED = PagedLayout<D, R == 0 ? 8 : R>::SMEM_USED;
   static constexpr uint32_t PREFIX_USED = PrefixLayout<D>::USED;
   static constexpr uint32_t OFF = R > 0 && OWN_USED > PREFIX_USED ? (OWN_USED + 15) / 16 * 16 : (PREFIX_USED + 15) / 16 * 16;
-  // plan [8], lens [32], sums [3][11], tmem slot, abort flag
-  static constexpr uint32_t PLAN = OFF, LENS = OFF + 32, SUMS = OFF + 160, SLOT = OFF + 336, FLAG = OFF + 340;
+  // plan [16], lens [32], sums [3][12], tmem slot, abort flag
+  static constexpr uint32_t PLAN = OFF, LENS = OFF + 64, SUMS = OFF + 192, SLOT = OFF + 336, FLAG = OFF + 340;
   static constexpr uint32_t ALLOC = OFF + 352 + 1024;
   static constexpr int NTHREADS = PrefixLayout<D>::NTHREADS;
   static_assert(ALLOC <= 232448, "shared memory");
