@@ -21,11 +21,10 @@ fa_status launch(RopeParams& p, bool neighbours, cudaStream_t s) {
     ++hs_log;
   p.hs_log = hs_log;
   const unsigned grid = static_cast<unsigned>((tokens + (ROWS >> hs_log) - 1) / (ROWS >> hs_log));
-  if (neighbours)
-    fa_rope_kernel<T, UN, true, APPEND><<<grid, 256, 0, s>>>(p);
-  else
-    fa_rope_kernel<T, UN, false, APPEND><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch_after(neighbours ? fa_rope_kernel<T, UN, true, APPEND> : fa_rope_kernel<T, UN, false, APPEND>,
+                      dim3(grid), dim3(256), s, p)
+             ? FA_OK
+             : FA_ERR_CUDA;
 }
 
 template <bool APPEND>

@@ -88,9 +88,8 @@ __device__ __forceinline__ void rope_turn(uint4& lo, uint4& hi, const float (&cs
 
 // UN = D / 16 units a head.
 template <typename T, int UN, bool NEIGHBOURS, bool APPEND>
-__global__ void __launch_bounds__(256) fa_rope_kernel(const RopeParams p) {
-  pdl_launch_dependents();
-  constexpr int ROWS = 256 / UN, C = 4;
+__global__ void __launch_bounds__(256, 4) fa_rope_kernel(const RopeParams p) {
+  constexpr int ROWS = 256 / UN, C = 2;
   const int u = threadIdx.x % UN, row = threadIdx.x / UN;
   const int HS = 1 << p.hs_log, hs = row & (HS - 1);
   const long long tokens = static_cast<long long>(p.B) * p.L;
@@ -100,6 +99,8 @@ __global__ void __launch_bounds__(256) fa_rope_kernel(const RopeParams p) {
   const int b = static_cast<int>(static_cast<unsigned>(tok) / static_cast<unsigned>(p.L));
   const int j = static_cast<int>(tok) - b * p.L;
 
+  pdl_launch_dependents();
+  pdl_wait();
   const uint4* qx = p.q.x + b * p.q.xb + j * p.q.xt;
   const uint4* kx = p.k.x + b * p.k.xb + j * p.k.xt;
   const uint4* vx = p.v.x + b * p.v.xb + j * p.v.xt;
