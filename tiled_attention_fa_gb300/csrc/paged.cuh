@@ -41,11 +41,15 @@
 // the dense forward.
 // Keys that no query sees (behind the length, before the window) may lie in
 // pages that were never written: their scores are replaced, not multiplied,
-// and their V rows are set to zero in shared memory before the PV product.
-// Measured (bf16, H32/8 D128): B16 16,384 keys 163 us, 6.58 TB/s (99% of the copy
-// rate; pages of 16 keys 174 us); B64 1,024 keys 49 us; B1 131,072 keys 92 us;
-// B1 500 keys 10.5 us, where launch, page ids, one tile and the join follow one
-// another; four tokens each of B8, window 4,096: 34 us (21 for the bytes alone).
+// and the warp that issues the PV products sets their V rows in shared memory to
+// zero before the first.
+// The roles' code together has to stay in the instruction cache: loops stay loops,
+// the waits are calls and each TMA load stands once.  (At 112 KB instead of 80 KB,
+// 256 sequences of 64 to 512 keys took 88 us, now 70.)
+// Measured (bf16, H32/8 D128): B16 16,384 keys 168 us, 6.4 TB/s (94% of the copy
+// rate; pages of 16 keys 175 us); B64 1,024 keys 47 us; B1 131,072 keys 90 us;
+// B1 500 keys 10.0 us, where launch, page ids, one tile and the join follow one
+// another; four tokens each of B8, window 4,096: 33 us (21 for the bytes alone).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -425,6 +429,10 @@ __device__ __forceinline__ void paged_join(const PagedParams& p, int b, int hkv,
   }
 }
 
+// Rows of a page a load brings at most behind a shared prefix, where items are short
+// and half a box is read in vain at each one's end.
+constexpr int kOwnBoxLog = 6;
+
 // The tiles' numbers among the groups: tile v is group v % NG's, its v / NG-th, and
 // has S buffer v % NB for the (v / NB)-th time.  In turn, the i-th tile of a part
 // is tile i; with whole items for a group, each group counts its own.
@@ -469,7 +477,8 @@ __device__ __forceinline__ void paged_body(const CUtensorMap& tmQ, const CUtenso
     // Ring order: the first NG K tiles, then K_{i+NG}, V_i.  Lane j loads the j-th box
     // (a page, or 128 rows of one) of the tile.
     const int page_log = 31 - __clz(p.page);  // (a page is a power of two)
-    const int box = min(p.page, 128), nbox = 128 >> min(page_log, 7), per_batch = 32 >> (7 - min(page_log, 7));
+    const int box_log = min(page_log, OWN ? kOwnBoxLog : 7), box = 1 << box_log, nbox = 128 >> box_log;
+    const int per_batch = 32 >> (7 - box_log);
     uint32_t stage = 0, phase = 0, used = 0, qcnt = 0;
     bool ok = true;
     const uint64_t stream = policy_evict_first();

@@ -52,18 +52,20 @@ PrefixPlan prefix_plan_of(const PrefixDecodeArgs& a) {
 }
 
 // K or V pool [pages, page, Hkv, D] with a free page stride, loaded as boxes of
-// 64 head-dim elements x min(page, 128) rows of one page and head.
+// 64 head-dim elements x min(page, 64) rows of one page and head.  The L2 fetches
+// what a head's row holds: 128 bytes at D = 64, where 256 would bring its
+// neighbour's row too, which another CTA reads at another time.
 bool make_pool_map(CUtensorMap* map, const void* ptr, int pages, int page, int Hkv, int D, long long page_stride,
                    bool bf16) {
   EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return false;
   cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)page, (cuuint64_t)pages};
   cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)Hkv * D * 2, (cuuint64_t)page_stride * 2};
-  cuuint32_t box[4] = {64, 1, (cuuint32_t)(page < 128 ? page : 128), 1};
+  cuuint32_t box[4] = {64, 1, (cuuint32_t)(page < 1 << kOwnBoxLog ? page : 1 << kOwnBoxLog), 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
             const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_SWIZZLE_128B, D == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

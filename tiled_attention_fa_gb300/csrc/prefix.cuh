@@ -10,30 +10,44 @@
 // Two launches: fa_prefix_kernel cuts both parts into chunks and leaves each
 // chunk's partial O and LSE in fp32; fa_prefix_join_kernel joins each row's.
 //
-// fa_prefix_kernel, a persistent CTA per SM.  A tile is up to 128 rows.  Of a
-// prefix: 128 / g tokens of the group (g query heads a K/V head), row = token * g
-// + head; an item is one K/V head of a group and two neighbouring tiles (the last
-// may have one).  Of own keys: an item is one sequence and K/V head, a tile of
-// Lq * g rows.  An item's units are its 128-key tiles.  The units of all items,
-// groups first, form one list, in which a unit weighs about what it takes, and
-// each CTA takes one of G equal parts of it, so all SMs work whatever the
-// lengths and groups are, and while some are bound by the products of the
-// prefixes others read own keys.  A part's share of an item is a chunk.  Chunks
-// are stored at item + part, which no two share: the next chunk in the list is of
-// a later item, a later part, or both.
+// fa_prefix_kernel, a persistent CTA per SM, of one of two kinds.
+//   Prefixes (prefix_body).  A tile is up to 128 rows: 128 / g tokens of a group (g
+//   query heads a K/V head), row = token * g + head.  An item is one K/V head of a
+//   group and two neighbouring tiles (the last may have one); its units are the
+//   prefix's 128-key tiles.  The units of all items form one list, in which a unit
+//   weighs about what it takes, and each CTA takes an equal part of it, so all work
+//   alike whatever the lengths and groups are.
+//   Own keys (paged_body, R > 0): the paged decode's roles, whose products are
+//   transposed and waste no rows on a sequence's few.  Sequences of more than 32
+//   rows (R = 0) fill a tile well enough: their items are in the prefixes' list, of
+//   one tile each.
+// How many CTAs are of each kind follows on the device from the lengths: the first
+// are bound by the products, the others by the read, so the two overlap on the
+// chip and one launch's start serves both.  A part's share of an item is a chunk.
+// Chunks are stored at item + part, which no two share: the next chunk in a list is
+// of a later item, a later part, or both; the join finds an item's first and last
+// part in a table.
+//
+// prefix_body:
 //   warps 0-3, 4-7  softmax, a thread per row.  Two tiles: one each.  One tile:
 //                   its even and its odd steps, each group with a maximum, a sum
 //                   and an O of its own; warps 4-7 join them at the chunk's end
-//                   while warps 0-3 begin the next.  Warps without a row wait.
+//                   while warps 0-3 begin the next
+//   warp 9          TMEM, MMAs: S_t = Q_t K_j^T, P over S as 16 bits, O_t += P V_j
 //   warp 10         TMA: Q, then K_0, V_0, K_1, V_1, ... through one ring across
 //                   chunks; lane i loads the i-th page of a tile
-//   warp 9          TMEM, MMAs: S_t = Q_t K_j^T, P over S as 16 bits, O_t += P V_j
-// Per 64 KB of K and V (D = 128) two tiles take 2,930 cycles of products and
-// exponentials that overlap; a CTA's share of the memory bandwidth brings 64 KB in
-// 2,790.  So up to 256 rows the read of the prefix bounds the kernel about as much
-// as the products, above it the products do and the other tiles' reads hit the L2.
-// Own keys are bound by their read: their tiles' empty rows cost the tensor cores
-// 1,024 cycles a unit, which the read hides.
+// Registers: 200 a softmax thread, 104 the others.  With fewer for the warp that
+// issues the products its descriptors are spilled, and a unit of two tiles took
+// 4,400 cycles instead of 2,950.
+// What bounds it: per 64 KB of K and V (D = 128) two tiles take 2,950 cycles, of
+// which the tensor cores work 2,200 (each tile's chain S, softmax, PV, S is in the
+// way, as in the dense forward); a CTA's share of the memory bandwidth brings 64 KB
+// in 2,790.  A launch's first 8 us go until all SMs stream (code, lengths, page ids,
+// the first tiles), its last 5 to the join.
+// Measured (bf16, H32/8 D128): 64 sequences of 100 to 1,000 own keys behind 32,768:
+// 66 us (the paged decode over tables that repeat the prefix reads it 64 times from
+// the L2); 256 of 64 to 512 behind 16,384: 100 us; 8 of 1 to 100 behind 2,001: 15.5
+// us; 8 of 1 key behind 32,768 38 us.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -65,8 +79,8 @@ struct PrefixParams {
   float sl2;                  // log2(e) / sqrt(D)
 };
 
-// mbar_wait_warp that reads the timer only once 32 polls have failed: most waits
-// here are short, and the read takes longer than they do.
+// mbar_wait_warp in less code, inlined: a call, as the paged decode's waits are,
+// does not go with the register split (its callee could not be allocated).
 __device__ __forceinline__ bool prefix_wait(uint32_t bar, uint32_t parity, AbortState* ab, unsigned int* err,
                                             unsigned int site) {
   bool ok = false;
@@ -96,12 +110,15 @@ __device__ __forceinline__ void prefix_arrive(uint32_t bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
 
-// What a unit weighs: of two tiles, of one.  (Two tiles are bound by the products,
-// one by the read, which gets more than its share while others compute.)
+// What a unit weighs, in thousands of cycles: of two tiles, of one (which the read
+// bounds, and that gets more than its share while others compute).
 constexpr int kPairWeight = 3, kOneWeight = 2;
-// Own keys that have CTAs of their own: a tile and an item in the same measure.
+// Own keys that have CTAs of their own: a tile and an item.  (The two cases above:
+// 101 and 67 us; with 1 and 1 107 and 74, with 2 and 2 102 and 70.)
 constexpr float kOwnTileWeight = 1.5f, kOwnItemWeight = 1.5f;
-// Items of at most so many tiles in the mean are short.
+// Own items of at most so many tiles in the mean go whole to a softmax group each,
+// in turn (100 to 2,000 keys: 55.7 us, with their tiles in turn 59.8; 24 tiles: no
+// difference).
 constexpr uint32_t kShortItem = 12;
 
 // An entry of the list: group e, or the own keys of sequence e - groups.
@@ -343,7 +360,8 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tmQ, const CUtens
     // ------------------------------------------------------------ producer
     setmaxnreg_dec<Ly::REGS_OTHER>();
     const int page_log = 31 - __clz(p.page);  // (a page is a power of two)
-    const int box = min(p.page, 128), nbox = 128 >> min(page_log, 7), per_batch = 32 >> (7 - min(page_log, 7));
+    const int box_log = min(page_log, kOwnBoxLog), box = 1 << box_log, nbox = 128 >> box_log;
+    const int per_batch = 32 >> (7 - box_log);
     uint32_t stage = 0, phase = 0, used = 0, slot = 0;
     uint32_t q_used = 0, q_odd = 0;  // bit t: slot t was filled; an odd number of times
     bool ok = true;
