@@ -277,8 +277,11 @@ fa_status fa_paged_append(const void* Q, long long q_batch, long long q_token, c
  * Results do not depend on timing.  `workspace`:
  * fa_paged_prefix_decode_workspace_size bytes, asked with the device that runs
  * the call current (FA_ERR_SCRATCH_TOO_SMALL when smaller), under
- * fa_paged_decode's rules; a part of it holds 128 x D floats for every tile of
- * 128 / (H / Hkv) tokens, group and K/V head and every SM.
+ * fa_paged_decode's rules; its largest part holds 256 x D floats for every SM and
+ * for every K/V head and two tiles of 128 / (H / Hkv) tokens, a group's tiles
+ * counted apart.  FA_ERR_UNSUPPORTED where three times the 128-key tiles of all
+ * prefixes (at their tables' lengths, for each K/V head and two tiles of tokens)
+ * and twice those of all own keys could add up to 2^32 or more.
  */
 size_t fa_paged_prefix_decode_workspace_size(int B, int Lq, int H, int Hkv, int D, int page,
                                              int groups, int prefix_pages, int max_pages);

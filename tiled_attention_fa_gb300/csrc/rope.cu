@@ -12,8 +12,9 @@ fa_status launch(RopeParams& p, bool neighbours, cudaStream_t s) {
   constexpr int ROWS = 256 / UN;
   const int all = p.H + (APPEND ? 2 : 1) * p.Hkv;
   const long long tokens = static_cast<long long>(p.B) * p.L;
-  // Threads that share a token's unit: as few as leave each at most 12 heads (the
-  // angles cost about as much as turning 3), more while the GPU is not full.
+  // Threads that share a token's unit: as few as leave each at most 12 heads (B4
+  // L4096 H32/8 D128 both directions 108 us, with at most 6 heads 116), more while
+  // the GPU is not full.
   const long long full = 1024ll * sm_count();
   int hs_log = 0;
   while ((2 << hs_log) <= ROWS && (1 << hs_log) < all &&
