@@ -74,7 +74,7 @@ def _link_binding(obj: str) -> None:
     tmp = BINDING_PATH + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L" + HERE, "-l:" + LIB_NAME,
            "-Wl,-rpath,$ORIGIN", "-L" + lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu",
-           "-lc10", "-lc10_cuda"]
+           "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link of the binding failed:\n" + r.stdout + r.stderr)

@@ -11,6 +11,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -68,17 +69,20 @@ const Tensor& wanted(PyObject* o, const char* name, at::IntArrayRef shape, at::S
   return t;
 }
 
+// A new tensor, without the dispatcher's part of at::empty.
+Tensor fresh(at::IntArrayRef shape, at::ScalarType dt, int dev) {
+  return at::detail::empty_cuda(shape, dt, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt);
+}
+
 // The tensor given, checked, or a new one.
-Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType dt, int dev,
-              const Tensor& like) {
-  if (o == Py_None) return at::empty(shape, like.options().dtype(dt));
+Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType dt, int dev) {
+  if (o == Py_None) return fresh(shape, dt, dev);
   return wanted(o, name, shape, dt, dev);
 }
 
 // A workspace given, or a new one of n bytes.
-Tensor workspace(PyObject* o, size_t n, int dev, const Tensor& like) {
-  if (o == Py_None)
-    return at::empty({static_cast<int64_t>(n < 16 ? 16 : n)}, like.options().dtype(at::kByte));
+Tensor workspace(PyObject* o, size_t n, int dev) {
+  if (o == Py_None) return fresh({static_cast<int64_t>(n < 16 ? 16 : n)}, at::kByte, dev);
   const Tensor& t = tensor(o, "workspace");
   want(t, "workspace", t.sizes(), t.scalar_type(), dev);
   return t;
@@ -225,8 +229,8 @@ PyObject* window_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor& v = wanted(a[2], "v", kv, dt, dev);
   const int window = number(a[3], "window"), sinks = number(a[4], "sinks");
   const Stream stream(a[7], dev);
-  const Tensor out = output(a[5], "out", q.sizes(), dt, dev, q);
-  const Tensor lse = output(a[6], "lse", ls, kF32, dev, q);
+  const Tensor out = output(a[5], "out", q.sizes(), dt, dev);
+  const Tensor lse = output(a[6], "lse", ls, kF32, dev);
   const fa_status st =
       fa_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr<float>(),
                     small(s.a), small(s.b), small(c.b), small(s.c), small(c.c), small(s.d), window,
@@ -258,13 +262,13 @@ PyObject* window_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const bool prep = a[3] != Py_None, zeroed = a[12] != Py_None && truth(a[13]);
   const Stream stream(a[14], dev);
   if (prep) wanted(a[3], "o", q.sizes(), dt, dev);
-  const Tensor delta = output(a[6], "delta", ls, kF32, dev, q);
+  const Tensor delta = output(a[6], "delta", ls, kF32, dev);
   if (!prep && a[6] == Py_None) fail(PyExc_TypeError, "delta must be a CUDA tensor");
-  const Tensor dq = output(a[9], "dq", q.sizes(), dt, dev, q);
-  const Tensor dk = output(a[10], "dk", kv, dt, dev, q);
-  const Tensor dv = output(a[11], "dv", kv, dt, dev, q);
+  const Tensor dq = output(a[9], "dq", q.sizes(), dt, dev);
+  const Tensor dk = output(a[10], "dk", kv, dt, dev);
+  const Tensor dv = output(a[11], "dv", kv, dt, dev);
   const size_t need = fa_window_bwd_workspace_size(B, L, Lk, H, Hkv, D, window, sinks);  // 0: refused below
-  const Tensor ws = workspace(a[12], need, dev, q);
+  const Tensor ws = workspace(a[12], need, dev);
   const size_t bytes = ws.numel() * ws.element_size();
   if (bytes < need) return status(FA_ERR_SCRATCH_TOO_SMALL);
   fa_status st = FA_OK;
@@ -334,10 +338,10 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int B = small(s.a), Lq = small(s.b), H = small(s.c), Hkv = small(p.hkv), D = small(p.d),
             page = small(p.page);
   const Stream stream(a[11], dev);
-  const Tensor out = output(a[8], "out", qs, dt, dev, q);
-  const Tensor lse = output(a[9], "lse", ls, kF32, dev, q);
+  const Tensor out = output(a[8], "out", qs, dt, dev);
+  const Tensor lse = output(a[9], "lse", ls, kF32, dev);
   const Tensor ws = workspace(
-      a[10], fa_paged_decode_workspace_size(B, Lq, H, Hkv, D, page, small(P), w != nullptr), dev, q);
+      a[10], fa_paged_decode_workspace_size(B, Lq, H, Hkv, D, page, small(P), w != nullptr), dev);
   const fa_status st = fa_paged_decode(
       q.data_ptr(), p.k.data_ptr(), p.v.data_ptr(), p.kst, p.vst, ints(table), ints(lens),
       out.data_ptr(), lse.data_ptr<float>(), w, wst, ws.data_ptr(), ws.numel() * ws.element_size(), B,
@@ -409,11 +413,11 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Angles g = angles(a[2], a[3], s.a, s.b, dev);
   const int interleaved = truth(a[4]) ? 1 : 0, backward = truth(a[5]) ? 1 : 0;
   const Stream stream(a[8], dev);
-  const Tensor out = a[6] == Py_None ? at::empty(q.sizes(), q.options()) : tensor(a[6], "out_q");
+  const Tensor out = a[6] == Py_None ? fresh(q.sizes(), dt, dev) : tensor(a[6], "out_q");
   const View qo = view(out, "out_q", q.sizes(), dt, dev);
   Tensor out_k;
   if (a[1] != Py_None) {
-    out_k = a[7] == Py_None ? at::empty(ks, q.options()) : tensor(a[7], "out_k");
+    out_k = a[7] == Py_None ? fresh(ks, dt, dev) : tensor(a[7], "out_k");
     ko = view(out_k, "out_k", ks, dt, dev);
   } else if (a[7] != Py_None) {
     fail(PyExc_ValueError, "out_k without k");
@@ -459,7 +463,7 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const float* nw =
       a[12] == Py_None ? nullptr : wanted(a[12], "new_weights", ns, kF32, dev).data_ptr<float>();
   const Stream stream(a[14], dev);
-  const Tensor out = a[13] == Py_None ? at::empty(qs, q.options()) : tensor(a[13], "out");
+  const Tensor out = a[13] == Py_None ? fresh(qs, dt, dev) : tensor(a[13], "out");
   const View qo = view(out, "out", qs, dt, dev);
   const fa_status st = fa_paged_append(
       qv.p, qv.batch, qv.token, kv.p, kv.batch, kv.token, vv.p, vv.batch, vv.token, qo.p, qo.batch, qo.token,
@@ -499,10 +503,10 @@ PyObject* paged_prefix_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int B = small(s.a), Lq = small(s.b), H = small(s.c), Hkv = small(p.hkv), D = small(p.d),
             page = small(p.page), G = small(groups);
   const Stream stream(a[11], dev);
-  const Tensor out = output(a[8], "out", qs, dt, dev, q);
-  const Tensor lse = output(a[9], "lse", ls, kF32, dev, q);
+  const Tensor out = output(a[8], "out", qs, dt, dev);
+  const Tensor lse = output(a[9], "lse", ls, kF32, dev);
   const Tensor ws = workspace(
-      a[10], fa_paged_prefix_decode_workspace_size(B, Lq, H, Hkv, D, page, G, small(PP), small(P)), dev, q);
+      a[10], fa_paged_prefix_decode_workspace_size(B, Lq, H, Hkv, D, page, G, small(PP), small(P)), dev);
   const fa_status st = fa_paged_prefix_decode(
       q.data_ptr(), p.k.data_ptr(), p.v.data_ptr(), p.kst, p.vst, ints(ptable), ints(plens), starts, ints(table),
       ints(lens), out.data_ptr(), lse.data_ptr<float>(), ws.data_ptr(), ws.numel() * ws.element_size(), B, Lq, H, Hkv,
@@ -532,9 +536,9 @@ PyObject* paged_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (keep < 1) fail(PyExc_ValueError, "keep must be at least 1");
   const int64_t ks[3] = {B, p.hkv, keep}, ns[3] = {B, p.hkv, P2 * p.page};
   const Stream stream(a[12], dev);
-  const Tensor kept = output(a[9], "kept", ks, kI32, dev, k);
-  const Tensor new_lens = output(a[10], "new_lens", bs, kI32, dev, k);
-  const Tensor new_w = output(a[11], "new_weights", ns, kF32, dev, k);
+  const Tensor kept = output(a[9], "kept", ks, kI32, dev);
+  const Tensor new_lens = output(a[10], "new_lens", bs, kI32, dev);
+  const Tensor new_w = output(a[11], "new_weights", ns, kF32, dev);
   const fa_status st = fa_paged_evict(
       p.k.data_ptr(), p.v.data_ptr(), p.kst, p.vst, ints(table), ints(lens), w, wst, ints(dst), keep,
       sinks, recent, kept.data_ptr<int>(), new_lens.data_ptr<int>(), new_w.data_ptr<float>(), small(B),
@@ -560,8 +564,8 @@ PyObject* key_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int causal = truth(a[3]) ? 1 : 0;
   const int window = number(a[4], "window"), sinks = number(a[5], "sinks");
   const Stream stream(a[8], dev);
-  const Tensor out = output(a[6], "out", os, kF32, dev, q);
-  const Tensor ws = workspace(a[7], fa_key_weights_workspace_size(), dev, q);
+  const Tensor out = output(a[6], "out", os, kF32, dev);
+  const Tensor ws = workspace(a[7], fa_key_weights_workspace_size(), dev);
   const fa_status st = fa_key_weights(
       q.data_ptr(), k.data_ptr(), lse.data_ptr<float>(), out.data_ptr<float>(), ws.data_ptr(),
       ws.numel() * ws.element_size(), small(s.a), small(s.b), small(c.b), small(s.c), small(c.c),

@@ -903,9 +903,9 @@ struct PrefixJoinParams {
 // SP threads join 4 dims of one row, each every SP-th of the prefix's partials; the
 // lanes run over the g heads of a K/V head, whose rows lie together in a prefix's
 // partial, then over the dims.  Block (x, y): token and K/V head x, the 128 / SP
-// cells from y * 128 / SP on.  Bound by latency: three loads that depend on one
-// another (lengths, an item's parts, the partials), so what does not depend goes
-// out together, and SP is 1 where a row has few partials.
+// cells from y * 128 / SP on.  Bound by latency: two loads that depend on one
+// another (an item's parts, the partials) behind fa_prefix_kernel's end, so what does
+// not depend goes out together, and SP is 1 where a row has few partials.
 template <int D, bool BF16, int SP>
 __global__ void __launch_bounds__(128) fa_prefix_join_kernel(const PrefixJoinParams a) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
@@ -919,10 +919,10 @@ __global__ void __launch_bounds__(128) fa_prefix_join_kernel(const PrefixJoinPar
   const int d4 = cell / p.g, hg = cell - d4 * p.g;
   const bool in = d4 < D / 4;
   pdl_launch_dependents();
-  pdl_wait();
+  // Lengths and starts are from before fa_prefix_kernel, which begins when all before
+  // it is done: they are read while it runs.
   const int own_n = min(max(p.lens[b], 0), p.cap);
   const int own_item = b * p.Hkv + hkv;
-  const int2 oe = __ldcg(reinterpret_cast<const int2*>(p.ends) + p.items + own_item);
   // The sequence's group.
   int grp = 0;
   if (p.groups > 1) {
@@ -937,6 +937,8 @@ __global__ void __launch_bounds__(128) fa_prefix_join_kernel(const PrefixJoinPar
   }
   const PrefixEntry s = prefix_entry(p, grp);
   const bool pad = own_n - p.Lq + ql < 0;
+  pdl_wait();
+  const int2 oe = __ldcg(reinterpret_cast<const int2*>(p.ends) + p.items + own_item);
   float mx = -INFINITY, den = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   auto add = [&](float lse, const float4& o) {
