@@ -32,7 +32,7 @@ PrefixPlan prefix_plan_of(const PrefixDecodeArgs& a) {
   w.own = static_cast<long long>(a.B) * a.Hkv;
   const long long prefix_units = w.items * ((static_cast<long long>(a.prefix_pages) * a.page + 127) / 128);
   const long long own_units = w.own * ((static_cast<long long>(a.max_pages) * a.page + 127) / 128);
-  w.most = prefix_units * kPairWeight + own_units * kOneWeight;
+  w.most = prefix_units * prefix_pair_weight(a.D) + own_units * kOneWeight;
   // (two at least: prefixes and own keys may have CTAs of their own)
   w.G = prefix_units + own_units < sms ? static_cast<int>(prefix_units + own_units) : sms;
   if (w.G < 2) w.G = 2;
@@ -173,6 +173,8 @@ fa_status pick_rows(const PrefixDecodeArgs& a, const PrefixPlan& w, cudaStream_t
   p.pcap = a.prefix_pages * a.page;
   p.cap = a.max_pages * a.page;
   p.sl2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
+  p.pair_weight = prefix_pair_weight(a.D);
+  p.own_weight = prefix_own_weight(a.D);
   j.O = a.O;
   j.LSE = a.LSE;
   j.G = w.G;

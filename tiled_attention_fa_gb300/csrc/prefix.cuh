@@ -77,6 +77,8 @@ struct PrefixParams {
   int ginv;                   // 65536 / g + 1: row / g = row * ginv >> 16
   int page, prefix_pages, max_pages, pcap, cap;  // caps: pages * page
   float sl2;                  // log2(e) / sqrt(D)
+  int pair_weight;            // of a unit of two tiles
+  float own_weight;           // of own keys in CTAs of their own
 };
 
 // mbar_wait_warp in less code, inlined: a call, as the paged decode's waits are,
@@ -110,12 +112,15 @@ __device__ __forceinline__ void prefix_arrive(uint32_t bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
 
-// What a unit weighs, in thousands of cycles: of two tiles, of one (which the read
-// bounds, and that gets more than its share while others compute).
-constexpr int kPairWeight = 3, kOneWeight = 2;
-// Own keys that have CTAs of their own: a tile and an item.  (The two cases above:
-// 101 and 67 us; with 1 and 1 107 and 74, with 2 and 2 102 and 70.)
-constexpr float kOwnTileWeight = 1.5f, kOwnItemWeight = 1.5f;
+// What a unit weighs: of one tile, and of two; and in the same measure the own keys
+// that have CTAs of their own, a tile and as much again an item.  At D = 128 a unit of
+// one tile is bound by the read and gets more than its share while others compute: own
+// keys 1.5 (256 sequences behind 16,384 keys 98 us, behind 32,768 65; with 1.3 103 and
+// 68, with 1.75 106 and 67).  At D = 64 one tile takes 1,300 cycles, two 2,700, an own
+// tile and an item 1,300 to 1,400 each (five groups 39 us; with 3, 2 and 1.5 43).
+constexpr int kOneWeight = 2;
+constexpr int prefix_pair_weight(int D) { return D == 64 ? 4 : 3; }
+constexpr float prefix_own_weight(int D) { return D == 64 ? 2.f : 1.5f; }
 // Own items of at most so many tiles in the mean go whole to a softmax group each,
 // in turn (100 to 2,000 keys: 55.7 us, with their tiles in turn 59.8; 24 tiles: no
 // difference).
@@ -143,7 +148,7 @@ __device__ __forceinline__ PrefixEntry prefix_entry(const PrefixParams& p, int e
     s.t1 = b1 * p.Lq;
     s.cnt = (s.n + 127) >> 7;
     s.items = s.cnt > 0 ? (s.t1 - s.t0 + 2 * p.tok - 1) / (2 * p.tok) : 0;
-    s.weight = s.t1 - s.t0 > p.tok ? kPairWeight : kOneWeight;
+    s.weight = s.t1 - s.t0 > p.tok ? p.pair_weight : kOneWeight;
   } else {
     s.n = min(max(p.lens[e - p.groups], 0), p.cap);
     s.t0 = s.t1 = 0;
@@ -169,7 +174,7 @@ struct PrefixWalk {
   PrefixEntry s;
 
   __device__ __forceinline__ int share() const {
-    return s.weight == kPairWeight ? rem / kPairWeight : rem / kOneWeight;
+    return s.weight == kOneWeight ? rem / kOneWeight : rem / s.weight;
   }
   __device__ __forceinline__ void next(const PrefixParams& p) {
     const bool ended = k + left < s.cnt;  // inside an item: the part's border
@@ -253,7 +258,7 @@ __device__ __forceinline__ PrefixShare prefix_plan(const PrefixParams& p, uint32
       units += n * s.cnt;
       items += n;
     } else {
-      pairs |= s.items > 0 && s.weight == kPairWeight;
+      pairs |= s.items > 0 && s.weight != kOneWeight;
       mine += n * s.cnt * s.weight;
     }
   }
@@ -289,7 +294,7 @@ __device__ __forceinline__ PrefixShare prefix_plan(const PrefixParams& p, uint32
   const int CTAs = gridDim.x;
   int G = CTAs;
   if (OWN) {
-    const float w = static_cast<float>(units) * kOwnTileWeight + static_cast<float>(items) * kOwnItemWeight;
+    const float w = (static_cast<float>(units) + static_cast<float>(items)) * p.own_weight;
     if (items > 0)
       G = total > 0 ? min(max(static_cast<int>(CTAs * (total / (total + w))), 1), CTAs - 1) : 0;
     if (threadIdx.x == 0) plan[5] = units <= kShortItem * items;
@@ -299,7 +304,7 @@ __device__ __forceinline__ PrefixShare prefix_plan(const PrefixParams& p, uint32
   // Part c is [x0, x1); a unit that a border lies in is the next part's.  No part
   // may be shorter than the longest unit, so that none between two parts of an item
   // is without one; CTAs beyond that many parts have none.
-  const uint32_t room = total / (pairs ? kPairWeight : kOneWeight);
+  const uint32_t room = total / (pairs ? p.pair_weight : kOneWeight);
   const uint32_t n = room < static_cast<uint32_t>(G) ? max(room, 1u) : max(G, 1);
   const uint32_t q = total / n, rest = total - q * n, c = r.own ? n : r.c;
   const uint32_t x0 = c * q + min(c, rest), x1 = x0 + q + (c < rest ? 1 : 0);
@@ -323,6 +328,94 @@ __device__ __forceinline__ PrefixShare prefix_plan(const PrefixParams& p, uint32
   }
   __syncthreads();
   return r;
+}
+
+// Part c of G of the own keys' tiles, for a CTA of their own: its walk in plan {b, hkv,
+// k, tiles}.  An item weighs a tile more than it has (its Q, and its end), before its
+// first: tile k begins at k + 1, the first at 0.  No part is narrower than 2, so that
+// none inside an item is without a tile.  Called by the whole CTA (NT threads).
+template <int NT>
+__device__ __forceinline__ void prefix_own_plan(const PagedOwnParams& p, int c, int G, uint32_t* sums, int* plan) {
+  const int lane = lane_id(), per = (p.B + NT - 1) / NT;
+  const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
+  uint32_t tiles = 0, items = 0;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const int cnt = paged_seq_of(p.lens[b], p).cnt;
+    tiles += cnt * p.Hkv;
+    items += cnt > 0 ? p.Hkv : 0;
+  }
+  uint32_t t_at = tiles, i_at = items;
+#pragma unroll
+  for (int h = 1; h < 32; h <<= 1) {
+    const uint32_t a = __shfl_up_sync(0xffffffffu, t_at, h), b = __shfl_up_sync(0xffffffffu, i_at, h);
+    if (lane >= h) {
+      t_at += a;
+      i_at += b;
+    }
+  }
+  constexpr int W = NT / 32;
+  if (lane == 31) {
+    sums[warp_id()] = t_at;
+    sums[W + warp_id()] = i_at;
+  }
+  __syncthreads();
+  t_at -= tiles;
+  i_at -= items;
+  uint32_t all_tiles = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w < static_cast<int>(warp_id())) {
+      t_at += sums[w];
+      i_at += sums[W + w];
+    }
+    all_tiles += sums[w];
+    total += sums[w] + sums[W + w];
+  }
+  const uint32_t n = min(static_cast<uint32_t>(G), max(total / 2, 1u));
+  const uint32_t q = total / n, rest = total - q * n;
+  // The part's first tile, and the next part's: the first at or behind a border.
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t part = c + i, x = part < n ? part * q + min(part, rest) : total;
+    if (x >= total) {
+      if (threadIdx.x == 0) plan[4 + i] = all_tiles;
+      continue;
+    }
+    uint32_t ta = t_at, at = t_at + i_at;
+    if (x - at >= tiles + items) continue;  // (in another thread's sequences)
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      const uint32_t cnt = paged_seq_of(p.lens[b], p).cnt;
+      const uint32_t all = cnt > 0 ? (cnt + 1) * p.Hkv : 0;
+      if (x - at < all) {
+        const uint32_t item = (x - at) / (cnt + 1), r = x - at - item * (cnt + 1);
+        const uint32_t k = r == 0 ? 0 : max(r - 1, 1u);  // (cnt: the next item's first)
+        plan[4 + i] = ta + item * cnt + k;
+        break;
+      }
+      at += all;
+      ta += cnt * p.Hkv;
+    }
+  }
+  __syncthreads();
+  const uint32_t first = plan[4], last = plan[5];
+  if (threadIdx.x == 0) plan[3] = last - first;
+  if (first < last && first - t_at < tiles) {
+    uint32_t ta = t_at;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      const uint32_t cnt = paged_seq_of(p.lens[b], p).cnt;
+      if (first - ta < cnt * p.Hkv) {
+        plan[0] = b;
+        plan[1] = (first - ta) / cnt;
+        plan[2] = (first - ta) % cnt;
+        break;
+      }
+      ta += cnt * p.Hkv;
+    }
+  }
+  __syncthreads();
 }
 
 template <bool OWN>
@@ -878,7 +971,7 @@ __global__ void __launch_bounds__(384, 1)
     const int len = (o.B <= 32 && static_cast<int>(lane) < o.B) ? o.lens[lane] : 0;
     if (warp == 0) lens_s[lane] = len;
     __syncthreads();  // (plan is read, and written again)
-    paged_plan<NT>(o, mine.c, mine.G, len, reinterpret_cast<int*>(sums), plan);
+    prefix_own_plan<NT>(o, mine.c, mine.G, sums, plan);
     paged_body<D, BF16, R>(tmOwnQ, tmK, tmV, o, gbase, base, tmem, ab, plan, o.B <= 32 ? lens_s : o.lens, mine.c, mine.G,
                                  brief);
   }
