@@ -33,9 +33,9 @@ PrefixPlan prefix_plan_of(const PrefixDecodeArgs& a) {
   const long long prefix_units = w.items * ((static_cast<long long>(a.prefix_pages) * a.page + 127) / 128);
   const long long own_units = w.own * ((static_cast<long long>(a.max_pages) * a.page + 127) / 128);
   w.most = prefix_units * prefix_pair_weight(a.D) + own_units * kOneWeight;
-  // (two at least: prefixes and own keys may have CTAs of their own)
+  // (in pairs: prefixes and own keys may have CTAs of their own)
   w.G = prefix_units + own_units < sms ? static_cast<int>(prefix_units + own_units) : sms;
-  if (w.G < 2) w.G = 2;
+  w.G = w.G < 2 ? 2 : (w.G + 1) / 2 * 2;
   size_t at = 0;
   w.part_o = at;
   at += static_cast<size_t>(w.items + w.G) * 256 * a.D * sizeof(float);
@@ -126,12 +126,11 @@ fa_status launch_prefix(const PrefixDecodeArgs& a, const PrefixPlan& w, PrefixJo
     if (cudaFuncGetAttributes(&at, kern) == cudaSuccess) num_regs = at.numRegs;
   });
   if (num_regs != PrefixLayout<D>::REGS) return FA_ERR_UNSUPPORTED;
-  // Launched when all before is done, not before: CTAs then lie in order, neighbours
-  // on the two SMs that share an instruction cache, and have the same role.  Placed
-  // one by one as SMs fall free, 256 sequences behind 16,384 keys took 142 us
-  // instead of 105.
-  kern<<<w.G, Sh::NTHREADS, Sh::ALLOC, s>>>(tq, to, tk, tv, p, o);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  // Clusters of two, which lie on the two SMs that seem to share an instruction cache,
+  // and have the same role.  Placed one by one as SMs fall free, 256 sequences behind
+  // 16,384 keys took 123 us instead of 97; launched when all before is done, the CTAs
+  // lie in order by themselves, but a call starts 2 to 3 us later.
+  if (!launch_pairs_after(kern, dim3(w.G), dim3(Sh::NTHREADS), Sh::ALLOC, s, tq, to, tk, tv, p, o)) return FA_ERR_CUDA;
   // Parts of a prefix's item in the mean: with more than 8, four threads share them.
   const int cells = p.g * (D / 4), sp = w.G > 8 * w.items ? 4 : 1;
   const dim3 grid(static_cast<unsigned>(a.B) * a.Lq * a.Hkv, (cells * sp + 127) / 128);

@@ -140,17 +140,17 @@ __device__ __forceinline__ PrefixEntry prefix_entry(const PrefixParams& p, int e
   if (e < p.groups) {
     int b0 = 0, b1 = p.B;
     if (p.starts != nullptr) {
-      b0 = min(max(p.starts[e], 0), p.B);
-      b1 = min(max(p.starts[e + 1], b0), p.B);
+      b0 = min(max(__ldcg(p.starts + e), 0), p.B);
+      b1 = min(max(__ldcg(p.starts + e + 1), b0), p.B);
     }
-    s.n = min(max(p.plens[e], 0), p.pcap);
+    s.n = min(max(__ldcg(p.plens + e), 0), p.pcap);
     s.t0 = b0 * p.Lq;
     s.t1 = b1 * p.Lq;
     s.cnt = (s.n + 127) >> 7;
     s.items = s.cnt > 0 ? (s.t1 - s.t0 + 2 * p.tok - 1) / (2 * p.tok) : 0;
     s.weight = s.t1 - s.t0 > p.tok ? p.pair_weight : kOneWeight;
   } else {
-    s.n = min(max(p.lens[e - p.groups], 0), p.cap);
+    s.n = min(max(__ldcg(p.lens + e - p.groups), 0), p.cap);
     s.t0 = s.t1 = 0;
     s.cnt = (s.n + 127) >> 7;
     s.items = s.cnt > 0 ? 1 : 0;
@@ -297,6 +297,8 @@ __device__ __forceinline__ PrefixShare prefix_plan(const PrefixParams& p, uint32
     const float w = (static_cast<float>(units) + static_cast<float>(items)) * p.own_weight;
     if (items > 0)
       G = total > 0 ? min(max(static_cast<int>(CTAs * (total / (total + w))), 1), CTAs - 1) : 0;
+    // (both CTAs of a cluster alike)
+    if (items > 0 && total > 0 && CTAs > 2) G = min((G + 1) & ~1, CTAs - 2);
     if (threadIdx.x == 0) plan[5] = units <= kShortItem * items;
   }
   const PrefixShare r = {static_cast<int>(blockIdx.x) >= G, static_cast<int>(blockIdx.x) - (static_cast<int>(blockIdx.x) >= G ? G : 0),
@@ -944,8 +946,8 @@ __global__ void __launch_bounds__(384, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();  // (now: what runs behind it may read what was there before this kernel)
   const PrefixShare mine = prefix_plan<NT, R != 0>(p, sums, plan);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -1012,9 +1014,9 @@ __global__ void __launch_bounds__(128) fa_prefix_join_kernel(const PrefixJoinPar
   const int d4 = cell / p.g, hg = cell - d4 * p.g;
   const bool in = d4 < D / 4;
   pdl_launch_dependents();
-  // Lengths and starts are from before fa_prefix_kernel, which begins when all before
-  // it is done: they are read while it runs.
-  const int own_n = min(max(p.lens[b], 0), p.cap);
+  // Lengths and starts are from before fa_prefix_kernel, whose CTAs let this one begin
+  // once all before it is done: they are read while it runs.
+  const int own_n = min(max(__ldcg(p.lens + b), 0), p.cap);
   const int own_item = b * p.Hkv + hkv;
   // The sequence's group.
   int grp = 0;
@@ -1023,7 +1025,7 @@ __global__ void __launch_bounds__(128) fa_prefix_join_kernel(const PrefixJoinPar
 #pragma unroll 1
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (p.starts[mid] <= b) lo = mid;
+      if (__ldcg(p.starts + mid) <= b) lo = mid;
       else hi = mid;
     }
     grp = lo;
