@@ -42,12 +42,13 @@
 // What bounds it: per 64 KB of K and V (D = 128) two tiles take 2,950 cycles, of
 // which the tensor cores work 2,200 (each tile's chain S, softmax, PV, S is in the
 // way, as in the dense forward); a CTA's share of the memory bandwidth brings 64 KB
-// in 2,790.  A launch's first 8 us go until all SMs stream (code, lengths, page ids,
-// the first tiles), its last 5 to the join.
-// Measured (bf16, H32/8 D128): 64 sequences of 100 to 1,000 own keys behind 32,768:
-// 66 us (the paged decode over tables that repeat the prefix reads it 64 times from
-// the L2); 256 of 64 to 512 behind 16,384: 100 us; 8 of 1 to 100 behind 2,001: 15.5
-// us; 8 of 1 key behind 32,768 38 us.
+// in 2,790.  A launch's first 5 us go until the first scores are there (2 to the plan:
+// code, lengths; then page ids, the first tiles), its last 5 to the join.
+// Measured (H32/8 D128): 64 sequences of 100 to 1,000 own keys behind 32,768: 60 us
+// (the paged decode over tables that repeat the prefix reads it 64 times from the L2);
+// 256 of 64 to 512 behind 16,384: 97 us; 20 of four tokens, 50 to 800 behind 6,001: 32
+// us; 8 of 1 to 100 behind 2,001: 15 us.  H16/16 D64: 40 of 16 to 500 in five groups
+// behind 1,000 to 9,000: 39 us.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -464,6 +465,9 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tmQ, const CUtens
 #pragma unroll 1
     for (auto w = prefix_walk<OWN>(p, plan); ok && w.left > 0; w.next(p)) {
       const bool own = w.own(p), pair = w.pair(p);
+      // What one item alone reads leaves the L2 first (64 sequences behind 32,768 keys 59
+      // us, kept like other data 64; four items of 256 sequences 103, kept 96).
+      const uint64_t policy = own || w.s.items == 1 ? first : normal;
       // Page ids of the next tiles, one box per lane, a batch ahead.
       const int max_pages = own ? p.max_pages : p.prefix_pages;
       const int* table = own ? p.table + static_cast<size_t>(w.e - p.groups) * p.max_pages
@@ -524,7 +528,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tmQ, const CUtens
 #pragma unroll
           for (int c = 0; c < Ly::KCH; ++c)
             tma_load_4d_hint(dst + c * Ly::CHUNK, map, bar(Ly::B_KVFULL + stage), c * 64, w.hkv, k0 & (p.page - 1), pid,
-                             own ? first : normal);
+                             policy);
         }
         used |= 1u << stage;
         if (++stage == Ly::STAGES) {
