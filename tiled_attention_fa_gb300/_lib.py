@@ -47,7 +47,7 @@ _SIGS = {
     "fa_paged_decode_workspace_size": ([_i] * 8, ctypes.c_size_t),
     "fa_paged_decode": ([_vp] * 3 + [_ll, _ll] + [_vp] * 5 + [_ll, _vp, ctypes.c_size_t] + [_i] * 11
                         + [_vp], _i),
-    "fa_rope": ([_vp, _ll, _ll] * 4 + [_vp] * 2 + [_i] * 9 + [_vp], _i),
+    "fa_rope": ([_vp, _ll, _ll] * 4 + [_vp] * 2 + [_i] * 10 + [_vp], _i),
     "fa_paged_append": ([_vp, _ll, _ll] * 4 + [_vp] * 2 + [_ll] * 2 + [_vp] * 5 + [_i, _vp, _ll, _vp] + [_i] * 11
                         + [_vp], _i),
     "fa_paged_prefix_decode_workspace_size": ([_i] * 9, ctypes.c_size_t),
