@@ -120,25 +120,6 @@ inline bool launch_after_smem(void (*kern)(P...), dim3 grid, dim3 block, size_t 
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...) == cudaSuccess;
 }
-// The same in clusters of two along x, of which grid.x is a multiple.
-template <typename... A, typename... P>
-inline bool launch_pairs_after(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                               const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = 2;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...) == cudaSuccess;
-}
 template <typename... A, typename... P>
 inline bool launch_after(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t s, const A&... args) {
   return launch_after_smem(kern, grid, block, 0, s, args...);

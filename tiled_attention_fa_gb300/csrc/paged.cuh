@@ -61,6 +61,17 @@
 
 namespace fa {
 
+// mbar_wait_warp with the wait as a call: these kernels have so many waits that their
+// code, inlined, would not stay in the instruction cache.
+static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, AbortState* ab,
+                                                   unsigned int* err_word, unsigned int site) {
+  return mbar_wait(bar, parity, ab, err_word, site);
+}
+__device__ __forceinline__ bool mbar_wait_warp_call(uint32_t bar, uint32_t parity, AbortState* ab,
+                                                    unsigned int* err_word, unsigned int site) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || __all_sync(0xffffffffu, mbar_wait_slow(bar, parity, ab, err_word, site));
+}
+
 struct PagedBase {
   const int* table;  // [B, max_pages]
   const int* lens;   // [B]

@@ -108,6 +108,12 @@ __device__ __forceinline__ bool prefix_wait(uint32_t bar, uint32_t parity, Abort
   return __all_sync(0xffffffffu, ok);
 }
 
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
 // Arrive n times.
 __device__ __forceinline__ void prefix_arrive(uint32_t bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");

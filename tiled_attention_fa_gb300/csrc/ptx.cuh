@@ -114,17 +114,6 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, Ab
   return __all_sync(0xffffffffu, ok);
 }
 
-// The same as a call: for kernels with so many waits that their code, inlined,
-// would not stay in the instruction cache.
-static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, AbortState* ab,
-                                                   unsigned int* err_word, unsigned int site) {
-  return mbar_wait(bar, parity, ab, err_word, site);
-}
-__device__ __forceinline__ bool mbar_wait_warp_call(uint32_t bar, uint32_t parity, AbortState* ab,
-                                                    unsigned int* err_word, unsigned int site) {
-  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || __all_sync(0xffffffffu, mbar_wait_slow(bar, parity, ab, err_word, site));
-}
-
 // Short bounded wait used only while unwinding (drain in-flight copies).
 __device__ __forceinline__ void mbar_wait_drain(uint32_t bar, uint32_t parity) {
   const unsigned long long t0 = globaltimer_ns();
@@ -164,11 +153,6 @@ __device__ __forceinline__ void tma_load_4d_hint(uint32_t dst, const CUtensorMap
 __device__ __forceinline__ uint64_t policy_evict_last() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
-  return p;
-}
-__device__ __forceinline__ uint64_t policy_evict_normal() {
-  uint64_t p;
-  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
 __device__ __forceinline__ uint64_t policy_evict_first() {
