@@ -214,8 +214,8 @@ fa_status fa_paged_decode(const void* Q, const void* K_pool, const void* V_pool,
  * 2 i and 2 i + 1; the others are copied.  Pair i (x, y) of a token at position n
  * on the pair's axis becomes
  *   (x cos t - y sin t, x sin t + y cos t),   t = n f_i,
- * with angles that are exact to 2^-22 rad at every int32 position, computed in
- * fp32, each result rounded once.  positions [axes, B, L] int32 (1 to 256 axes;
+ * with angles within 2^-23 rad of the entry's turns times n at every int32
+ * position, computed in fp32, each result rounded once.  positions [axes, B, L] int32 (1 to 256 axes;
  * a table's axis beyond the last counts as the last), or NULL with one axis: the
  * token's number 0 .. L - 1.
  *

@@ -11,8 +11,8 @@
 // Angles: the table holds f_i / 2 pi, the turns a position adds, as a 64-bit
 // fixed-point fraction whose low 8 bits are the pair's axis.  The turns of
 // position n are the product of two integers modulo 2^64, exact for every 32-bit
-// position up to the fraction's own 2^-57; its top 32 bits are the angle, to
-// which sincospif answers in 32 bits.  An fp32 product n f_i at n = 100,000 is
+// position (what the entry itself is off by grows with it); its top 32 bits are
+// the angle, to which sincospif answers in 32 bits.  An fp32 product n f_i at n = 100,000 is
 // already off by 2^-8 rad.
 //
 // Bound by the read and the write of the heads.  A thread owns one unit of a
