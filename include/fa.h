@@ -277,9 +277,10 @@ fa_status fa_paged_append(const void* Q, long long q_batch, long long q_token, c
  * Results do not depend on timing.  `workspace`:
  * fa_paged_prefix_decode_workspace_size bytes, asked with the device that runs
  * the call current (FA_ERR_SCRATCH_TOO_SMALL when smaller), under
- * fa_paged_decode's rules; its largest part holds 256 x D floats for every SM and
- * for every K/V head and two tiles of 128 / (H / Hkv) tokens, a group's tiles
- * counted apart.  FA_ERR_UNSUPPORTED where three times (D = 64: four times) the
+ * fa_paged_decode's rules; it holds D + 1 floats for twice every query row
+ * (B * Lq * H) and for 256 + (H / Hkv) * Lq rows of every SM, and 8 bytes for every
+ * group, sequence and pair of tiles of 128 / (H / Hkv) tokens and K/V head.
+ * FA_ERR_UNSUPPORTED where three times (D = 64: four times) the
  * 128-key tiles of all prefixes (at their tables' lengths, for each K/V head and
  * two tiles of tokens) and twice those of all own keys could add up to 2^32 or
  * more.

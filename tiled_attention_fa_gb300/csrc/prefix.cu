@@ -55,11 +55,13 @@ PrefixPlan prefix_plan_of(const PrefixDecodeArgs& a) {
   // (in pairs: prefixes and own keys may have CTAs of their own)
   w.G = prefix_units + own_units < sms ? static_cast<int>(prefix_units + own_units) : sms;
   w.G = w.G < 2 ? 2 : (w.G + 1) / 2 * 2;
+  // Prefix partials: every query row once, and an item's 256 for every part.
+  const size_t rows = static_cast<size_t>(tokens) * a.H + 256 * static_cast<size_t>(w.G);
   size_t at = 0;
   w.part_o = at;
-  at += static_cast<size_t>(w.items + w.G) * 256 * a.D * sizeof(float);
+  at += align256(rows * a.D * sizeof(float));
   w.part_lse = at;
-  at += static_cast<size_t>(w.items + w.G) * 256 * sizeof(float);
+  at += align256(rows * sizeof(float));
   w.own_o = at;
   at += align256(static_cast<size_t>(w.own + w.G) * w.rows * a.D * sizeof(float));
   w.own_lse = at;

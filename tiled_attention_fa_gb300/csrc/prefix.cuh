@@ -24,9 +24,10 @@
 // How many CTAs are of each kind follows on the device from the lengths: the first
 // are bound by the products, the others by the read, so the two overlap on the
 // chip and one launch's start serves both.  A part's share of an item is a chunk.
-// Chunks are stored at item + part, which no two share: the next chunk in a list is
-// of a later item, a later part, or both; the join finds an item's first and last
-// part in a table.
+// Own keys' chunks are stored at item + part, which no two share: the next chunk in a
+// list is of a later item, a later part, or both.  Prefixes' are stored at the rows
+// before the item + 256 part (an item has 256 rows at most), for the same reason.
+// The join finds an item's first and last part in a table.
 //
 // prefix_body:
 //   warps 0-3, 4-7  softmax, a thread per row.  Two tiles: one each.  One tile:
@@ -65,8 +66,8 @@ struct PrefixParams {
   const int *ptable, *plens;  // [groups, prefix_pages], [groups]
   const int* starts;          // [groups + 1] first sequence of each group, or NULL: one group of all
   const int *table, *lens;    // [B, max_pages], [B]: own keys
-  float* part_o;              // [prefix items + G][2][D / 4][128][4]: a warp's rows lie together
-  float* part_lse;            // [prefix items + G][2][128], log2 units
+  float* part_o;              // prefix partials: a tile's [D / 4][its rows][4], so that a warp's rows lie together
+  float* part_lse;            // a row's, log2 units; where a chunk's rows begin: prefix_first_row
   float* own_o;               // [B * Hkv + G][rows][D]
   float* own_lse;             // [B * Hkv + G][rows], log2 units
   int* ends;                  // [prefix items][2], then [B * Hkv][2]: an item's first and last part
@@ -170,6 +171,13 @@ __device__ __forceinline__ PrefixEntry prefix_entry(const PrefixParams& p, int e
 // (a group of n tokens has at most n / (2 tok) + 1 items a K/V head).
 __device__ __forceinline__ int prefix_first_item(const PrefixParams& p, const PrefixEntry& s, int grp) {
   return (s.t0 / (2 * p.tok) + grp) * p.Hkv;
+}
+
+// Where the rows of a group's item's chunk in a part begin, among all partials: as
+// many as the items before it have, whatever the groups' sizes, and the parts' 256.
+// (B * Lq * H is below 2^31.)
+__device__ __forceinline__ uint32_t prefix_first_row(const PrefixParams& p, const PrefixEntry& s, int hkv, int it, int part) {
+  return static_cast<uint32_t>((s.t0 * p.Hkv + (s.t1 - s.t0) * hkv + 2 * p.tok * it) * p.g) + 256u * part;
 }
 
 // Walk over the chunks of one part.  OWN: own keys are in the list too.
@@ -783,14 +791,15 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tmQ, const CUtens
         // moved (the commit behind this S covers the tile's, or group's, last PV).
         auto p_ready = [&](int h) {
           if (h == 0 && rescale) {
+            // (16 at a time, in a loop: beside 128 scores more registers would be spilled)
+#pragma unroll 1
+            for (int cc = 0; cc < D / 16; ++cc) {
+              uint32_t o[16];
+              tmem_ld16(tO + D * t + 16 * cc, o);
+              tmem_ld_wait16(o);
 #pragma unroll
-            for (int cc = 0; cc < D / 32; ++cc) {
-              uint32_t o[32];
-              tmem_ld32(tO + D * t + 32 * cc, o);
-              tmem_ld_wait32(o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st32(tO + D * t + 32 * cc, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st16(tO + D * t + 16 * cc, o);
             }
           }
           tmem_st_wait();
@@ -863,16 +872,18 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tmQ, const CUtens
       }
       const int item = own ? (w.e - p.groups) * p.Hkv + w.hkv
                            : prefix_first_item(p, w.s, w.e) + w.hkv * w.s.items + w.it;
-      const size_t at = static_cast<size_t>(item) + part;
       if (some) {
         tc_fence_after();
         const float inv = l > 0.f ? 1.f / l : 0.f;
         f0 *= inv;
         f1 *= inv;
-        const size_t tile = 2 * at + (pair ? t : 0);
-        float4* dst = own ? reinterpret_cast<float4*>(p.own_o) + (at * p.rows + r) * (D / 4)
-                          : reinterpret_cast<float4*>(p.part_o) + tile * (D / 4) * 128 + r;
-        const int pitch = own ? 1 : 128;
+        const uint32_t row0 = own ? static_cast<uint32_t>(item + part) * p.rows
+                                : prefix_first_row(p, w.s, w.hkv, w.it, part) + (pair && t ? p.tok * p.g : 0);
+        const float lse = l == 0.f ? -INFINITY : m * sl2 + __log2f(l);  // (NaN stays NaN)
+        if (live) (own ? p.own_lse : p.part_lse)[row0 + r] = lse;
+        float4* dst = reinterpret_cast<float4*>(own ? p.own_o : p.part_o) + static_cast<size_t>(own ? row0 + r : row0) * (D / 4) +
+                      (own ? 0 : r);
+        const int pitch = own ? 1 : w.rows(p, pair ? t : 0);
 #pragma unroll 1
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t o[32];
@@ -889,12 +900,10 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tmQ, const CUtens
           }
           if (live) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[(8 * cc + i) * pitch] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            for (int i = 0; i < 8; ++i, dst += pitch)
+              *dst = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         }
-        const float lse = l == 0.f ? -INFINITY : m * sl2 + __log2f(l);  // (NaN stays NaN)
-        if (live) (own ? p.own_lse + at * p.rows : p.part_lse + tile * 128)[r] = lse;
         tc_fence_before();
       }
       // The item's first and last part, for the join.
@@ -1059,15 +1068,17 @@ __global__ void __launch_bounds__(128) fa_prefix_join_kernel(const PrefixJoinPar
   };
   if (!pad && in) {
     // The chunks of the row's tile.
-    int n = 0, slot = 0, row = 0;
+    int n = 0, row = 0, pitch = 0;
+    uint32_t row0 = 0;
     if (s.items > 0 && tk >= s.t0 && tk < s.t1) {
       const int tile = (tk - s.t0) / p.tok;
       row = (tk - s.t0 - tile * p.tok) * p.g + hg;
+      pitch = min(p.tok, s.t1 - s.t0 - tile * p.tok) * p.g;
       const int item = prefix_first_item(p, s, grp) + hkv * s.items + (tile >> 1);
       const int2 e = __ldcg(reinterpret_cast<const int2*>(p.ends) + item);
       const int c0 = min(max(e.x, 0), a.G - 1);  // (in bounds even where starts fall)
       n = min(max(e.y, c0), a.G - 1) - c0 + 1;
-      slot = 2 * (item + c0) + (tile & 1);
+      row0 = prefix_first_row(p, s, hkv, tile >> 1, c0) + (tile & 1 ? p.tok * p.g : 0);
     }
     // The own keys' first partial, nearly always the only one, beside them.
     const int o0 = min(max(oe.x, 0), a.G - 1), o1 = min(max(oe.y, o0), a.G - 1);
@@ -1075,8 +1086,8 @@ __global__ void __launch_bounds__(128) fa_prefix_join_kernel(const PrefixJoinPar
     const float4* own_o = reinterpret_cast<const float4*>(p.own_o) + d4;
     const float ol = __ldcg(p.own_lse + own_at);
     const float4 oo = __ldcg(own_o + own_at * (D / 4));
-    const float* lses = p.part_lse + static_cast<size_t>(slot) * 128 + row;
-    const float4* os = reinterpret_cast<const float4*>(p.part_o) + (static_cast<size_t>(slot) * (D / 4) + d4) * 128 + row;
+    const float* lses = p.part_lse + row0 + row;
+    const float4* os = reinterpret_cast<const float4*>(p.part_o) + static_cast<size_t>(row0) * (D / 4) + d4 * pitch + row;
 #pragma unroll 1
     for (int q0 = sp; q0 < n; q0 += SP * C) {
       float ls[C];
@@ -1088,7 +1099,7 @@ __global__ void __launch_bounds__(128) fa_prefix_join_kernel(const PrefixJoinPar
         o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (q < n) {
           ls[c] = __ldcg(lses + static_cast<size_t>(q) * 256);
-          o[c] = __ldcg(os + static_cast<size_t>(q) * (2 * (D / 4) * 128));
+          o[c] = __ldcg(os + static_cast<size_t>(q) * (256 * (D / 4)));
         }
       }
 #pragma unroll
