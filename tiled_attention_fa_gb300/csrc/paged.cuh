@@ -44,12 +44,12 @@
 // and the warp that issues the PV products sets their V rows in shared memory to
 // zero before the first.
 // The roles' code together has to stay in the instruction cache: loops stay loops,
-// the waits are calls and each TMA load stands once.  (At 112 KB instead of 80 KB,
-// 256 sequences of 64 to 512 keys took 88 us, now 70.)
+// the waits are calls.  (At 112 KB instead of 80 KB, 256 sequences of 64 to 512 keys
+// took 90 us, now 72.)
 // Measured (bf16, H32/8 D128): B16 16,384 keys 168 us, 6.4 TB/s (94% of the copy
-// rate; pages of 16 keys 175 us); B64 1,024 keys 47 us; B1 131,072 keys 90 us;
+// rate; pages of 16 keys 169 us); B64 1,024 keys 49 us; B1 131,072 keys 91 us;
 // B1 500 keys 10.0 us, where launch, page ids, one tile and the join follow one
-// another; four tokens each of B8, window 4,096: 33 us (21 for the bytes alone).
+// another; four tokens each of B8, window 4,096: 34 us (21 for the bytes alone).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -486,7 +486,7 @@ __device__ __forceinline__ void paged_body(const CUtensorMap& tmQ, const CUtenso
   if (warp == Ly::SW) {
     // ------------------------------------------------------------ producer
     // Ring order: the first NG K tiles, then K_{i+NG}, V_i.  Lane j loads the j-th box
-    // (a page, or 128 rows of one) of the tile.
+    // (a page, or 128 rows of one; behind a prefix at most 64) of the tile.
     const int page_log = 31 - __clz(p.page);  // (a page is a power of two)
     const int box_log = min(page_log, OWN ? kOwnBoxLog : 7), box = 1 << box_log, nbox = 128 >> box_log;
     const int per_batch = 32 >> (7 - box_log);
@@ -580,12 +580,19 @@ __device__ __forceinline__ void paged_body(const CUtensorMap& tmQ, const CUtenso
       if (lane == 0)
         mbar_arrive_expect_tx(bar(Ly::B_KVFULL + stage), boxes * box * static_cast<uint32_t>(D) * 2u);
       __syncwarp();
+      // (The two loads apart: with one whose tensor map is chosen at run time, 16 sequences
+      // of 16,384 keys in pages of 16 took 175.6 us instead of 169.)
       if (row >= 0) {
-        const CUtensorMap* map = is_k ? &tmK : &tmV;
+        const uint32_t dst = base + Ly::RING_OFF + stage * Ly::TILE + lane * box * 128u;
+        if (is_k) {
 #pragma unroll
-        for (int c = 0; c < Ly::KCH; ++c)
-          tma_load_4d_hint(base + Ly::RING_OFF + stage * Ly::TILE + c * Ly::CHUNK + lane * box * 128u, map,
-                           bar(Ly::B_KVFULL + stage), c * 64, head, row, page, stream);
+          for (int c = 0; c < Ly::KCH; ++c)
+            tma_load_4d_hint(dst + c * Ly::CHUNK, &tmK, bar(Ly::B_KVFULL + stage), c * 64, head, row, page, stream);
+        } else {
+#pragma unroll
+          for (int c = 0; c < Ly::KCH; ++c)
+            tma_load_4d_hint(dst + c * Ly::CHUNK, &tmV, bar(Ly::B_KVFULL + stage), c * 64, head, row, page, stream);
+        }
       }
       used |= 1u << stage;
       if (++stage == Ly::STAGES) {
