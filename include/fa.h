@@ -258,7 +258,8 @@ fa_status fa_paged_append(const void* Q, long long q_batch, long long q_token, c
 
 /*
  * fa_paged_prefix_decode: fa_paged_decode (no window, no weights) for sequences
- * that share key/value prefixes, each prefix read once for all of them.  Group i
+ * that share key/value prefixes, each prefix read once for every two tiles of
+ * 128 / (H / Hkv) tokens of its sequences, not once a sequence.  Group i
  * is the sequences group_starts[i] .. group_starts[i + 1] - 1 (group_starts
  * [groups + 1] int32, never falling; NULL with one group: all of them); its
  * prefix is the first prefix_lens[i] keys of the pages in row i of prefix_table
@@ -273,6 +274,8 @@ fa_status fa_paged_append(const void* Q, long long q_batch, long long q_token, c
  * (starts that fall anywhere give unspecified results).  Slots behind a length
  * are never used, whatever they hold; V must be finite at a key that some query
  * of the call sees, and NaN in a query or in a key it sees gives that row NaN.
+ * As in all calls on 16-bit inputs, probabilities are rounded to their type before
+ * the product with V (half a step, relative), sums take them unrounded.
  * (H / Hkv) * Lq <= 128 (FA_ERR_UNSUPPORTED otherwise).
  * Results do not depend on timing.  `workspace`:
  * fa_paged_prefix_decode_workspace_size bytes, asked with the device that runs

@@ -78,7 +78,8 @@ def paged_prefix_decode_workspace_size(B: int, Lq: int, H: int, Hkv: int, D: int
 def paged_prefix_decode(q, k_cache, v_cache, prefix_table, prefix_lens, block_table, lens, group_starts=None,
                         out=None, lse=None, workspace=None, stream=None):
     """``paged_decode`` for sequences that share key/value prefixes, each
-    prefix read once for all of them.  O, LSE of the last Lq tokens of every
+    prefix read once for every two tiles of 128 / (H / Hkv) tokens of its
+    sequences, not once a sequence.  O, LSE of the last Lq tokens of every
     sequence, q [B, Lq, H, D].  Group i is the sequences group_starts[i] up to
     group_starts[i + 1] (int32 [G + 1], never falling; None with one group: all
     of them), its prefix the first prefix_lens[i] keys in the pages of

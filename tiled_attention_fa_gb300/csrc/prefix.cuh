@@ -5,7 +5,7 @@
 // each: LSE = ln sum_s exp(LSE_s), O = sum_s exp(LSE_s - LSE) O_s.  Every new
 // token behind a prefix sees all of it, so the prefix's part is one product
 // chain of all rows (tokens x query heads of a K/V head) with the prefix's keys
-// and values, which are read once, not once per sequence.
+// and values, which are read once for 256 rows, not once per sequence.
 //
 // Two launches: fa_prefix_kernel cuts both parts into chunks and leaves each
 // chunk's partial O and LSE in fp32; fa_prefix_join_kernel joins each row's.
@@ -45,11 +45,14 @@
 // way, as in the dense forward); a CTA's share of the memory bandwidth brings 64 KB
 // in 2,790.  A launch's first 5 us go until the first scores are there (2 to the plan:
 // code, lengths; then page ids, the first tiles), its last 5 to the join.
-// Measured (H32/8 D128): 64 sequences of 100 to 1,000 own keys behind 32,768: 60 us
+// P goes to its product in the inputs' 16-bit type, like all of this library's: the
+// outputs' distance from 64 bits is 1.3 to 1.4 times that of one rounding at the end.
+// Measured (H32/8 D128): 64 sequences of 100 to 1,000 own keys behind 32,768: 59.5 us
 // (the paged decode over tables that repeat the prefix reads it 64 times from the L2);
-// 256 of 64 to 512 behind 16,384: 97 us; 20 of four tokens, 50 to 800 behind 6,001: 32
-// us; 8 of 1 to 100 behind 2,001: 15 us.  H16/16 D64: 40 of 16 to 500 in five groups
-// behind 1,000 to 9,000: 39 us.
+// 256 of 64 to 512 behind 16,384: 95.6 us, with pages of 16 137; 20 of four tokens, 50
+// to 800 behind 6,001: 31 us, of 8 tokens (32 rows) 46, of 16 (64 rows) 58; 8 of 1 to
+// 100 behind 2,001: 14 us.  H16/16 D64: 40 of 16 to 500 in five groups behind 1,000 to
+// 9,000: 36.5 us.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -126,6 +129,8 @@ __device__ __forceinline__ void prefix_arrive(uint32_t bar, uint32_t n) {
 // keys 1.5 (256 sequences behind 16,384 keys 98 us, behind 32,768 65; with 1.3 103 and
 // 68, with 1.75 106 and 67).  At D = 64 one tile takes 1,300 cycles, two 2,700, an own
 // tile and an item 1,300 to 1,400 each (five groups 39 us; with 3, 2 and 1.5 43).
+// Swept with 1 to 4 rows a sequence; tiles of more rows, which take longer, weigh the
+// same (of 16: the own keys' CTAs end a quarter later than the others).
 constexpr int kOneWeight = 2;
 constexpr int prefix_pair_weight(int D) { return D == 64 ? 4 : 3; }
 constexpr float prefix_own_weight(int D) { return D == 64 ? 2.f : 1.5f; }
